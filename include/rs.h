@@ -285,6 +285,103 @@ rs_status rs_sort_morton30(const float *xyz, size_t n, const float *box_lo, cons
 rs_status rs_sort_keys_u32_noalloc(const uint32_t *keys_in, uint32_t *keys_out, size_t n,
                                    int begin_bit, int end_bit, hipStream_t stream);
 
+/* Mixture-of-experts calls: the routing of tokens, the sort of their slots by
+ * expert, and token rows carried to their sorted places and back.
+ *
+ * T tokens choose k of E experts each; slot s = t * k + j is choice j of token
+ * t, and n = T * k.  All arrays are DEVICE memory, aligned to their element.
+ * Logits and rows are float32, float16 or bfloat16 (rs_dtype; one type per
+ * call), row-major with consecutive elements and a stride between rows, in
+ * elements; an output's stride is at least its width, an input's is free.
+ * Weights, chosen experts, places and offsets are contiguous.  Sums and gates
+ * are computed in float32 and rounded once, to nearest even, where the result
+ * is 16 bits wide; every sum has a fixed order, so results repeat bit for bit.
+ * Outputs may not overlap an input or another output.  The calls allocate
+ * nothing, only enqueue on `stream` (of the current device), keep no state
+ * and can be captured into a graph.  Argument errors are reported before any
+ * HIP call, as for the sorts: RS_ERROR_INVALID_VALUE for a NULL or misaligned
+ * pointer, a size outside the stated limits, an unknown type or gate, or an
+ * overlap. */
+typedef enum rs_dtype { RS_F32 = 0, RS_F16 = 1, RS_BF16 = 2 } rs_dtype;
+typedef enum rs_gate { RS_GATE_SOFTMAX = 0, RS_GATE_SIGMOID = 1 } rs_gate;
+#define RS_MAX_EXPERTS 1024          /* E */
+#define RS_MAX_CHOICES 64            /* k */
+#define RS_MAX_ROW_WIDTH (1 << 20)   /* elements of a row */
+#define RS_MAX_SLOTS ((size_t)0x7FFFFFFFu)
+
+/* The k largest of each row of logits [tokens][experts], descending, ties to
+ * the lowest index: experts_out[t][j], and their gate values
+ *   softmax: p_i = exp(l_i) / sum over the row of exp(l)
+ *   sigmoid: p_i = 1 / (1 + exp(-l_i))
+ * as weights_out[t][j] = scale * p, or scale * p / (sum of the chosen p) if
+ * renormalize != 0.  -0 equals +0; a NaN ranks above every number.  A logit of
+ * -inf marks an expert that the row may not use: it is never chosen, and slots
+ * left over get expert -1 and weight 0 (a row of -inf: all of them).  NaN and
+ * +inf give what the formulas give.  1 <= k <= min(experts, RS_MAX_CHOICES). */
+rs_status rs_route_topk(const void *logits, int dtype, size_t tokens, int experts, size_t stride, int k, int gate,
+                        int renormalize, float scale, float *weights_out, int32_t *experts_out, hipStream_t stream);
+
+/* The gradient of the logits from that of the weights, for the experts that
+ * rs_route_topk chose; every element of the rows is written.  Slots whose
+ * expert is outside [0, experts) or has a logit of -inf add nothing, whatever
+ * their gradient holds; an expert named by several slots gets the sum. */
+rs_status rs_route_topk_backward(const void *logits, int dtype, size_t tokens, int experts, size_t stride,
+                                 const int32_t *chosen, const float *grad_weights, int k, int gate, int renormalize,
+                                 float scale, void *grad_logits, size_t grad_stride, hipStream_t stream);
+
+/* Slots sorted stably by expert.  ids: n expert numbers; those in
+ * [first, first + experts) are counted, all others (-1, another rank's) are
+ * dropped and sort last.  order_out[p] = the slot at place p;
+ * position_out[s] = the place of slot s, stored as ~place where it is dropped;
+ * offsets_out[e], e = 0 .. experts: the slots of experts below first + e, so
+ * expert e holds the places [offsets[e], offsets[e + 1]) and the dropped slots
+ * the rest.  n <= RS_MAX_SLOTS (0: only the offsets are written); first >= 0,
+ * first + experts <= 2^31.  temp: 256-byte aligned, rs_temp_bytes_experts(n,
+ * experts) bytes, nothing in it is kept or expected; NULL where that is 0. */
+size_t rs_temp_bytes_experts(size_t n, int experts);
+rs_status rs_sort_experts_i32(const int32_t *ids, size_t n, int first, int experts, int32_t *order_out,
+                              int32_t *position_out, int32_t *offsets_out, void *temp, size_t temp_bytes,
+                              hipStream_t stream);
+rs_status rs_sort_experts_i64(const int64_t *ids, size_t n, int first, int experts, int32_t *order_out,
+                              int32_t *position_out, int32_t *offsets_out, void *temp, size_t temp_bytes,
+                              hipStream_t stream);
+
+/* Rows to their sorted places: rows[place of (t, j)] = w[t][j] * x[t]
+ * (weights NULL: x[t]), and zeros for a dropped slot, so the places of
+ * rs_sort_experts fill every row.  position: as rs_sort_experts writes it; a
+ * place at or beyond num_rows is skipped, a row that no slot names is left as
+ * it was, and one that several name holds one of theirs.  1 <= k <=
+ * RS_MAX_CHOICES, 1 <= width <= RS_MAX_ROW_WIDTH, num_rows <= RS_MAX_SLOTS. */
+rs_status rs_dispatch_rows(const void *x, int dtype, size_t tokens, int width, size_t x_stride,
+                           const int32_t *position, const float *weights, int k, void *rows, size_t num_rows,
+                           size_t rows_stride, hipStream_t stream);
+
+/* Its gradients: grad_x[t] = sum over j of w[t][j] * grad_rows[place of (t, j)]
+ * and, if grad_weights is given, grad_weights[t][j] = <x[t], grad_rows[place]>
+ * (x may be NULL otherwise).  Dropped slots and skipped places add nothing and
+ * have gradient 0; their rows are not read. */
+rs_status rs_dispatch_rows_backward(const void *grad_rows, int dtype, size_t num_rows, size_t grad_rows_stride,
+                                    const int32_t *position, const float *weights, int k, const void *x,
+                                    size_t x_stride, void *grad_x, size_t grad_x_stride, float *grad_weights,
+                                    size_t tokens, int width, hipStream_t stream);
+
+/* Rows back to their tokens: out[t] = sum over j of w[t][j] * rows[place of
+ * (t, j)] (weights NULL: their sum), added in the order of j.  Dropped slots
+ * and skipped places add nothing: their rows are not read, and a token
+ * without any other slot gets zeros.  Limits as for rs_dispatch_rows. */
+rs_status rs_combine_rows(const void *rows, int dtype, size_t num_rows, size_t rows_stride, const int32_t *position,
+                          const float *weights, int k, void *out, size_t tokens, int width, size_t out_stride,
+                          hipStream_t stream);
+
+/* Its gradients: grad_rows[place of (t, j)] = w[t][j] * grad_out[t], zeros for
+ * a dropped slot (every row of rs_sort_experts's places is written), and, if
+ * grad_weights is given, grad_weights[t][j] = <grad_out[t], rows[place]>, 0 for
+ * a dropped slot (rows may be NULL otherwise). */
+rs_status rs_combine_rows_backward(const void *grad_out, int dtype, size_t tokens, int width, size_t grad_out_stride,
+                                   const int32_t *position, const float *weights, int k, const void *rows,
+                                   size_t rows_stride, void *grad_rows, size_t grad_rows_stride, size_t num_rows,
+                                   float *grad_weights, hipStream_t stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char *rs_status_string(rs_status status);
 

@@ -30,7 +30,10 @@ typedef enum rs_kernel_kind {
     RS_KERNEL_PASS = 3,   /* one digit pass: rank + chained scan + scatter */
     RS_KERNEL_COPY = 4,   /* plain copies (trivial calls, odd in-place passes) */
     RS_KERNEL_SMALL = 5,  /* a whole sort of a small input in one launch */
-    RS_KERNEL_KINDS = 6
+    RS_KERNEL_ROUTE = 6,  /* top-k routing and its gradient */
+    RS_KERNEL_EXPERT = 7, /* slots sorted by expert (counting and placing launches) */
+    RS_KERNEL_ROWS = 8,   /* rows dispatched or combined, and their gradients */
+    RS_KERNEL_KINDS = 9
 } rs_kernel_kind;
 
 /* Turn per-kernel event timing on (non-zero) or off: while on, every kernel

@@ -24,12 +24,16 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib
+from .experts import (MAX_CHOICES, MAX_EXPERTS, ExpertOrder, combine_rows, combine_rows_backward, dispatch_rows,
+                      dispatch_rows_backward, route_topk, route_topk_backward, sort_experts, temp_bytes_experts)
 
 __all__ = [
     "RadixSortError", "key_bits", "temp_bytes", "temp_bytes_morton30", "sort_morton30", "alloc_temp", "sort_keys", "sort_pairs",
     "copy_u32", "prof_enable", "prof_reset", "prof_summary", "prof_small_path", "library_path",
     "error_word", "skipped_passes", "order_flag", "prof_tile_items", "sort_keys_u32_noalloc",
     "NOALLOC_MAX_KEYS", "DeviceGuardError", "prof_samples", "prof_force_giveup", "lds_rank_probe", "prof_ranker",
+    "MAX_CHOICES", "MAX_EXPERTS", "ExpertOrder", "route_topk", "route_topk_backward", "temp_bytes_experts",
+    "sort_experts", "dispatch_rows", "dispatch_rows_backward", "combine_rows", "combine_rows_backward",
 ]
 
 TEMP_ALIGN = 256

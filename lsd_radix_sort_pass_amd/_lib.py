@@ -20,12 +20,16 @@ RS_KERNEL_SCAN = 2
 RS_KERNEL_PASS = 3
 RS_KERNEL_COPY = 4
 RS_KERNEL_SMALL = 5
-RS_KERNEL_KINDS = 6
+RS_KERNEL_ROUTE = 6
+RS_KERNEL_EXPERT = 7
+RS_KERNEL_ROWS = 8
+RS_KERNEL_KINDS = 9
 
 # Every function the two public headers declare, with its ctypes signature.
 _VP = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _I = ctypes.c_int
+_F = ctypes.c_float
 _FP = ctypes.POINTER(ctypes.c_float)
 SIGNATURES = {
     "rs_temp_bytes": (_SZ, [_SZ, _I, _I, _I]),
@@ -61,6 +65,15 @@ SIGNATURES = {
     "rs_temp_bytes_morton30": (_SZ, [_SZ]),
     "rs_sort_morton30": (_I, [_VP, _SZ, _FP, _FP, _VP, _VP, _VP, _SZ, _VP]),
     "rs_sort_keys_u32_noalloc": (_I, [_VP, _VP, _SZ, _I, _I, _VP]),
+    "rs_route_topk": (_I, [_VP, _I, _SZ, _I, _SZ, _I, _I, _I, _F, _VP, _VP, _VP]),
+    "rs_route_topk_backward": (_I, [_VP, _I, _SZ, _I, _SZ, _VP, _VP, _I, _I, _I, _F, _VP, _SZ, _VP]),
+    "rs_temp_bytes_experts": (_SZ, [_SZ, _I]),
+    "rs_sort_experts_i32": (_I, [_VP, _SZ, _I, _I, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "rs_sort_experts_i64": (_I, [_VP, _SZ, _I, _I, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "rs_dispatch_rows": (_I, [_VP, _I, _SZ, _I, _SZ, _VP, _VP, _I, _VP, _SZ, _SZ, _VP]),
+    "rs_dispatch_rows_backward": (_I, [_VP, _I, _SZ, _SZ, _VP, _VP, _I, _VP, _SZ, _VP, _SZ, _VP, _SZ, _I, _VP]),
+    "rs_combine_rows": (_I, [_VP, _I, _SZ, _SZ, _VP, _VP, _I, _VP, _SZ, _I, _SZ, _VP]),
+    "rs_combine_rows_backward": (_I, [_VP, _I, _SZ, _I, _SZ, _VP, _VP, _I, _VP, _SZ, _VP, _SZ, _SZ, _VP, _VP]),
     "rs_status_string": (ctypes.c_char_p, [_I]),
     "rs_prof_enable": (_I, [_I]),
     "rs_prof_reset": (None, []),

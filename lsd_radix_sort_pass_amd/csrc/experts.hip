@@ -1,0 +1,403 @@
+// experts.hip -- C ABI of the mixture-of-experts calls (routing, slots sorted
+// by expert, rows dispatched and combined): argument checks and launches.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "experts.hpp"
+#include "launch.hpp"
+#include "rs.h"
+#include "rs_prof.h"
+
+namespace {
+
+using namespace rs_host;
+
+constexpr unsigned kMaxGrid = 1u << 20;  // workgroups; the kernels stride over the rest
+constexpr size_t kTempAlign = 256;
+
+int dtype_bytes(int dtype) {
+    switch (dtype) {
+        case RS_F32: return 4;
+        case RS_F16:
+        case RS_BF16: return 2;
+        default: return 0;
+    }
+}
+
+bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// Bytes that `count` rows of `width` elements span.
+size_t span_bytes(size_t count, size_t width, size_t stride, size_t elem) {
+    return count == 0 ? 0 : ((count - 1) * stride + width) * elem;
+}
+
+// A present, aligned array; or any pointer for an empty one.
+bool good(const void *p, size_t count, size_t align) { return count == 0 || (p != nullptr && aligned(p, align)); }
+
+constexpr size_t kMaxStride = size_t{1} << 40;
+
+// Whether the rows of an array are addressable and, for an output, disjoint.
+bool good_rows(const void *p, size_t count, int width, size_t stride, size_t elem, bool output) {
+    if (!good(p, count, elem)) return false;
+    if (count <= 1) return true;
+    return stride <= kMaxStride && (!output || stride >= static_cast<size_t>(width));
+}
+
+bool disjoint(const Span *spans, int outputs, int all) {
+    for (int o = 0; o < outputs; ++o) {
+        for (int i = o + 1; i < all; ++i) {
+            if (spans[o].lo != spans[o].hi && spans[i].lo != spans[i].hi && overlap(spans[o], spans[i])) return false;
+        }
+    }
+    return true;
+}
+
+// ---------------------------------------------------------------------------
+// Routing
+// ---------------------------------------------------------------------------
+// Calls f(T{}, integral_constant G, integral_constant V) for a row of
+// `experts` logits held by G lanes, V each.
+template <class T, int G, class F>
+bool with_values(int per_lane, F &&f) {
+    if (per_lane <= 1) return f(T{}, std::integral_constant<int, G>{}, std::integral_constant<int, 1>{});
+    if (per_lane <= 2) return f(T{}, std::integral_constant<int, G>{}, std::integral_constant<int, 2>{});
+    if (per_lane <= 4) return f(T{}, std::integral_constant<int, G>{}, std::integral_constant<int, 4>{});
+    if (per_lane <= 8) return f(T{}, std::integral_constant<int, G>{}, std::integral_constant<int, 8>{});
+    return f(T{}, std::integral_constant<int, G>{}, std::integral_constant<int, 16>{});
+}
+
+template <class T, class F>
+bool with_group(int experts, int k, F &&f) {
+    if (k <= 16 && experts <= 256) return with_values<T, 16>((experts + 15) / 16, f);
+    return with_values<T, 64>((experts + 63) / 64, f);
+}
+
+template <class F>
+bool with_dtype(int dtype, F &&f) {
+    switch (dtype) {
+        case RS_F32: return f(float{});
+        case RS_F16: return f(rs::f16{});
+        default: return f(rs::bf16{});
+    }
+}
+
+bool good_route(int dtype, size_t tokens, int experts, int k, int gate) {
+    return dtype_bytes(dtype) != 0 && experts >= 1 && experts <= RS_MAX_EXPERTS && k >= 1 && k <= experts &&
+           k <= RS_MAX_CHOICES && (gate == RS_GATE_SOFTMAX || gate == RS_GATE_SIGMOID) &&
+           tokens <= RS_MAX_SLOTS / static_cast<size_t>(k);
+}
+
+// ---------------------------------------------------------------------------
+// Slots sorted by expert
+// ---------------------------------------------------------------------------
+// Up to kOneGroup slots one workgroup places them all.  Above, the slots are
+// cut into at most kMaxChunks chunks of whole tiles, counted by one launch and
+// placed by a second.
+constexpr size_t kOneGroup = 8 * rs::kPlaceBlock;
+constexpr int kTileItems = 8;
+constexpr size_t kTile = size_t{kTileItems} * rs::kPlaceBlock;
+constexpr size_t kMaxChunks = 256;
+
+struct ExpertPlan {
+    size_t chunk = 0;
+    unsigned chunks = 1;
+};
+
+ExpertPlan expert_plan(size_t n) {
+    ExpertPlan p;
+    const size_t tiles = (n + kTile - 1) / kTile;
+    const size_t per_chunk = (tiles + kMaxChunks - 1) / kMaxChunks;
+    p.chunk = (per_chunk ? per_chunk : 1) * kTile;
+    p.chunks = static_cast<unsigned>(n ? (n + p.chunk - 1) / p.chunk : 1);
+    return p;
+}
+
+size_t expert_temp(size_t n, int experts) {
+    if (n <= kOneGroup) return 0;
+    const size_t bytes = size_t{expert_plan(n).chunks} * (static_cast<size_t>(experts) + 1) * 4;
+    return (bytes + kTempAlign - 1) / kTempAlign * kTempAlign;
+}
+
+bool good_experts(size_t n, int experts) {
+    return experts >= 1 && experts <= RS_MAX_EXPERTS && n <= RS_MAX_SLOTS;
+}
+
+template <class ID>
+rs_status sort_experts(const ID *ids, size_t n, int first, int experts, int32_t *order, int32_t *position,
+                       int32_t *offsets, void *temp, size_t temp_bytes, hipStream_t stream) {
+    if (!good_experts(n, experts) || first < 0 || first > INT32_MAX - experts + 1) return RS_ERROR_INVALID_VALUE;
+    if (!good(ids, n, sizeof(ID)) || !good(order, n, 4) || !good(position, n, 4) || !good(offsets, 1, 4)) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    const size_t need = expert_temp(n, experts);
+    if (need != 0) {
+        if (!temp || !aligned(temp, kTempAlign)) return RS_ERROR_INVALID_VALUE;
+        if (temp_bytes < need) return RS_ERROR_INSUFFICIENT_TEMP;
+    }
+    const Span spans[] = {span_of(order, n * 4), span_of(position, n * 4),
+                          span_of(offsets, 4 * (static_cast<size_t>(experts) + 1)), span_of(temp, need),
+                          span_of(ids, n * sizeof(ID))};
+    if (!disjoint(spans, 4, 5)) return RS_ERROR_INVALID_VALUE;
+
+    int key_bits = 1;
+    while ((1 << key_bits) <= experts) ++key_bits;  // keys 0 .. experts
+    const auto e = static_cast<uint32_t>(experts);
+    const auto f = static_cast<ID>(first);
+    auto *table = static_cast<uint32_t *>(temp);
+    bool ok;
+    if (n <= kOneGroup) {
+        ok = launch_kernel(RS_KERNEL_EXPERT, stream, [&] {
+            const uint32_t *none = nullptr;
+            if (n <= rs::kPlaceBlock) {
+                run_kernel(rs::expert_place_kernel<ID, 1, false>, 1, rs::kPlaceBlock, stream, ids, n, f, e, key_bits, n,
+                           none, order, position, offsets);
+            } else {
+                run_kernel(rs::expert_place_kernel<ID, 8, false>, 1, rs::kPlaceBlock, stream, ids, n, f, e, key_bits, n,
+                           none, order, position, offsets);
+            }
+        });
+    } else {
+        const ExpertPlan p = expert_plan(n);
+        ok = launch_kernel(RS_KERNEL_EXPERT, stream, [&] {
+            run_kernel(rs::expert_count_kernel<ID>, p.chunks, rs::kPlaceBlock, stream, ids, n, f, e, p.chunk, table);
+        });
+        ok = ok && launch_kernel(RS_KERNEL_EXPERT, stream, [&] {
+            run_kernel(rs::expert_place_kernel<ID, kTileItems, true>, p.chunks, rs::kPlaceBlock, stream, ids, n, f, e,
+                       key_bits, p.chunk, table, order, position, offsets);
+        });
+    }
+    return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
+}
+
+// ---------------------------------------------------------------------------
+// Rows
+// ---------------------------------------------------------------------------
+bool good_shape(int dtype, size_t tokens, int width, int k, size_t num_rows) {
+    return dtype_bytes(dtype) != 0 && width >= 1 && width <= RS_MAX_ROW_WIDTH && k >= 1 && k <= RS_MAX_CHOICES &&
+           tokens <= RS_MAX_SLOTS / static_cast<size_t>(k) && num_rows <= RS_MAX_SLOTS;
+}
+
+struct RowGrid {
+    int lanes, chunks;
+    unsigned grid;
+};
+
+RowGrid row_grid(size_t tokens, int width, int vec) {
+    const int vecs = (width + vec - 1) / vec;
+    RowGrid g;
+    g.lanes = 1;
+    while (g.lanes < vecs && g.lanes < rs::kRowBlock) g.lanes *= 2;
+    g.chunks = (vecs + g.lanes - 1) / g.lanes;
+    g.grid = grid_for(tokens * static_cast<size_t>(g.chunks), static_cast<unsigned>(rs::kRowBlock / g.lanes), kMaxGrid);
+    return g;
+}
+
+bool launch_spread(int dtype, const void *x, size_t tokens, int width, size_t x_stride, const int32_t *position,
+                   const float *weights, int k, void *rows, size_t num_rows, size_t rows_stride, hipStream_t stream) {
+    if (tokens == 0 || num_rows == 0) return true;
+    return with_dtype(dtype, [&](auto zero) {
+        using T = decltype(zero);
+        const RowGrid g = row_grid(tokens, width, rs::kVec<T>);
+        const auto go = [&](auto kernel) {
+            return launch_kernel(RS_KERNEL_ROWS, stream, [&] {
+                run_kernel(kernel, g.grid, rs::kRowBlock, stream, static_cast<const T *>(x), tokens, width, x_stride,
+                           position, weights, k, static_cast<T *>(rows), num_rows, rows_stride, g.lanes, g.chunks);
+            });
+        };
+        return weights ? go(rs::spread_rows_kernel<T, true>) : go(rs::spread_rows_kernel<T, false>);
+    });
+}
+
+bool launch_join(int dtype, const void *rows, size_t num_rows, size_t rows_stride, const int32_t *position,
+                 const float *weights, int k, void *out, size_t tokens, int width, size_t out_stride,
+                 hipStream_t stream) {
+    if (tokens == 0) return true;
+    return with_dtype(dtype, [&](auto zero) {
+        using T = decltype(zero);
+        const RowGrid g = row_grid(tokens, width, rs::kVec<T>);
+        const auto go = [&](auto kernel) {
+            return launch_kernel(RS_KERNEL_ROWS, stream, [&] {
+                run_kernel(kernel, g.grid, rs::kRowBlock, stream, static_cast<const T *>(rows), num_rows, rows_stride,
+                           position, weights, k, static_cast<T *>(out), tokens, width, out_stride, g.lanes, g.chunks);
+            });
+        };
+        return weights ? go(rs::join_rows_kernel<T, true>) : go(rs::join_rows_kernel<T, false>);
+    });
+}
+
+bool launch_dots(int dtype, const void *x, size_t tokens, int width, size_t x_stride, const void *rows,
+                 size_t num_rows, size_t rows_stride, const int32_t *position, int k, float *dots,
+                 hipStream_t stream) {
+    if (tokens == 0) return true;
+    return with_dtype(dtype, [&](auto zero) {
+        using T = decltype(zero);
+        const unsigned grid = grid_for(tokens * static_cast<size_t>(k), rs::kRowBlock / 64, kMaxGrid);
+        return launch_kernel(RS_KERNEL_ROWS, stream, [&] {
+            run_kernel(rs::dot_rows_kernel<T>, grid, rs::kRowBlock, stream, static_cast<const T *>(x), tokens, width,
+                       x_stride, static_cast<const T *>(rows), num_rows, rows_stride, position, k, dots);
+        });
+    });
+}
+
+}  // namespace
+
+extern "C" {
+
+rs_status rs_route_topk(const void *logits, int dtype, size_t tokens, int experts, size_t stride, int k, int gate,
+                        int renormalize, float scale, float *weights_out, int32_t *experts_out, hipStream_t stream) {
+    if (!good_route(dtype, tokens, experts, k, gate)) return RS_ERROR_INVALID_VALUE;
+    const size_t elem = static_cast<size_t>(dtype_bytes(dtype)), slots = tokens * static_cast<size_t>(k);
+    if (!good_rows(logits, tokens, experts, stride, elem, false) || !good(weights_out, slots, 4) ||
+        !good(experts_out, slots, 4)) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    const Span spans[] = {span_of(weights_out, slots * 4), span_of(experts_out, slots * 4),
+                          span_of(logits, span_bytes(tokens, static_cast<size_t>(experts), stride, elem))};
+    if (!disjoint(spans, 2, 3)) return RS_ERROR_INVALID_VALUE;
+    if (tokens == 0) return RS_SUCCESS;
+    const bool ok = with_dtype(dtype, [&](auto zero) {
+        return with_group<decltype(zero)>(experts, k, [&](auto t, auto g, auto v) {
+            using T = decltype(t);
+            constexpr int G = decltype(g)::value, V = decltype(v)::value;
+            const unsigned grid = grid_for(tokens, rs::kRouteBlock / G, kMaxGrid);
+            return launch_kernel(RS_KERNEL_ROUTE, stream, [&] {
+                run_kernel(rs::route_topk_kernel<T, G, V>, grid, rs::kRouteBlock, stream,
+                           static_cast<const T *>(logits), tokens, experts, stride, k, gate, renormalize, scale,
+                           weights_out, experts_out);
+            });
+        });
+    });
+    return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
+}
+
+rs_status rs_route_topk_backward(const void *logits, int dtype, size_t tokens, int experts, size_t stride,
+                                 const int32_t *chosen, const float *grad_weights, int k, int gate, int renormalize,
+                                 float scale, void *grad_logits, size_t grad_stride, hipStream_t stream) {
+    if (!good_route(dtype, tokens, experts, k, gate)) return RS_ERROR_INVALID_VALUE;
+    const size_t elem = static_cast<size_t>(dtype_bytes(dtype)), slots = tokens * static_cast<size_t>(k);
+    if (!good_rows(logits, tokens, experts, stride, elem, false) || !good(chosen, slots, 4) ||
+        !good(grad_weights, slots, 4) || !good_rows(grad_logits, tokens, experts, grad_stride, elem, true)) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    const auto row = static_cast<size_t>(experts);
+    const Span spans[] = {span_of(grad_logits, span_bytes(tokens, row, grad_stride, elem)), span_of(chosen, slots * 4),
+                          span_of(grad_weights, slots * 4), span_of(logits, span_bytes(tokens, row, stride, elem))};
+    if (!disjoint(spans, 1, 4)) return RS_ERROR_INVALID_VALUE;
+    if (tokens == 0) return RS_SUCCESS;
+    const bool ok = with_dtype(dtype, [&](auto zero) {
+        return with_group<decltype(zero)>(experts, k, [&](auto t, auto g, auto v) {
+            using T = decltype(t);
+            constexpr int G = decltype(g)::value, V = decltype(v)::value;
+            const unsigned grid = grid_for(tokens, rs::kRouteBlock / G, kMaxGrid);
+            return launch_kernel(RS_KERNEL_ROUTE, stream, [&] {
+                run_kernel(rs::route_topk_backward_kernel<T, G, V>, grid, rs::kRouteBlock, stream,
+                           static_cast<const T *>(logits), tokens, experts, stride, chosen, grad_weights, k, gate,
+                           renormalize, scale, static_cast<T *>(grad_logits), grad_stride);
+            });
+        });
+    });
+    return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
+}
+
+size_t rs_temp_bytes_experts(size_t n, int experts) { return good_experts(n, experts) ? expert_temp(n, experts) : 0; }
+
+rs_status rs_sort_experts_i32(const int32_t *ids, size_t n, int first, int experts, int32_t *order_out,
+                              int32_t *position_out, int32_t *offsets_out, void *temp, size_t temp_bytes,
+                              hipStream_t stream) {
+    return sort_experts(ids, n, first, experts, order_out, position_out, offsets_out, temp, temp_bytes, stream);
+}
+
+rs_status rs_sort_experts_i64(const int64_t *ids, size_t n, int first, int experts, int32_t *order_out,
+                              int32_t *position_out, int32_t *offsets_out, void *temp, size_t temp_bytes,
+                              hipStream_t stream) {
+    return sort_experts(ids, n, first, experts, order_out, position_out, offsets_out, temp, temp_bytes, stream);
+}
+
+rs_status rs_dispatch_rows(const void *x, int dtype, size_t tokens, int width, size_t x_stride,
+                           const int32_t *position, const float *weights, int k, void *rows, size_t num_rows,
+                           size_t rows_stride, hipStream_t stream) {
+    if (!good_shape(dtype, tokens, width, k, num_rows)) return RS_ERROR_INVALID_VALUE;
+    const size_t elem = static_cast<size_t>(dtype_bytes(dtype)), slots = tokens * static_cast<size_t>(k);
+    if (!good_rows(x, tokens, width, x_stride, elem, false) || !good(position, slots, 4) ||
+        !good_rows(rows, num_rows, width, rows_stride, elem, true) || (weights && !aligned(weights, 4))) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    const auto w = static_cast<size_t>(width);
+    const Span spans[] = {span_of(rows, span_bytes(num_rows, w, rows_stride, elem)),
+                          span_of(x, span_bytes(tokens, w, x_stride, elem)), span_of(position, slots * 4),
+                          span_of(weights, weights ? slots * 4 : 0)};
+    if (!disjoint(spans, 1, 4)) return RS_ERROR_INVALID_VALUE;
+    return launch_spread(dtype, x, tokens, width, x_stride, position, weights, k, rows, num_rows, rows_stride, stream)
+               ? RS_SUCCESS
+               : RS_ERROR_LAUNCH;
+}
+
+rs_status rs_dispatch_rows_backward(const void *grad_rows, int dtype, size_t num_rows, size_t grad_rows_stride,
+                                    const int32_t *position, const float *weights, int k, const void *x,
+                                    size_t x_stride, void *grad_x, size_t grad_x_stride, float *grad_weights,
+                                    size_t tokens, int width, hipStream_t stream) {
+    if (!good_shape(dtype, tokens, width, k, num_rows)) return RS_ERROR_INVALID_VALUE;
+    const size_t elem = static_cast<size_t>(dtype_bytes(dtype)), slots = tokens * static_cast<size_t>(k);
+    if (!good_rows(grad_rows, num_rows, width, grad_rows_stride, elem, false) || !good(position, slots, 4) ||
+        !good_rows(grad_x, tokens, width, grad_x_stride, elem, true) || (weights && !aligned(weights, 4))) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    const bool dots = grad_weights != nullptr;
+    if (dots && (!aligned(grad_weights, 4) || !good_rows(x, tokens, width, x_stride, elem, false))) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    const auto w = static_cast<size_t>(width);
+    const Span spans[] = {span_of(grad_x, span_bytes(tokens, w, grad_x_stride, elem)),
+                          span_of(grad_weights, dots ? slots * 4 : 0),
+                          span_of(grad_rows, span_bytes(num_rows, w, grad_rows_stride, elem)),
+                          span_of(position, slots * 4), span_of(weights, weights ? slots * 4 : 0),
+                          span_of(x, dots ? span_bytes(tokens, w, x_stride, elem) : 0)};
+    if (!disjoint(spans, 2, 6)) return RS_ERROR_INVALID_VALUE;
+    bool ok = launch_join(dtype, grad_rows, num_rows, grad_rows_stride, position, weights, k, grad_x, tokens, width,
+                          grad_x_stride, stream);
+    if (dots) {
+        ok = ok && launch_dots(dtype, x, tokens, width, x_stride, grad_rows, num_rows, grad_rows_stride, position, k,
+                               grad_weights, stream);
+    }
+    return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
+}
+
+rs_status rs_combine_rows(const void *rows, int dtype, size_t num_rows, size_t rows_stride, const int32_t *position,
+                          const float *weights, int k, void *out, size_t tokens, int width, size_t out_stride,
+                          hipStream_t stream) {
+    return rs_dispatch_rows_backward(rows, dtype, num_rows, rows_stride, position, weights, k, nullptr, 0, out,
+                                     out_stride, nullptr, tokens, width, stream);
+}
+
+rs_status rs_combine_rows_backward(const void *grad_out, int dtype, size_t tokens, int width, size_t grad_out_stride,
+                                   const int32_t *position, const float *weights, int k, const void *rows,
+                                   size_t rows_stride, void *grad_rows, size_t grad_rows_stride, size_t num_rows,
+                                   float *grad_weights, hipStream_t stream) {
+    if (!good_shape(dtype, tokens, width, k, num_rows)) return RS_ERROR_INVALID_VALUE;
+    const size_t elem = static_cast<size_t>(dtype_bytes(dtype)), slots = tokens * static_cast<size_t>(k);
+    if (!good_rows(grad_out, tokens, width, grad_out_stride, elem, false) || !good(position, slots, 4) ||
+        !good_rows(grad_rows, num_rows, width, grad_rows_stride, elem, true) || (weights && !aligned(weights, 4))) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    const bool dots = grad_weights != nullptr;
+    if (dots && (!aligned(grad_weights, 4) || !good_rows(rows, num_rows, width, rows_stride, elem, false))) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    const auto w = static_cast<size_t>(width);
+    const Span spans[] = {span_of(grad_rows, span_bytes(num_rows, w, grad_rows_stride, elem)),
+                          span_of(grad_weights, dots ? slots * 4 : 0),
+                          span_of(grad_out, span_bytes(tokens, w, grad_out_stride, elem)),
+                          span_of(position, slots * 4), span_of(weights, weights ? slots * 4 : 0),
+                          span_of(rows, dots ? span_bytes(num_rows, w, rows_stride, elem) : 0)};
+    if (!disjoint(spans, 2, 6)) return RS_ERROR_INVALID_VALUE;
+    bool ok = launch_spread(dtype, grad_out, tokens, width, grad_out_stride, position, weights, k, grad_rows, num_rows,
+                            grad_rows_stride, stream);
+    if (dots) {
+        ok = ok && launch_dots(dtype, grad_out, tokens, width, grad_out_stride, rows, num_rows, rows_stride, position,
+                               k, grad_weights, stream);
+    }
+    return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
+}
+
+}  // extern "C"

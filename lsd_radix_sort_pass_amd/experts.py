@@ -1,0 +1,383 @@
+"""Mixture-of-experts calls: tokens routed, their slots sorted by expert, and
+token rows carried to their sorted places and back.
+
+T tokens choose k of E experts each; slot s = t * k + j is choice j of token t.
+
+    w, e = rs.route_topk(logits, k)                       # (T, k) weights, experts
+    order, position, offsets = rs.sort_experts(e, E)      # slots by expert
+    rows = rs.dispatch_rows(x, position)                  # (T * k, H), expert by expert
+    # expert i works on rows[offsets[i]:offsets[i + 1]]
+    out = rs.combine_rows(rows, position, w)              # (T, H)
+
+Each call only marshals arguments to the C ABI (include/rs.h, which states the
+results in full).  Gradients are calls of their own (`*_backward`), as every
+call here is one or two kernel launches on the caller's stream: all of them
+can be captured into a graph.  They do not record for autograd, and refuse
+tensors that require a gradient while gradients are enabled: call them inside
+a torch.autograd.Function, or under torch.no_grad().
+
+`stream` works as if the call were made under torch.cuda.stream(stream):
+outputs and temp storage that a call allocates belong to that stream, and
+inputs are kept from reuse until its work is done; ordering the streams is the
+caller's.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import NamedTuple, Optional, Tuple, Union
+
+import torch
+
+from . import _lib
+
+__all__ = [
+    "MAX_EXPERTS", "MAX_CHOICES", "ExpertOrder", "route_topk", "route_topk_backward", "temp_bytes_experts",
+    "sort_experts", "dispatch_rows", "dispatch_rows_backward", "combine_rows", "combine_rows_backward",
+]
+
+MAX_EXPERTS = 1024      # RS_MAX_EXPERTS in include/rs.h
+MAX_CHOICES = 64        # RS_MAX_CHOICES
+
+_ROW_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}      # rs_dtype
+_GATES = {"softmax": 0, "sigmoid": 1}                                      # rs_gate
+_SORT_FN = {torch.int32: "rs_sort_experts_i32", torch.int64: "rs_sort_experts_i64"}
+
+
+class ExpertOrder(NamedTuple):
+    """Slots sorted by expert: order[p] is the slot at place p, position[t, j]
+    the place of slot (t, j) (~place where it is dropped), and expert e holds
+    the places offsets[e] .. offsets[e + 1] - 1."""
+    order: torch.Tensor
+    position: torch.Tensor
+    offsets: torch.Tensor
+
+
+def _tensor(t, name, dtypes, dim, device=None) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device tensor (got {t.device})")
+    if t.dtype not in dtypes:
+        names = ", ".join(str(d).replace("torch.", "") for d in dtypes)
+        raise TypeError(f"{name} must be one of {names} (got {t.dtype})")
+    if dim is not None and t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions (got {t.dim()})")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, which this call does not record: use it in a "
+                         "torch.autograd.Function or under torch.no_grad()")
+    return t
+
+
+def _rows(t, name, device=None, dtype=None, shape=None) -> torch.Tensor:
+    """A 2-D float tensor with consecutive elements in a row, any row stride."""
+    _tensor(t, name, _ROW_DTYPES if dtype is None else (dtype,), 2, device)
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape} (got {tuple(t.shape)})")
+    if t.shape[1] > 1 and t.stride(1) != 1 and t.shape[0]:
+        raise ValueError(f"{name} must have consecutive elements in each row")
+    return t
+
+
+def _flat(t, name, dtypes, device, shape=None, dim=None) -> torch.Tensor:
+    _tensor(t, name, dtypes, dim, device)
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape} (got {tuple(t.shape)})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _places(position, weights, device) -> Tuple[int, int]:
+    """(tokens, k) of a call's places, with its weights checked against them."""
+    _flat(position, "position", (torch.int32,), device, dim=2)
+    if weights is not None:
+        _flat(weights, "weights", (torch.float32,), device, tuple(position.shape))
+    return position.shape[0], position.shape[1]
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+class _Call:
+    """Device, stream and allocation of one call: its tensors belong to the
+    stream it runs on, and its kernels are launched on that stream's device."""
+
+    def __init__(self, device, stream, *inputs):
+        self._guards = []
+        if device.index != torch.cuda.current_device():
+            self._guards.append(torch.cuda.device(device))
+        if stream is not None and stream != torch.cuda.current_stream(device):
+            if stream.device != device:
+                raise ValueError(f"stream must belong to {device} (got {stream.device})")
+            self._guards.append(torch.cuda.stream(stream))
+            for t in inputs:
+                if t is not None:
+                    t.record_stream(stream)
+        self.handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+    def run(self, body):
+        if not self._guards:
+            return body(self.handle)
+        with contextlib.ExitStack() as stack:
+            for guard in self._guards:
+                stack.enter_context(guard)
+            return body(self.handle)
+
+
+def _ok(code: int, name: str) -> None:
+    if code != _lib.RS_SUCCESS:
+        from . import RadixSortError
+        raise RadixSortError(code, name)
+
+
+def _gate(mode) -> int:
+    if mode not in _GATES:
+        raise ValueError(f"mode must be one of {', '.join(_GATES)} (got {mode!r})")
+    return _GATES[mode]
+
+
+def _choices(k, experts) -> int:
+    k = int(k)
+    if not 1 <= k <= min(experts, MAX_CHOICES):
+        raise ValueError(f"k must be between 1 and min(experts, {MAX_CHOICES}) (got {k} of {experts} experts)")
+    return k
+
+
+def route_topk(logits: torch.Tensor, k: int, mode: str = "softmax", renormalize: bool = False, scale: float = 1.0,
+               weights_out: Optional[torch.Tensor] = None, experts_out: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The k largest logits of each row of a (T, E) tensor (float32, float16
+    or bfloat16), ties to the lowest index, and the weights of those experts.
+
+    mode "softmax" takes the softmax over the whole row, "sigmoid" each
+    logit's own sigmoid; renormalize divides by the sum of the chosen ones
+    (with "softmax": the softmax of the chosen logits); scale multiplies.
+    Returns (weights float32, experts int32), both (T, k).  A logit of -inf
+    bars the row from an expert; slots without one get expert -1, weight 0."""
+    _rows(logits, "logits")
+    tokens, experts = logits.shape
+    k, gate, device = _choices(k, experts), _gate(mode), logits.device
+    if weights_out is not None:
+        _flat(weights_out, "weights_out", (torch.float32,), device, (tokens, k))
+    if experts_out is not None:
+        _flat(experts_out, "experts_out", (torch.int32,), device, (tokens, k))
+    call = _Call(device, stream, logits, weights_out, experts_out)
+
+    def body(handle):
+        w = torch.empty((tokens, k), dtype=torch.float32, device=device) if weights_out is None else weights_out
+        e = torch.empty((tokens, k), dtype=torch.int32, device=device) if experts_out is None else experts_out
+        _ok(_lib.load().rs_route_topk(logits.data_ptr(), _ROW_DTYPES[logits.dtype], tokens, experts,
+                                      logits.stride(0), k, gate, 1 if renormalize else 0, scale, w.data_ptr(),
+                                      e.data_ptr(), handle), "rs_route_topk")
+        return w, e
+    return call.run(body)
+
+
+def route_topk_backward(logits: torch.Tensor, experts: torch.Tensor, grad_weights: torch.Tensor,
+                        mode: str = "softmax", renormalize: bool = False, scale: float = 1.0,
+                        out: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The gradient of route_topk's logits, (T, E) in their dtype, from that
+    of its weights; experts, mode, renormalize and scale are the forward
+    call's."""
+    _rows(logits, "logits")
+    tokens, count = logits.shape
+    device, gate = logits.device, _gate(mode)
+    _flat(experts, "experts", (torch.int32,), device, dim=2)
+    k = _choices(experts.shape[1], count)
+    if experts.shape[0] != tokens:
+        raise ValueError("experts must have a row for each row of logits")
+    _flat(grad_weights, "grad_weights", (torch.float32,), device, (tokens, k))
+    if out is not None:
+        _rows(out, "out", device, logits.dtype, (tokens, count))
+    call = _Call(device, stream, logits, experts, grad_weights, out)
+
+    def body(handle):
+        grad = torch.empty((tokens, count), dtype=logits.dtype, device=device) if out is None else out
+        _ok(_lib.load().rs_route_topk_backward(logits.data_ptr(), _ROW_DTYPES[logits.dtype], tokens, count,
+                                               logits.stride(0), experts.data_ptr(), grad_weights.data_ptr(), k,
+                                               gate, 1 if renormalize else 0, scale, grad.data_ptr(),
+                                               grad.stride(0), handle), "rs_route_topk_backward")
+        return grad
+    return call.run(body)
+
+
+def temp_bytes_experts(n: int, num_experts: int) -> int:
+    """Temp bytes of sort_experts on n slots."""
+    return int(_lib.load().rs_temp_bytes_experts(n, num_experts))
+
+
+def sort_experts(experts: torch.Tensor, num_experts: int, first_expert: int = 0,
+                 order_out: Optional[torch.Tensor] = None, position_out: Optional[torch.Tensor] = None,
+                 offsets_out: Optional[torch.Tensor] = None, temp: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> ExpertOrder:
+    """Stable sort of the slots of a contiguous int32 or int64 tensor of
+    expert numbers (any shape) by expert.
+
+    Experts first_expert .. first_expert + num_experts - 1 are counted; slots
+    of any other number are dropped: they sort last, and position holds ~place
+    for them.  Returns ExpertOrder(order (n,), position (the shape of experts),
+    offsets (num_experts + 1,)), all int32."""
+    _flat(experts, "experts", _SORT_FN, None)
+    n, device, num = experts.numel(), experts.device, int(num_experts)
+    if not 1 <= num <= MAX_EXPERTS:
+        raise ValueError(f"num_experts must be between 1 and {MAX_EXPERTS} (got {num})")
+    if not 0 <= int(first_expert) <= 2**31 - num:
+        raise ValueError(f"first_expert must be between 0 and 2^31 - num_experts (got {first_expert})")
+    if order_out is not None:
+        _flat(order_out, "order_out", (torch.int32,), device, (n,))
+    if position_out is not None:
+        _flat(position_out, "position_out", (torch.int32,), device, tuple(experts.shape))
+    if offsets_out is not None:
+        _flat(offsets_out, "offsets_out", (torch.int32,), device, (num + 1,))
+    if temp is not None:
+        _flat(temp, "temp", (torch.uint8,), device)
+    call = _Call(device, stream, experts, order_out, position_out, offsets_out, temp)
+    name = _SORT_FN[experts.dtype]
+
+    def body(handle):
+        lib = _lib.load()
+        new = lambda shape: torch.empty(shape, dtype=torch.int32, device=device)
+        order = new(n) if order_out is None else order_out
+        position = new(experts.shape) if position_out is None else position_out
+        offsets = new(num + 1) if offsets_out is None else offsets_out
+        store = temp
+        if store is None:
+            need = int(lib.rs_temp_bytes_experts(n, num))
+            store = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        _ok(getattr(lib, name)(experts.data_ptr(), n, int(first_expert), num, order.data_ptr(), position.data_ptr(),
+                               offsets.data_ptr(), _ptr(store), 0 if store is None else store.numel(), handle), name)
+        return ExpertOrder(order, position, offsets)
+    return call.run(body)
+
+
+def dispatch_rows(x: torch.Tensor, position: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Token rows carried to their sorted places: out[position[t, j]] = x[t],
+    times weights[t, j] if given, and zeros at the place of a dropped slot.
+
+    x (T, H) float32, float16 or bfloat16; position (T, k) int32 as
+    sort_experts gives it; weights (T, k) float32.  out (rows, H) defaults to
+    a new (T * k, H) tensor, which sort_experts's positions fill; rows of a
+    given `out` that no slot names are left as they were, and places beyond it
+    are skipped."""
+    _rows(x, "x")
+    device = x.device
+    tokens, k = _places(position, weights, device)
+    if x.shape[0] != tokens:
+        raise ValueError("position must have a row for each row of x")
+    if out is not None:
+        _rows(out, "out", device, x.dtype)
+        if out.shape[1] != x.shape[1]:
+            raise ValueError("out must have the width of x")
+    call = _Call(device, stream, x, position, weights, out)
+
+    def body(handle):
+        rows = torch.empty((tokens * k, x.shape[1]), dtype=x.dtype, device=device) if out is None else out
+        _ok(_lib.load().rs_dispatch_rows(x.data_ptr(), _ROW_DTYPES[x.dtype], tokens, x.shape[1], x.stride(0),
+                                         position.data_ptr(), _ptr(weights), k, rows.data_ptr(), rows.shape[0],
+                                         rows.stride(0), handle), "rs_dispatch_rows")
+        return rows
+    return call.run(body)
+
+
+def dispatch_rows_backward(grad_rows: torch.Tensor, position: torch.Tensor, x: Optional[torch.Tensor] = None,
+                           weights: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                           grad_weights_out: Optional[torch.Tensor] = None,
+                           stream: Optional[torch.cuda.Stream] = None
+                           ) -> Union[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]]:
+    """The gradients of dispatch_rows from that of its rows: grad_x (T, H), and
+    with x given also grad_weights (T, k) float32, as a pair.  weights are the
+    forward call's."""
+    _rows(grad_rows, "grad_rows")
+    device, width = grad_rows.device, grad_rows.shape[1]
+    tokens, k = _places(position, weights, device)
+    if x is not None:
+        _rows(x, "x", device, grad_rows.dtype, (tokens, width))
+    elif grad_weights_out is not None:
+        raise ValueError("grad_weights_out needs x")
+    if out is not None:
+        _rows(out, "out", device, grad_rows.dtype, (tokens, width))
+    if grad_weights_out is not None:
+        _flat(grad_weights_out, "grad_weights_out", (torch.float32,), device, (tokens, k))
+    call = _Call(device, stream, grad_rows, position, x, weights, out, grad_weights_out)
+
+    def body(handle):
+        grad = torch.empty((tokens, width), dtype=grad_rows.dtype, device=device) if out is None else out
+        dots = grad_weights_out
+        if x is not None and dots is None:
+            dots = torch.empty((tokens, k), dtype=torch.float32, device=device)
+        _ok(_lib.load().rs_dispatch_rows_backward(
+            grad_rows.data_ptr(), _ROW_DTYPES[grad_rows.dtype], grad_rows.shape[0], grad_rows.stride(0),
+            position.data_ptr(), _ptr(weights), k, _ptr(x), 0 if x is None else x.stride(0), grad.data_ptr(),
+            grad.stride(0), _ptr(dots), tokens, width, handle), "rs_dispatch_rows_backward")
+        return grad if x is None else (grad, dots)
+    return call.run(body)
+
+
+def combine_rows(rows: torch.Tensor, position: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Sorted rows joined back to their tokens: out[t] = the sum over j of
+    rows[position[t, j]], times weights[t, j] if given, without the dropped
+    slots; zeros for a token that has no other.
+
+    rows (n, H) float32, float16 or bfloat16, position (T, k) int32, weights
+    (T, k) float32; out (T, H) in the dtype of rows, summed in float32."""
+    _rows(rows, "rows")
+    device, width = rows.device, rows.shape[1]
+    tokens, k = _places(position, weights, device)
+    if out is not None:
+        _rows(out, "out", device, rows.dtype, (tokens, width))
+    call = _Call(device, stream, rows, position, weights, out)
+
+    def body(handle):
+        res = torch.empty((tokens, width), dtype=rows.dtype, device=device) if out is None else out
+        _ok(_lib.load().rs_combine_rows(rows.data_ptr(), _ROW_DTYPES[rows.dtype], rows.shape[0], rows.stride(0),
+                                        position.data_ptr(), _ptr(weights), k, res.data_ptr(), tokens, width,
+                                        res.stride(0), handle), "rs_combine_rows")
+        return res
+    return call.run(body)
+
+
+def combine_rows_backward(grad_out: torch.Tensor, position: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                          weights: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                          grad_weights_out: Optional[torch.Tensor] = None,
+                          stream: Optional[torch.cuda.Stream] = None
+                          ) -> Union[torch.Tensor, Tuple[torch.Tensor, torch.Tensor]]:
+    """The gradients of combine_rows from that of its result: grad_rows, and
+    with rows given also grad_weights (T, k) float32, as a pair.  weights are
+    the forward call's.  grad_rows has the shape of rows, or (T * k, H) without
+    them; the rows of dropped slots are zeros, and as in dispatch_rows rows
+    that no slot names are left as they were."""
+    _rows(grad_out, "grad_out")
+    device, width = grad_out.device, grad_out.shape[1]
+    tokens, k = _places(position, weights, device)
+    if grad_out.shape[0] != tokens:
+        raise ValueError("position must have a row for each row of grad_out")
+    count = tokens * k if out is None else out.shape[0]
+    if rows is not None:
+        count = rows.shape[0]
+        _rows(rows, "rows", device, grad_out.dtype, (count, width))
+    elif grad_weights_out is not None:
+        raise ValueError("grad_weights_out needs rows")
+    if out is not None:
+        _rows(out, "out", device, grad_out.dtype, (count, width))
+    if grad_weights_out is not None:
+        _flat(grad_weights_out, "grad_weights_out", (torch.float32,), device, (tokens, k))
+    call = _Call(device, stream, grad_out, position, rows, weights, out, grad_weights_out)
+
+    def body(handle):
+        grad = torch.empty((count, width), dtype=grad_out.dtype, device=device) if out is None else out
+        dots = grad_weights_out
+        if rows is not None and dots is None:
+            dots = torch.empty((tokens, k), dtype=torch.float32, device=device)
+        _ok(_lib.load().rs_combine_rows_backward(
+            grad_out.data_ptr(), _ROW_DTYPES[grad_out.dtype], tokens, width, grad_out.stride(0),
+            position.data_ptr(), _ptr(weights), k, _ptr(rows), 0 if rows is None else rows.stride(0),
+            grad.data_ptr(), grad.stride(0), count, _ptr(dots), handle), "rs_combine_rows_backward")
+        return grad if rows is None else (grad, dots)
+    return call.run(body)
