@@ -95,7 +95,7 @@ bool good_route(int dtype, size_t tokens, int experts, int k, int gate) {
 // cut into at most kMaxChunks chunks of whole tiles, counted by one launch and
 // placed by a second.
 constexpr size_t kOneGroup = 8 * rs::kPlaceBlock;
-constexpr int kTileItems = 8;
+constexpr int kTileItems = 4;
 constexpr size_t kTile = size_t{kTileItems} * rs::kPlaceBlock;
 constexpr size_t kMaxChunks = 256;
 
@@ -115,7 +115,7 @@ ExpertPlan expert_plan(size_t n) {
 
 size_t expert_temp(size_t n, int experts) {
     if (n <= kOneGroup) return 0;
-    const size_t bytes = size_t{expert_plan(n).chunks} * (static_cast<size_t>(experts) + 1) * 4;
+    const size_t bytes = size_t{expert_plan(n).chunks} * rs::table_stride(static_cast<uint32_t>(experts)) * 4;
     return (bytes + kTempAlign - 1) / kTempAlign * kTempAlign;
 }
 
@@ -140,33 +140,29 @@ rs_status sort_experts(const ID *ids, size_t n, int first, int experts, int32_t 
                           span_of(ids, n * sizeof(ID))};
     if (!disjoint(spans, 4, 5)) return RS_ERROR_INVALID_VALUE;
 
-    int key_bits = 1;
-    while ((1 << key_bits) <= experts) ++key_bits;  // keys 0 .. experts
     const auto e = static_cast<uint32_t>(experts);
     const auto f = static_cast<ID>(first);
     auto *table = static_cast<uint32_t *>(temp);
-    bool ok;
-    if (n <= kOneGroup) {
-        ok = launch_kernel(RS_KERNEL_EXPERT, stream, [&] {
-            const uint32_t *none = nullptr;
-            if (n <= rs::kPlaceBlock) {
-                run_kernel(rs::expert_place_kernel<ID, 1, false>, 1, rs::kPlaceBlock, stream, ids, n, f, e, key_bits, n,
-                           none, order, position, offsets);
-            } else {
-                run_kernel(rs::expert_place_kernel<ID, 8, false>, 1, rs::kPlaceBlock, stream, ids, n, f, e, key_bits, n,
-                           none, order, position, offsets);
-            }
+    const ExpertPlan p = expert_plan(n);
+    const auto place = [&](auto kernel, unsigned grid, size_t chunk, const uint32_t *counts) {
+        return launch_kernel(RS_KERNEL_EXPERT, stream, [&] {
+            run_kernel(kernel, grid, rs::kPlaceBlock, stream, ids, n, f, e, chunk, counts, order, position, offsets);
         });
-    } else {
-        const ExpertPlan p = expert_plan(n);
-        ok = launch_kernel(RS_KERNEL_EXPERT, stream, [&] {
-            run_kernel(rs::expert_count_kernel<ID>, p.chunks, rs::kPlaceBlock, stream, ids, n, f, e, p.chunk, table);
+    };
+    const auto run = [&](auto bits) {
+        constexpr int kBits = decltype(bits)::value;
+        if (n <= rs::kPlaceBlock) return place(rs::expert_place_kernel<ID, 1, false, kBits>, 1, n, nullptr);
+        if (n <= kOneGroup) return place(rs::expert_place_kernel<ID, 8, false, kBits>, 1, n, nullptr);
+        const bool ok = launch_kernel(RS_KERNEL_EXPERT, stream, [&] {
+            run_kernel(rs::expert_count_kernel<ID, kTileItems>, p.chunks, rs::kPlaceBlock, stream, ids, n, f, e, p.chunk,
+                       table);
         });
-        ok = ok && launch_kernel(RS_KERNEL_EXPERT, stream, [&] {
-            run_kernel(rs::expert_place_kernel<ID, kTileItems, true>, p.chunks, rs::kPlaceBlock, stream, ids, n, f, e,
-                       key_bits, p.chunk, table, order, position, offsets);
-        });
-    }
+        return ok && place(rs::expert_place_kernel<ID, kTileItems, true, kBits>, p.chunks, p.chunk, table);
+    };
+    // Keys 0 .. experts in as few ballots as these cover.
+    const bool ok = experts < 128   ? run(std::integral_constant<int, 7>{})
+                    : experts < 512 ? run(std::integral_constant<int, 9>{})
+                                    : run(std::integral_constant<int, 11>{});
     return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
 }
 
@@ -178,65 +174,94 @@ bool good_shape(int dtype, size_t tokens, int width, int k, size_t num_rows) {
            tokens <= RS_MAX_SLOTS / static_cast<size_t>(k) && num_rows <= RS_MAX_SLOTS;
 }
 
-struct RowGrid {
-    int lanes, chunks;
-    unsigned grid;
-};
+// Calls f(integral_constant B) with the batch for k slots: the fewest batches
+// of at most kMaxBatch, of even size.
+template <class F>
+bool with_batch(int k, F &&f) {
+    const int batches = (k + rs::kMaxBatch - 1) / rs::kMaxBatch;
+    const int size = (k + batches - 1) / batches;
+    if (size <= 1) return f(std::integral_constant<int, 1>{});
+    if (size <= 2) return f(std::integral_constant<int, 2>{});
+    if (size <= 4) return f(std::integral_constant<int, 4>{});
+    if (size <= 6) return f(std::integral_constant<int, 6>{});
+    return f(std::integral_constant<int, 8>{});
+}
 
-RowGrid row_grid(size_t tokens, int width, int vec) {
-    const int vecs = (width + vec - 1) / vec;
-    RowGrid g;
-    g.lanes = 1;
-    while (g.lanes < vecs && g.lanes < rs::kRowBlock) g.lanes *= 2;
-    g.chunks = (vecs + g.lanes - 1) / g.lanes;
-    g.grid = grid_for(tokens * static_cast<size_t>(g.chunks), static_cast<unsigned>(rs::kRowBlock / g.lanes), kMaxGrid);
-    return g;
+// Enqueues the spread or the join of w, with its dots if w.dots is set.
+template <bool SPREAD, class T>
+bool launch_rows(rs::RowWork<T> w, hipStream_t stream) {
+    const int vecs = (w.width + rs::kVec<T> - 1) / rs::kVec<T>;
+    const auto go = [&](auto kernel, size_t units, int per_block) {
+        const unsigned grid = grid_for(units, static_cast<unsigned>(per_block), kMaxGrid);
+        return launch_kernel(RS_KERNEL_ROWS, stream, [&] { run_kernel(kernel, grid, rs::kRowBlock, stream, w); });
+    };
+    const auto dots = [&] {
+        return go(rs::dot_rows_kernel<T>, w.tokens * static_cast<size_t>(w.k), rs::kRowBlock / 64);
+    };
+    if (vecs <= rs::kNarrow) {
+        w.lanes = 1;
+        while (w.lanes < vecs) w.lanes *= 2;
+        const int per_block = rs::kRowBlock / w.lanes;
+        const bool ok = w.weights ? go(rs::narrow_rows_kernel<T, SPREAD, true>, w.tokens, per_block)
+                                  : go(rs::narrow_rows_kernel<T, SPREAD, false>, w.tokens, per_block);
+        return ok && (w.dots == nullptr || dots());
+    }
+    const bool weighted = w.weights != nullptr;
+    if (w.dots != nullptr && (SPREAD || w.k <= rs::kMaxBatch)) {
+        return with_batch(w.k, [&](auto batch) {
+            constexpr int B = decltype(batch)::value;
+            if (vecs <= 64) {
+                w.chunks = 1;
+                return weighted ? go(rs::wide_rows_kernel<T, 64, B, SPREAD, true, true>, w.tokens, rs::kRowBlock / 64)
+                                : go(rs::wide_rows_kernel<T, 64, B, SPREAD, false, true>, w.tokens, rs::kRowBlock / 64);
+            }
+            constexpr int L = rs::kRowBlock;
+            w.chunks = (vecs + L - 1) / L;
+            return weighted ? go(rs::wide_rows_kernel<T, L, B, SPREAD, true, true>, w.tokens, 1)
+                            : go(rs::wide_rows_kernel<T, L, B, SPREAD, false, true>, w.tokens, 1);
+        });
+    }
+    w.chunks = (vecs + 63) / 64;
+    const size_t units = w.tokens * static_cast<size_t>(w.chunks);
+    const auto plain = [&](auto batch) {
+        constexpr int B = decltype(batch)::value;
+        return weighted ? go(rs::wide_rows_kernel<T, 64, B, SPREAD, true, false>, units, rs::kRowBlock / 64)
+                        : go(rs::wide_rows_kernel<T, 64, B, SPREAD, false, false>, units, rs::kRowBlock / 64);
+    };
+    // A spread without dots loads no rows: its batch only unrolls the stores.
+    const bool ok = SPREAD ? plain(std::integral_constant<int, rs::kMaxBatch>{}) : with_batch(w.k, plain);
+    return ok && (w.dots == nullptr || dots());
 }
 
 bool launch_spread(int dtype, const void *x, size_t tokens, int width, size_t x_stride, const int32_t *position,
-                   const float *weights, int k, void *rows, size_t num_rows, size_t rows_stride, hipStream_t stream) {
-    if (tokens == 0 || num_rows == 0) return true;
+                   const float *weights, int k, void *rows, size_t num_rows, size_t rows_stride, const void *rows_in,
+                   size_t rows_in_stride, float *dots, hipStream_t stream) {
+    if (tokens == 0 || (num_rows == 0 && dots == nullptr)) return true;
     return with_dtype(dtype, [&](auto zero) {
         using T = decltype(zero);
-        const RowGrid g = row_grid(tokens, width, rs::kVec<T>);
-        const auto go = [&](auto kernel) {
-            return launch_kernel(RS_KERNEL_ROWS, stream, [&] {
-                run_kernel(kernel, g.grid, rs::kRowBlock, stream, static_cast<const T *>(x), tokens, width, x_stride,
-                           position, weights, k, static_cast<T *>(rows), num_rows, rows_stride, g.lanes, g.chunks);
-            });
-        };
-        return weights ? go(rs::spread_rows_kernel<T, true>) : go(rs::spread_rows_kernel<T, false>);
+        rs::RowWork<T> w{};
+        w.x = static_cast<const T *>(x), w.x_stride = x_stride;
+        w.rows_in = static_cast<const T *>(rows_in), w.rows_in_stride = rows_in_stride;
+        w.rows_out = static_cast<T *>(rows), w.rows_out_stride = rows_stride;
+        w.dots = dots, w.position = position, w.weights = weights;
+        w.tokens = tokens, w.num_rows = num_rows, w.width = width, w.k = k;
+        return launch_rows<true>(w, stream);
     });
 }
 
 bool launch_join(int dtype, const void *rows, size_t num_rows, size_t rows_stride, const int32_t *position,
-                 const float *weights, int k, void *out, size_t tokens, int width, size_t out_stride,
-                 hipStream_t stream) {
+                 const float *weights, int k, void *out, size_t tokens, int width, size_t out_stride, const void *x,
+                 size_t x_stride, float *dots, hipStream_t stream) {
     if (tokens == 0) return true;
     return with_dtype(dtype, [&](auto zero) {
         using T = decltype(zero);
-        const RowGrid g = row_grid(tokens, width, rs::kVec<T>);
-        const auto go = [&](auto kernel) {
-            return launch_kernel(RS_KERNEL_ROWS, stream, [&] {
-                run_kernel(kernel, g.grid, rs::kRowBlock, stream, static_cast<const T *>(rows), num_rows, rows_stride,
-                           position, weights, k, static_cast<T *>(out), tokens, width, out_stride, g.lanes, g.chunks);
-            });
-        };
-        return weights ? go(rs::join_rows_kernel<T, true>) : go(rs::join_rows_kernel<T, false>);
-    });
-}
-
-bool launch_dots(int dtype, const void *x, size_t tokens, int width, size_t x_stride, const void *rows,
-                 size_t num_rows, size_t rows_stride, const int32_t *position, int k, float *dots,
-                 hipStream_t stream) {
-    if (tokens == 0) return true;
-    return with_dtype(dtype, [&](auto zero) {
-        using T = decltype(zero);
-        const unsigned grid = grid_for(tokens * static_cast<size_t>(k), rs::kRowBlock / 64, kMaxGrid);
-        return launch_kernel(RS_KERNEL_ROWS, stream, [&] {
-            run_kernel(rs::dot_rows_kernel<T>, grid, rs::kRowBlock, stream, static_cast<const T *>(x), tokens, width,
-                       x_stride, static_cast<const T *>(rows), num_rows, rows_stride, position, k, dots);
-        });
+        rs::RowWork<T> w{};
+        w.x = static_cast<const T *>(x), w.x_stride = x_stride;
+        w.rows_in = static_cast<const T *>(rows), w.rows_in_stride = rows_stride;
+        w.out = static_cast<T *>(out), w.out_stride = out_stride;
+        w.dots = dots, w.position = position, w.weights = weights;
+        w.tokens = tokens, w.num_rows = num_rows, w.width = width, w.k = k;
+        return launch_rows<false>(w, stream);
     });
 }
 
@@ -328,9 +353,9 @@ rs_status rs_dispatch_rows(const void *x, int dtype, size_t tokens, int width, s
                           span_of(x, span_bytes(tokens, w, x_stride, elem)), span_of(position, slots * 4),
                           span_of(weights, weights ? slots * 4 : 0)};
     if (!disjoint(spans, 1, 4)) return RS_ERROR_INVALID_VALUE;
-    return launch_spread(dtype, x, tokens, width, x_stride, position, weights, k, rows, num_rows, rows_stride, stream)
-               ? RS_SUCCESS
-               : RS_ERROR_LAUNCH;
+    const bool ok = launch_spread(dtype, x, tokens, width, x_stride, position, weights, k, rows, num_rows, rows_stride,
+                                  nullptr, 0, nullptr, stream);
+    return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
 }
 
 rs_status rs_dispatch_rows_backward(const void *grad_rows, int dtype, size_t num_rows, size_t grad_rows_stride,
@@ -354,12 +379,8 @@ rs_status rs_dispatch_rows_backward(const void *grad_rows, int dtype, size_t num
                           span_of(position, slots * 4), span_of(weights, weights ? slots * 4 : 0),
                           span_of(x, dots ? span_bytes(tokens, w, x_stride, elem) : 0)};
     if (!disjoint(spans, 2, 6)) return RS_ERROR_INVALID_VALUE;
-    bool ok = launch_join(dtype, grad_rows, num_rows, grad_rows_stride, position, weights, k, grad_x, tokens, width,
-                          grad_x_stride, stream);
-    if (dots) {
-        ok = ok && launch_dots(dtype, x, tokens, width, x_stride, grad_rows, num_rows, grad_rows_stride, position, k,
-                               grad_weights, stream);
-    }
+    const bool ok = launch_join(dtype, grad_rows, num_rows, grad_rows_stride, position, weights, k, grad_x, tokens,
+                                width, grad_x_stride, x, x_stride, grad_weights, stream);
     return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
 }
 
@@ -391,12 +412,8 @@ rs_status rs_combine_rows_backward(const void *grad_out, int dtype, size_t token
                           span_of(position, slots * 4), span_of(weights, weights ? slots * 4 : 0),
                           span_of(rows, dots ? span_bytes(num_rows, w, rows_stride, elem) : 0)};
     if (!disjoint(spans, 2, 6)) return RS_ERROR_INVALID_VALUE;
-    bool ok = launch_spread(dtype, grad_out, tokens, width, grad_out_stride, position, weights, k, grad_rows, num_rows,
-                            grad_rows_stride, stream);
-    if (dots) {
-        ok = ok && launch_dots(dtype, grad_out, tokens, width, grad_out_stride, rows, num_rows, rows_stride, position,
-                               k, grad_weights, stream);
-    }
+    const bool ok = launch_spread(dtype, grad_out, tokens, width, grad_out_stride, position, weights, k, grad_rows,
+                                  num_rows, grad_rows_stride, rows, rows_stride, grad_weights, stream);
     return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
 }
 

@@ -9,6 +9,8 @@
 
 #include <type_traits>
 
+#include "device.hpp"
+
 namespace rs {
 
 // ---------------------------------------------------------------------------
@@ -434,122 +436,138 @@ __device__ __forceinline__ uint32_t expert_key(ID id, ID first, uint32_t experts
     return e < static_cast<U>(experts) ? static_cast<uint32_t>(e) : experts;
 }
 
-// Keys of each workgroup's chunk of slots, counted in LDS:
-// table[key][workgroup].
-template <class ID>
+// Row length of the count table: whole 16-byte accesses.
+constexpr uint32_t table_stride(uint32_t experts) { return (experts + 3u) & ~3u; }
+
+// Experts of each workgroup's chunk of slots, counted in LDS:
+// table[workgroup][expert].
+template <class ID, int ITEMS>
 __global__ __launch_bounds__(kPlaceBlock) void expert_count_kernel(const ID *__restrict__ ids, size_t n, ID first,
                                                                    uint32_t experts, size_t chunk,
                                                                    uint32_t *__restrict__ table) {
-    __shared__ uint32_t count[kMaxExperts + 1];
-    for (uint32_t e = threadIdx.x; e <= experts; e += kPlaceBlock) count[e] = 0;
-    __syncthreads();
+    __shared__ uint32_t count[kMaxExperts + 4];
+    const uint32_t stride = table_stride(experts);
     const size_t lo = blockIdx.x * chunk;
     const size_t hi = lo + chunk < n ? lo + chunk : n;
-    for (size_t i = lo + threadIdx.x; i < hi; i += kPlaceBlock) atomicAdd(&count[expert_key(ids[i], first, experts)], 1u);
+    for (uint32_t e = threadIdx.x; e < stride; e += kPlaceBlock) count[e] = 0;
     __syncthreads();
-    for (uint32_t e = threadIdx.x; e <= experts; e += kPlaceBlock) table[e * gridDim.x + blockIdx.x] = count[e];
+    for (size_t tile = lo + threadIdx.x; tile < hi; tile += static_cast<size_t>(kPlaceBlock) * ITEMS) {
+        uint32_t key[ITEMS];
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const size_t slot = tile + static_cast<size_t>(i) * kPlaceBlock;
+            key[i] = slot < hi ? expert_key(ids[slot], first, experts) : experts;
+        }
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            if (key[i] < experts) atomicAdd(&count[key[i]], 1u);
+        }
+    }
+    __syncthreads();
+    for (uint32_t e = threadIdx.x; e < stride; e += kPlaceBlock) {
+        table[static_cast<size_t>(blockIdx.x) * stride + e] = count[e];
+    }
 }
 
 // Places of a chunk of slots: order[place] = slot, position[slot] = place
 // (~place for a dropped slot).  A slot's place is
 //   (slots of smaller keys) + (slots of its key in earlier chunks, waves and
 //   rounds of its wave) + (lanes below it in its round with its key),
-// so equal keys keep slot order whatever the waves' timing.  The lanes of a
-// round that share a key find each other by one ballot per key bit.
-// Without a table the grid is one workgroup that holds every slot.
-template <class ID, int ITEMS, bool TABLE>
+// so equal keys keep slot order whatever the waves' timing.  KEY_BITS bits hold
+// every key (0 .. experts).
+// With a table every workgroup sums all of its rows (the totals) and those
+// above its own (the earlier chunks); without, the grid is one workgroup that
+// holds every slot.
+template <class ID, int ITEMS, bool TABLE, int KEY_BITS>
 __global__ __launch_bounds__(kPlaceBlock) void expert_place_kernel(const ID *__restrict__ ids, size_t n, ID first,
-                                                                   uint32_t experts, int key_bits, size_t chunk,
+                                                                   uint32_t experts, size_t chunk,
                                                                    const uint32_t *__restrict__ table,
                                                                    int32_t *__restrict__ order,
                                                                    int32_t *__restrict__ position,
                                                                    int32_t *__restrict__ offsets) {
-    __shared__ uint32_t count[kPlaceWaves * (kMaxExperts + 1)];
-    __shared__ uint32_t base[kMaxExperts + 1];    // first place of the chunk's slots of a key
-    __shared__ uint32_t wave_total[kPlaceWaves];
+    __shared__ __attribute__((aligned(16))) uint32_t count[kPlaceWaves * (kMaxExperts + 1)];
+    __shared__ uint32_t base[kMaxExperts + 1];  // place of the next slot of a key
+    __shared__ uint32_t wave_total[2][kPlaceWaves];
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     const uint32_t keys = experts + 1;
     constexpr size_t kTile = static_cast<size_t>(kPlaceBlock) * ITEMS;
     const size_t lo = blockIdx.x * chunk;
     const size_t hi = lo + chunk < n ? lo + chunk : n;
 
-    uint32_t total = 0, before = 0;  // of key threadIdx.x: all slots, slots of earlier chunks
+    uint32_t key[ITEMS], rank[ITEMS];
+    const auto load_keys = [&](size_t tile) {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const size_t slot = tile + (static_cast<size_t>(wave) * ITEMS + i) * 64 + lane;
+            key[i] = slot < hi ? expert_key(ids[slot], first, experts) : 0xFFFFFFFFu;
+        }
+    };
+    load_keys(lo);
+
+    uint32_t total = 0, before = 0;  // of expert threadIdx.x: all slots, slots of earlier chunks
     if constexpr (TABLE) {
-        // A wave sums a key's row of the table.
-        for (uint32_t e = wave; e < keys; e += kPlaceWaves) {
-            uint32_t all = 0, ahead = 0;
-            for (uint32_t b = lane; b < gridDim.x; b += 64) {
-                const uint32_t c = table[e * gridDim.x + b];
-                all += c;
-                ahead += b < blockIdx.x ? c : 0u;
-            }
-            all = group_sum_u32<64>(all);
-            ahead = group_sum_u32<64>(ahead);
-            if (lane == 0) {
-                count[e] = all;
-                base[e] = ahead;
+        // A thread sums four experts over every splits-th row; the partial
+        // sums meet in LDS.
+        const uint32_t stride = table_stride(experts);
+        uint32_t quads = 16;
+        while (quads * 4 < stride) quads *= 2;
+        const uint32_t splits = kPlaceBlock / quads;
+        const uint32_t quad = threadIdx.x % quads, split = threadIdx.x / quads;
+        uint4 all = make_uint4(0, 0, 0, 0), ahead = make_uint4(0, 0, 0, 0);
+        if (quad * 4 < stride) {
+#pragma unroll 8
+            for (uint32_t b = split; b < gridDim.x; b += splits) {
+                const uint4 c = *reinterpret_cast<const uint4 *>(table + static_cast<size_t>(b) * stride + quad * 4);
+                const uint32_t m = b < blockIdx.x ? 0xFFFFFFFFu : 0u;
+                all.x += c.x, all.y += c.y, all.z += c.z, all.w += c.w;
+                ahead.x += c.x & m, ahead.y += c.y & m, ahead.z += c.z & m, ahead.w += c.w & m;
             }
         }
+        uint4 *const sums = reinterpret_cast<uint4 *>(count);  // [2][splits][quads]
+        sums[threadIdx.x] = all;
+        sums[kPlaceBlock + threadIdx.x] = ahead;
         __syncthreads();
         if (threadIdx.x < experts) {
-            total = count[threadIdx.x];
-            before = base[threadIdx.x];
+            for (uint32_t i = 0; i < splits; ++i) {
+                total += count[i * quads * 4 + threadIdx.x];
+                before += count[kPlaceBlock * 4 + i * quads * 4 + threadIdx.x];
+            }
         }
         __syncthreads();
     }
 
-    for (size_t tile = lo; tile < hi || (!TABLE && tile == lo); tile += kTile) {
+    for (size_t tile = lo; tile == lo || tile < hi; tile += kTile) {
+        if (tile != lo) load_keys(tile);
         for (uint32_t i = threadIdx.x; i < kPlaceWaves * keys; i += kPlaceBlock) count[i] = 0;
         __syncthreads();
-        uint32_t key[ITEMS], rank[ITEMS];
-        const size_t mine = tile + static_cast<size_t>(wave) * 64 * ITEMS + lane;
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const size_t slot = mine + i * 64;
-            key[i] = slot < hi ? expert_key(ids[slot], first, experts) : 0xFFFFFFFFu;
-        }
         uint32_t *const own = count + wave * keys;
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const bool live = key[i] != 0xFFFFFFFFu;
-            uint64_t same = __ballot(live);
-            for (int bit = 0; bit < key_bits; ++bit) {
-                const bool one = (key[i] >> bit) & 1u;
-                const uint64_t ones = __ballot(one);
-                same &= one ? ones : ~ones;
-            }
-            const uint32_t below = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(same >> 32),
-                                                             __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(same), 0u));
-            uint32_t start = 0;
-            if (live && below == 0) start = atomicAdd(&own[key[i]], static_cast<uint32_t>(__popcll(same)));
-            const int leader = live ? __ffsll(static_cast<unsigned long long>(same)) - 1 : 0;
-            rank[i] = __shfl(start, leader) + below;
-        }
+        for (int i = 0; i < ITEMS; ++i) rank[i] = match_rank<KEY_BITS>(key[i], key[i] != 0xFFFFFFFFu, own, 1u);
         __syncthreads();
 
         if (tile == lo) {
-            // Bases: an exclusive scan of the keys' totals.
+            // Bases: an exclusive scan of the experts' totals.  The dropped
+            // slots of earlier chunks are what is left of those chunks.
             if constexpr (!TABLE) {
                 if (threadIdx.x < experts) {
                     for (int w = 0; w < kPlaceWaves; ++w) total += count[w * keys + threadIdx.x];
                 }
             }
-            uint32_t incl = threadIdx.x < experts ? total : 0u;
-            const uint32_t own_total = incl;
-            for (int d = 1; d < 64; d <<= 1) {
-                const uint32_t up = __shfl_up(incl, d);
-                if (lane >= d) incl += up;
+            const uint32_t incl = wave_inclusive_sum(total);
+            if (lane == 63) wave_total[0][wave] = incl;
+            if constexpr (TABLE) {
+                const uint32_t ahead = group_sum_u32<64>(before);
+                if (lane == 0) wave_total[1][wave] = ahead;
             }
-            if (lane == 63) wave_total[wave] = incl;
             __syncthreads();
-            uint32_t prior = 0, sum = 0;
-            for (int w = 0; w < kPlaceWaves; ++w) {
-                prior += w < wave ? wave_total[w] : 0u;
-                sum += wave_total[w];
-            }
-            const uint32_t start = prior + incl - own_total;
+            const uint32_t others = lane < kPlaceWaves ? wave_total[0][lane] : 0u;
+            const uint32_t prior = group_sum_u32<64>(lane < wave ? others : 0u);
+            const uint32_t sum = group_sum_u32<64>(others);
+            uint32_t ahead = 0;
+            if constexpr (TABLE) ahead = group_sum_u32<64>(lane < kPlaceWaves ? wave_total[1][lane] : 0u);
+            const uint32_t start = prior + incl - total;
             if (threadIdx.x < experts) base[threadIdx.x] = start + before;
-            if (threadIdx.x == 0) base[experts] = sum + (TABLE ? base[experts] : 0u);
+            if (threadIdx.x == 0) base[experts] = sum + static_cast<uint32_t>(lo) - ahead;
             if (blockIdx.x == 0) {
                 if (threadIdx.x < experts) offsets[threadIdx.x] = static_cast<int32_t>(start);
                 if (threadIdx.x == 0) offsets[experts] = static_cast<int32_t>(sum);
@@ -558,18 +576,20 @@ __global__ __launch_bounds__(kPlaceBlock) void expert_place_kernel(const ID *__r
         }
         // Each wave's first place per key; the next tile starts behind the last.
         for (uint32_t e = threadIdx.x; e < keys; e += kPlaceBlock) {
-            uint32_t run = base[e];
+            uint32_t run = base[e], c[kPlaceWaves];
+#pragma unroll
+            for (int w = 0; w < kPlaceWaves; ++w) c[w] = count[w * keys + e];
+#pragma unroll
             for (int w = 0; w < kPlaceWaves; ++w) {
-                const uint32_t c = count[w * keys + e];
                 count[w * keys + e] = run;
-                run += c;
+                run += c[w];
             }
             base[e] = run;
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            const size_t slot = mine + i * 64;
+            const size_t slot = tile + (static_cast<size_t>(wave) * ITEMS + i) * 64 + lane;
             if (slot < hi) {
                 const uint32_t place = own[key[i]] + rank[i];
                 order[place] = static_cast<int32_t>(slot);
@@ -598,100 +618,228 @@ __device__ __forceinline__ Slot slot_of(int32_t position, size_t num_rows) {
     return {place < num_rows ? static_cast<int64_t>(place) : int64_t{-1}, used};
 }
 
-// rows[place of slot (t, j)] = w[t, j] * x[t]; zeros for a dropped slot.
-// A group of `lanes` threads takes a 16-byte column of a token and writes it
-// k times: x is read once.
-template <class T, bool WEIGHTED>
-__global__ __launch_bounds__(kRowBlock) void spread_rows_kernel(const T *__restrict__ x, size_t tokens, int width,
-                                                                size_t x_stride, const int32_t *__restrict__ position,
-                                                                const float *__restrict__ weights, int k,
-                                                                T *__restrict__ rows, size_t num_rows,
-                                                                size_t rows_stride, int lanes, int chunks) {
-    constexpr int W = kVec<T>;
-    const int per_block = kRowBlock / lanes;
-    const size_t units = tokens * static_cast<size_t>(chunks);
-    for (size_t u = static_cast<size_t>(blockIdx.x) * per_block + threadIdx.x / lanes; u < units;
-         u += static_cast<size_t>(gridDim.x) * per_block) {
-        const size_t t = u / chunks;
-        const int col = (static_cast<int>(u % chunks) * lanes + static_cast<int>(threadIdx.x % lanes)) * W;
-        const int have = width - col;
-        if (have <= 0) continue;
-        float f[W];
-        load_some<T, W>(x + t * x_stride + col, have, f);
-        for (int j = 0; j < k; ++j) {
-            const size_t s = t * static_cast<size_t>(k) + j;
-            const Slot slot = slot_of(position[s], num_rows);
-            if (slot.row < 0) continue;
-            float v[W];
-            const float w = WEIGHTED ? weights[s] : 1.0f;
-#pragma unroll
-            for (int i = 0; i < W; ++i) v[i] = slot.used ? (WEIGHTED ? w * f[i] : f[i]) : 0.0f;
-            store_some<T, W>(rows + static_cast<size_t>(slot.row) * rows_stride + col, have, v);
-        }
-    }
-}
-
-// out[t] = sum over the used slots j of w[t, j] * rows[place of (t, j)], in
-// float, in the order of j.
-template <class T, bool WEIGHTED>
-__global__ __launch_bounds__(kRowBlock) void join_rows_kernel(const T *__restrict__ rows, size_t num_rows,
-                                                              size_t rows_stride, const int32_t *__restrict__ position,
-                                                              const float *__restrict__ weights, int k,
-                                                              T *__restrict__ out, size_t tokens, int width,
-                                                              size_t out_stride, int lanes, int chunks) {
-    constexpr int W = kVec<T>;
-    const int per_block = kRowBlock / lanes;
-    const size_t units = tokens * static_cast<size_t>(chunks);
-    for (size_t u = static_cast<size_t>(blockIdx.x) * per_block + threadIdx.x / lanes; u < units;
-         u += static_cast<size_t>(gridDim.x) * per_block) {
-        const size_t t = u / chunks;
-        const int col = (static_cast<int>(u % chunks) * lanes + static_cast<int>(threadIdx.x % lanes)) * W;
-        const int have = width - col;
-        if (have <= 0) continue;
-        float acc[W] = {};
-        for (int j = 0; j < k; ++j) {
-            const size_t s = t * static_cast<size_t>(k) + j;
-            const Slot slot = slot_of(position[s], num_rows);
-            if (slot.row < 0 || !slot.used) continue;
-            float f[W];
-            load_some<T, W>(rows + static_cast<size_t>(slot.row) * rows_stride + col, have, f);
-            const float w = WEIGHTED ? weights[s] : 1.0f;
-#pragma unroll
-            for (int i = 0; i < W; ++i) acc[i] = WEIGHTED ? __builtin_fmaf(w, f[i], acc[i]) : acc[i] + f[i];
-        }
-        store_some<T, W>(out + t * out_stride + col, have, acc);
-    }
-}
-
-// dots[t, j] = <x[t], rows[place of (t, j)]> in float, 0 for a dropped slot.
-// A wave takes a slot.
+// What a row kernel works on.  Spread: rows_out[place of slot (t, j)] =
+// w[t, j] * x[t], zeros for a dropped slot.  Join: out[t] = sum over the used
+// slots j of w[t, j] * rows_in[place of (t, j)], in float, in the order of j.
+// Dots: dots[t, j] = <x[t], rows_in[place of (t, j)]> in float, 0 for a
+// dropped slot.
 template <class T>
-__global__ __launch_bounds__(kRowBlock) void dot_rows_kernel(const T *__restrict__ x, size_t tokens, int width,
-                                                             size_t x_stride, const T *__restrict__ rows,
-                                                             size_t num_rows, size_t rows_stride,
-                                                             const int32_t *__restrict__ position, int k,
-                                                             float *__restrict__ dots) {
+struct RowWork {
+    const T *x;
+    size_t x_stride;
+    const T *rows_in;
+    size_t rows_in_stride;
+    T *rows_out;
+    size_t rows_out_stride;
+    T *out;
+    size_t out_stride;
+    float *dots;
+    const int32_t *position;
+    const float *weights;
+    size_t tokens;
+    size_t num_rows;
+    int width;
+    int k;
+    int lanes;   // narrow rows: threads of a row
+    int chunks;  // wide rows: rounds of the lanes that cover a row
+};
+
+constexpr int kMaxBatch = 8;  // slots of a token whose rows are in flight together
+
+// Rows of more than kNarrow 16-byte accesses.  LANES threads hold 16-byte
+// columns of a token's row: they read x once and write it k times, or read k
+// rows (BATCH of them in flight) and write their sum once.  A token is the
+// same for a whole wave: its places and weights are scalars.
+// Without dots a wave takes one chunk of 64 columns of a token.  With dots the
+// LANES threads take the whole row, chunk after chunk, since their products
+// meet at the end; a join with dots holds one batch (k <= BATCH).
+// The loads of a batch are issued without a branch between them, which would
+// wait for the one before: an unused slot reads a used one's row.
+// The last access of a row is moved back to end with it where the width is no
+// multiple of the access: its first elements are computed twice, to the same
+// result, and counted once in the products.
+constexpr int kNarrow = 32;
+
+template <class T, int LANES, int BATCH, bool SPREAD, bool WEIGHTED, bool DOTS>
+__global__ __launch_bounds__(kRowBlock) void wide_rows_kernel(const RowWork<T> a) {
     constexpr int W = kVec<T>;
-    const int lane = threadIdx.x % 64;
-    const size_t slots = tokens * static_cast<size_t>(k);
+    using Vec = typename VecOf<T, W>::type;
+    constexpr int kPer = kRowBlock / LANES;
+    constexpr int kWaves = LANES / 64;
+    static_assert(LANES == 64 || (DOTS && LANES == kRowBlock));
+    __shared__ float partial[kWaves > 1 ? BATCH : 1][kWaves > 1 ? kWaves : 1];
+    const int lane = threadIdx.x % LANES;
+    const int group = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / LANES);
+    const size_t units = DOTS ? a.tokens : a.tokens * static_cast<size_t>(a.chunks);
+    const int vecs = (a.width + W - 1) / W;
+    for (size_t u = static_cast<size_t>(blockIdx.x) * kPer + group; u < units;
+         u += static_cast<size_t>(gridDim.x) * kPer) {
+        const size_t t = DOTS ? u : u / static_cast<unsigned>(a.chunks);
+        const int first = DOTS ? 0 : static_cast<int>(u % static_cast<unsigned>(a.chunks));
+        float acc[W] = {};
+        for (int j0 = 0; j0 < a.k; j0 += BATCH) {
+            // Lane i of each wave loads slot j0 + i; the wave reads them as scalars.
+            const int mine = j0 + static_cast<int>(threadIdx.x % 64);
+            const size_t at = t * static_cast<size_t>(a.k) + (mine < a.k ? mine : a.k - 1);
+            int32_t my_place = a.position[at];
+            float my_weight = WEIGHTED ? a.weights[at] : 1.0f;
+            asm volatile("" : "+v"(my_place), "+v"(my_weight));  // one wait for both loads
+            Slot slot[BATCH];
+            float w[BATCH];
+            int64_t some = -1;  // the row of a used slot
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                slot[i] = slot_of(__builtin_amdgcn_readlane(my_place, i), a.num_rows);
+                w[i] = __uint_as_float(lane_value(__float_as_uint(my_weight), i));
+                if (j0 + i >= a.k) slot[i].row = -1;
+                slot[i].used = slot[i].used & (slot[i].row >= 0);
+                some = slot[i].used ? slot[i].row : some;
+            }
+            float dot[BATCH] = {};
+            for (int c = first; c < (DOTS ? a.chunks : first + 1); ++c) {
+                const int vec = c * LANES + lane;
+                if (vec < vecs) {
+                    const int begin = vec * W;
+                    const int col = begin + W <= a.width ? begin : a.width - W;
+                    Vec raw[BATCH];
+                    if constexpr (!SPREAD || DOTS) {
+                        if (some >= 0) {
+#pragma unroll
+                            for (int i = 0; i < BATCH; ++i) {
+                                const auto row = static_cast<size_t>(slot[i].used ? slot[i].row : some);
+                                raw[i] = *reinterpret_cast<const Vec *>(a.rows_in + row * a.rows_in_stride + col);
+                            }
+                        }
+                    }
+                    float x[W];
+                    if constexpr (SPREAD || DOTS) load_vec<T, W>(a.x + t * a.x_stride + col, x);
+                    if constexpr (SPREAD) {
+#pragma unroll
+                        for (int i = 0; i < BATCH; ++i) {
+                            if (slot[i].row < 0) continue;
+                            float v[W];
+#pragma unroll
+                            for (int e = 0; e < W; ++e) v[e] = !slot[i].used ? 0.0f : WEIGHTED ? w[i] * x[e] : x[e];
+                            store_vec<T, W>(a.rows_out + static_cast<size_t>(slot[i].row) * a.rows_out_stride + col, v);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) {
+                        if ((SPREAD && !DOTS) || !slot[i].used) continue;
+                        float f[W];
+#pragma unroll
+                        for (int e = 0; e < W; ++e) f[e] = static_cast<float>(raw[i][e]);
+                        if constexpr (!SPREAD) {
+#pragma unroll
+                            for (int e = 0; e < W; ++e) {
+                                acc[e] = WEIGHTED ? __builtin_fmaf(w[i], f[e], acc[e]) : acc[e] + f[e];
+                            }
+                        }
+                        if constexpr (DOTS) {
+                            if (col == begin) {
+#pragma unroll
+                                for (int e = 0; e < W; ++e) dot[i] = __builtin_fmaf(x[e], f[e], dot[i]);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < W; ++e) {
+                                    if (col + e >= begin) dot[i] = __builtin_fmaf(x[e], f[e], dot[i]);
+                                }
+                            }
+                        }
+                    }
+                    if constexpr (!SPREAD) {
+                        if (DOTS || j0 + BATCH >= a.k) {
+                            store_vec<T, W>(a.out + t * a.out_stride + col, acc);
+#pragma unroll
+                            for (int e = 0; e < W; ++e) acc[e] = 0.0f;
+                        }
+                    }
+                }
+            }
+            if constexpr (DOTS) {
+                float total = 0.0f;
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const float sum = group_sum<64>(dot[i]);
+                    if constexpr (kWaves > 1) {
+                        if (lane % 64 == i) partial[i][lane / 64] = sum;
+                    } else {
+                        total = lane == i ? sum : total;
+                    }
+                }
+                if constexpr (kWaves > 1) {
+                    __syncthreads();
+                    if (lane < BATCH) {
+#pragma unroll
+                        for (int i = 0; i < kWaves; ++i) total += partial[lane][i];
+                    }
+                }
+                // An unused slot's sum is 0: nothing was added to it.
+                if (lane < BATCH && j0 + lane < a.k) a.dots[t * static_cast<size_t>(a.k) + j0 + lane] = total;
+                if constexpr (kWaves > 1) __syncthreads();
+            }
+        }
+    }
+}
+
+// Rows of at most kNarrow 16-byte accesses: a.lanes threads (a power of two)
+// take a token's row, an access each.
+template <class T, bool SPREAD, bool WEIGHTED>
+__global__ __launch_bounds__(kRowBlock) void narrow_rows_kernel(const RowWork<T> a) {
+    constexpr int W = kVec<T>;
+    const int per_block = kRowBlock / a.lanes;
+    const int col = static_cast<int>(threadIdx.x % a.lanes) * W;
+    const int have = a.width - col;
+    if (have <= 0) return;
+    for (size_t t = static_cast<size_t>(blockIdx.x) * per_block + threadIdx.x / a.lanes; t < a.tokens;
+         t += static_cast<size_t>(gridDim.x) * per_block) {
+        float f[W], acc[W] = {};
+        if constexpr (SPREAD) load_some<T, W>(a.x + t * a.x_stride + col, have, f);
+        for (int j = 0; j < a.k; ++j) {
+            const size_t s = t * static_cast<size_t>(a.k) + j;
+            const Slot slot = slot_of(a.position[s], a.num_rows);
+            if (slot.row < 0 || (!SPREAD && !slot.used)) continue;
+            const float w = WEIGHTED ? a.weights[s] : 1.0f;
+            if constexpr (SPREAD) {
+                float v[W];
+#pragma unroll
+                for (int i = 0; i < W; ++i) v[i] = !slot.used ? 0.0f : WEIGHTED ? w * f[i] : f[i];
+                store_some<T, W>(a.rows_out + static_cast<size_t>(slot.row) * a.rows_out_stride + col, have, v);
+            } else {
+                load_some<T, W>(a.rows_in + static_cast<size_t>(slot.row) * a.rows_in_stride + col, have, f);
+#pragma unroll
+                for (int i = 0; i < W; ++i) acc[i] = WEIGHTED ? __builtin_fmaf(w, f[i], acc[i]) : acc[i] + f[i];
+            }
+        }
+        if constexpr (!SPREAD) store_some<T, W>(a.out + t * a.out_stride + col, have, acc);
+    }
+}
+
+// Dots alone, for the shapes that the kernel above does not join with them:
+// narrow rows, and joins of more than a batch.  A wave takes a slot.
+template <class T>
+__global__ __launch_bounds__(kRowBlock) void dot_rows_kernel(const RowWork<T> a) {
+    constexpr int W = kVec<T>;
     constexpr int kWaves = kRowBlock / 64;
+    const int lane = threadIdx.x % 64;
+    const size_t slots = a.tokens * static_cast<size_t>(a.k);
     for (size_t s = static_cast<size_t>(blockIdx.x) * kWaves + threadIdx.x / 64; s < slots;
          s += static_cast<size_t>(gridDim.x) * kWaves) {
-        const Slot slot = slot_of(position[s], num_rows);
+        const Slot slot = slot_of(a.position[s], a.num_rows);
         float acc = 0.0f;
         if (slot.row >= 0 && slot.used) {
-            const T *a = x + (s / k) * x_stride;
-            const T *b = rows + static_cast<size_t>(slot.row) * rows_stride;
-            for (int col = lane * W; col < width; col += 64 * W) {
+            const T *x = a.x + (s / a.k) * a.x_stride;
+            const T *row = a.rows_in + static_cast<size_t>(slot.row) * a.rows_in_stride;
+            for (int col = lane * W; col < a.width; col += 64 * W) {
                 float f[W], h[W];
-                load_some<T, W>(a + col, width - col, f);
-                load_some<T, W>(b + col, width - col, h);
+                load_some<T, W>(x + col, a.width - col, f);
+                load_some<T, W>(row + col, a.width - col, h);
 #pragma unroll
                 for (int i = 0; i < W; ++i) acc = __builtin_fmaf(f[i], h[i], acc);
             }
         }
         acc = group_sum<64>(acc);
-        if (lane == 0) dots[s] = acc;
+        if (lane == 0) a.dots[s] = acc;
     }
 }
 
