@@ -91,13 +91,20 @@ bool good_route(int dtype, size_t tokens, int experts, int k, int gate) {
 // ---------------------------------------------------------------------------
 // Slots sorted by expert
 // ---------------------------------------------------------------------------
-// Up to kOneGroup slots one workgroup places them all.  Above, the slots are
-// cut into at most kMaxChunks chunks of whole tiles, counted by one launch and
-// placed by a second.
+// Up to kOneGroup slots one workgroup places them all: 8192 slots of 256
+// experts take it 6 us, the two launches below 8.4; 12000 slots would take 8.7
+// (16 slots a thread) against 8.5.  Above, the slots are cut into at most
+// kMaxChunks chunks of whole tiles (one per CU), counted by one launch and
+// placed by another, which sums the table of counts itself while that has at
+// most kSumWords words, since every workgroup reads it: 2^18 slots of 256
+// experts (64 KiB) 10.5 us against 12.1 with a launch that scans it between
+// the two, 2^20 slots of 128 experts (128 KiB) 13.7 against 14.4, but of 256
+// experts (256 KiB) 16.8 against 15.3.
 constexpr size_t kOneGroup = 8 * rs::kPlaceBlock;
 constexpr int kTileItems = 4;
 constexpr size_t kTile = size_t{kTileItems} * rs::kPlaceBlock;
 constexpr size_t kMaxChunks = 256;
+constexpr size_t kSumWords = 32768;
 
 struct ExpertPlan {
     size_t chunk = 0;
@@ -115,7 +122,8 @@ ExpertPlan expert_plan(size_t n) {
 
 size_t expert_temp(size_t n, int experts) {
     if (n <= kOneGroup) return 0;
-    const size_t bytes = size_t{expert_plan(n).chunks} * rs::table_stride(static_cast<uint32_t>(experts)) * 4;
+    // The table, and a row of totals.
+    const size_t bytes = (size_t{expert_plan(n).chunks} + 1) * rs::table_stride(static_cast<uint32_t>(experts)) * 4;
     return (bytes + kTempAlign - 1) / kTempAlign * kTempAlign;
 }
 
@@ -144,25 +152,32 @@ rs_status sort_experts(const ID *ids, size_t n, int first, int experts, int32_t 
     const auto f = static_cast<ID>(first);
     auto *table = static_cast<uint32_t *>(temp);
     const ExpertPlan p = expert_plan(n);
-    const auto place = [&](auto kernel, unsigned grid, size_t chunk, const uint32_t *counts) {
+    uint32_t *totals = table + size_t{p.chunks} * rs::table_stride(e);
+    const auto place = [&](auto kernel, unsigned grid, size_t chunk) {
         return launch_kernel(RS_KERNEL_EXPERT, stream, [&] {
-            run_kernel(kernel, grid, rs::kPlaceBlock, stream, ids, n, f, e, chunk, counts, order, position, offsets);
+            run_kernel(kernel, grid, rs::kPlaceBlock, stream, ids, n, f, e, chunk, table, totals, order, position,
+                       offsets);
         });
     };
-    const auto run = [&](auto bits) {
-        constexpr int kBits = decltype(bits)::value;
-        if (n <= rs::kPlaceBlock) return place(rs::expert_place_kernel<ID, 1, false, kBits>, 1, n, nullptr);
-        if (n <= kOneGroup) return place(rs::expert_place_kernel<ID, 8, false, kBits>, 1, n, nullptr);
-        const bool ok = launch_kernel(RS_KERNEL_EXPERT, stream, [&] {
+    const auto run = [&](auto keys) {
+        constexpr int kKeys = decltype(keys)::value;
+        if (n <= rs::kPlaceBlock) return place(rs::expert_place_kernel<ID, 1, kKeys, rs::kNoTable>, 1, n);
+        if (n <= 4 * rs::kPlaceBlock) return place(rs::expert_place_kernel<ID, 4, kKeys, rs::kNoTable>, 1, n);
+        if (n <= kOneGroup) return place(rs::expert_place_kernel<ID, 8, kKeys, rs::kNoTable>, 1, n);
+        bool ok = launch_kernel(RS_KERNEL_EXPERT, stream, [&] {
             run_kernel(rs::expert_count_kernel<ID, kTileItems>, p.chunks, rs::kPlaceBlock, stream, ids, n, f, e, p.chunk,
                        table);
         });
-        return ok && place(rs::expert_place_kernel<ID, kTileItems, true, kBits>, p.chunks, p.chunk, table);
+        if (p.chunks * size_t{rs::table_stride(e)} <= kSumWords) {
+            return ok && place(rs::expert_place_kernel<ID, kTileItems, kKeys, rs::kCounts>, p.chunks, p.chunk);
+        }
+        ok = ok && launch_kernel(RS_KERNEL_EXPERT, stream, [&] {
+            const unsigned grid = grid_for(rs::table_stride(e), 4 * rs::kScanQuads, kMaxGrid);
+            run_kernel(rs::expert_scan_kernel, grid, rs::kPlaceBlock, stream, table, p.chunks, e, totals);
+        });
+        return ok && place(rs::expert_place_kernel<ID, kTileItems, kKeys, rs::kScanned>, p.chunks, p.chunk);
     };
-    // Keys 0 .. experts in as few ballots as these cover.
-    const bool ok = experts < 128   ? run(std::integral_constant<int, 7>{})
-                    : experts < 512 ? run(std::integral_constant<int, 9>{})
-                                    : run(std::integral_constant<int, 11>{});
+    const bool ok = experts <= 256 ? run(std::integral_constant<int, 256>{}) : run(std::integral_constant<int, 1024>{});
     return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
 }
 

@@ -469,131 +469,225 @@ __global__ __launch_bounds__(kPlaceBlock) void expert_count_kernel(const ID *__r
     }
 }
 
+// Exclusive sums of each expert's column of the table, in place, and the
+// columns' totals.  A workgroup takes 64 columns; a thread four of them over
+// consecutive rows, 64 threads per column.
+constexpr int kScanQuads = 16;
+constexpr int kScanSplits = kPlaceBlock / kScanQuads;
+
+__global__ __launch_bounds__(kPlaceBlock) void expert_scan_kernel(uint32_t *__restrict__ table, uint32_t chunks,
+                                                                  uint32_t experts, uint32_t *__restrict__ totals) {
+    __shared__ uint4 sums[kScanSplits][kScanQuads];
+    const uint32_t stride = table_stride(experts) / 4;
+    const uint32_t q = threadIdx.x % kScanQuads, split = threadIdx.x / kScanQuads;
+    const uint32_t quad = blockIdx.x * kScanQuads + q;
+    const uint32_t rows = (chunks + kScanSplits - 1) / kScanSplits;
+    const uint32_t lo = split * rows, hi = lo + rows < chunks ? lo + rows : chunks;
+    uint4 *const column = reinterpret_cast<uint4 *>(table) + quad;
+    const bool mine = quad < stride;
+    const auto add = [](uint4 &a, const uint4 &b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; };
+    constexpr int kHold = 4;  // rows kept in registers between the two passes
+    uint4 held[kHold], sum = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+        held[i] = mine && lo + i < hi ? column[static_cast<size_t>(lo + i) * stride] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) add(sum, held[i]);
+    if (mine) {
+        for (uint32_t b = lo + kHold; b < hi; ++b) add(sum, column[static_cast<size_t>(b) * stride]);
+    }
+    sums[split][q] = sum;
+    __syncthreads();
+    uint4 run = make_uint4(0, 0, 0, 0);
+    for (uint32_t i = 0; i < split; ++i) add(run, sums[i][q]);
+    if (!mine) return;
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+        if (lo + i < hi) column[static_cast<size_t>(lo + i) * stride] = run;
+        add(run, held[i]);
+    }
+    for (uint32_t b = lo + kHold; b < hi; ++b) {
+        const uint4 c = column[static_cast<size_t>(b) * stride];
+        column[static_cast<size_t>(b) * stride] = run;
+        add(run, c);
+    }
+    if (split == kScanSplits - 1) reinterpret_cast<uint4 *>(totals)[quad] = run;
+}
+
 // Places of a chunk of slots: order[place] = slot, position[slot] = place
 // (~place for a dropped slot).  A slot's place is
 //   (slots of smaller keys) + (slots of its key in earlier chunks, waves and
 //   rounds of its wave) + (lanes below it in its round with its key),
-// so equal keys keep slot order whatever the waves' timing.  KEY_BITS bits hold
-// every key (0 .. experts).
-// With a table every workgroup sums all of its rows (the totals) and those
-// above its own (the earlier chunks); without, the grid is one workgroup that
-// holds every slot.
-template <class ID, int ITEMS, bool TABLE, int KEY_BITS>
+// so equal keys keep slot order whatever the waves' timing.  The last two terms
+// are what an LDS add to the wave's counter of the key returns: like the pass
+// kernel's local rank, this takes the lanes' same-address adds to be served
+// in lane order, which the lane order test pins.  Dropped slots, often a long
+// run of padding, are ranked by a ballot instead of 64 adds to one address.
+// A tile's slots are put in key order in LDS, so that order is written in
+// runs.  KEYS >= experts sizes the LDS.
+enum : int {
+    kNoTable = 0,  // one workgroup that holds every slot in one tile
+    kCounts = 1,   // every chunk's counts are in the table: each workgroup sums them
+    kScanned = 2,  // the table's columns are scanned, their totals beside it
+};
+
+template <class ID, int ITEMS, int KEYS, int TABLE>
 __global__ __launch_bounds__(kPlaceBlock) void expert_place_kernel(const ID *__restrict__ ids, size_t n, ID first,
                                                                    uint32_t experts, size_t chunk,
                                                                    const uint32_t *__restrict__ table,
+                                                                   const uint32_t *__restrict__ totals,
                                                                    int32_t *__restrict__ order,
                                                                    int32_t *__restrict__ position,
                                                                    int32_t *__restrict__ offsets) {
-    __shared__ __attribute__((aligned(16))) uint32_t count[kPlaceWaves * (kMaxExperts + 1)];
-    __shared__ uint32_t base[kMaxExperts + 1];  // place of the next slot of a key
+    constexpr uint32_t kTile = kPlaceBlock * ITEMS;
+    static_assert(kTile <= 0x10000 && KEYS <= kPlaceBlock);
+    __shared__ uint32_t count[kPlaceWaves * (KEYS + 1)];  // [wave][key]
+    __shared__ uint32_t base[KEYS + 1];                   // place of the next slot of a key
+    __shared__ uint32_t delta[KEYS + 1];                  // a slot's place less its place in the tile
+    __shared__ __attribute__((aligned(16))) uint32_t sorted[kTile];  // the tile in key order: slot in tile | key << 16
     __shared__ uint32_t wave_total[2][kPlaceWaves];
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const uint32_t tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
     const uint32_t keys = experts + 1;
-    constexpr size_t kTile = static_cast<size_t>(kPlaceBlock) * ITEMS;
     const size_t lo = blockIdx.x * chunk;
     const size_t hi = lo + chunk < n ? lo + chunk : n;
 
     uint32_t key[ITEMS], rank[ITEMS];
+    const uint32_t mine = wave * 64 * ITEMS + lane;  // the thread's first slot in a tile
     const auto load_keys = [&](size_t tile) {
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            const size_t slot = tile + (static_cast<size_t>(wave) * ITEMS + i) * 64 + lane;
+            const size_t slot = tile + mine + i * 64;
             key[i] = slot < hi ? expert_key(ids[slot], first, experts) : 0xFFFFFFFFu;
         }
     };
+    // The workgroup's sum of x below this thread, and all of it.
+    const auto scan = [&](uint32_t x, uint32_t *wave_sum, uint32_t &all) {
+        const uint32_t incl = wave_inclusive_sum(x);
+        if (lane == 63) wave_sum[wave] = incl;
+        __syncthreads();
+        const uint32_t others = lane < kPlaceWaves ? wave_sum[lane] : 0u;
+        all = group_sum_u32<64>(others);
+        return group_sum_u32<64>(lane < wave ? others : 0u) + incl - x;
+    };
     load_keys(lo);
-
-    uint32_t total = 0, before = 0;  // of expert threadIdx.x: all slots, slots of earlier chunks
-    if constexpr (TABLE) {
-        // A thread sums four experts over every splits-th row; the partial
+    uint32_t total = 0, before = 0;  // of expert tid: all slots, slots of earlier chunks
+    if constexpr (TABLE == kCounts) {
+        // A thread sums four experts over every splits-th row; the threads'
         // sums meet in LDS.
+        static_assert(kTile >= 4 * kPlaceBlock || TABLE != kCounts);
         const uint32_t stride = table_stride(experts);
         uint32_t quads = 16;
         while (quads * 4 < stride) quads *= 2;
-        const uint32_t splits = kPlaceBlock / quads;
-        const uint32_t quad = threadIdx.x % quads, split = threadIdx.x / quads;
+        const uint32_t splits = kPlaceBlock / quads, quad = tid % quads, split = tid / quads;
         uint4 all = make_uint4(0, 0, 0, 0), ahead = make_uint4(0, 0, 0, 0);
         if (quad * 4 < stride) {
 #pragma unroll 8
             for (uint32_t b = split; b < gridDim.x; b += splits) {
-                const uint4 c = *reinterpret_cast<const uint4 *>(table + static_cast<size_t>(b) * stride + quad * 4);
+                const uint4 c = reinterpret_cast<const uint4 *>(table)[static_cast<size_t>(b) * (stride / 4) + quad];
                 const uint32_t m = b < blockIdx.x ? 0xFFFFFFFFu : 0u;
                 all.x += c.x, all.y += c.y, all.z += c.z, all.w += c.w;
                 ahead.x += c.x & m, ahead.y += c.y & m, ahead.z += c.z & m, ahead.w += c.w & m;
             }
         }
-        uint4 *const sums = reinterpret_cast<uint4 *>(count);  // [2][splits][quads]
-        sums[threadIdx.x] = all;
-        sums[kPlaceBlock + threadIdx.x] = ahead;
-        __syncthreads();
-        if (threadIdx.x < experts) {
-            for (uint32_t i = 0; i < splits; ++i) {
-                total += count[i * quads * 4 + threadIdx.x];
-                before += count[kPlaceBlock * 4 + i * quads * 4 + threadIdx.x];
+        const auto meet = [&](const uint4 &part) {
+            uint4 *const parts = reinterpret_cast<uint4 *>(sorted);
+            parts[tid] = part;
+            __syncthreads();
+            uint32_t sum = 0;
+            if (tid < experts) {
+#pragma unroll 8
+                for (uint32_t i = 0; i < splits; ++i) sum += sorted[i * quads * 4 + tid];
             }
-        }
-        __syncthreads();
+            __syncthreads();
+            return sum;
+        };
+        total = meet(all);
+        before = meet(ahead);
+    }
+    if (TABLE == kScanned && tid < experts) {
+        total = totals[tid];
+        before = table[blockIdx.x * static_cast<size_t>(table_stride(experts)) + tid];
     }
 
     for (size_t tile = lo; tile == lo || tile < hi; tile += kTile) {
-        if (tile != lo) load_keys(tile);
-        for (uint32_t i = threadIdx.x; i < kPlaceWaves * keys; i += kPlaceBlock) count[i] = 0;
+        for (uint32_t i = tid; i < kPlaceWaves * keys; i += kPlaceBlock) count[i] = 0;
         __syncthreads();
         uint32_t *const own = count + wave * keys;
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) rank[i] = match_rank<KEY_BITS>(key[i], key[i] != 0xFFFFFFFFu, own, 1u);
-        __syncthreads();
-
-        if (tile == lo) {
-            // Bases: an exclusive scan of the experts' totals.  The dropped
-            // slots of earlier chunks are what is left of those chunks.
-            if constexpr (!TABLE) {
-                if (threadIdx.x < experts) {
-                    for (int w = 0; w < kPlaceWaves; ++w) total += count[w * keys + threadIdx.x];
+        for (int i = 0; i < ITEMS; ++i) {
+            if (key[i] < experts) rank[i] = atomicAdd(&own[key[i]], 1u);
+            const uint64_t dropped = __ballot(key[i] == experts);
+            if (dropped != 0) {
+                uint32_t start = 0;
+                if (lane == 0) start = atomicAdd(&own[experts], static_cast<uint32_t>(__popcll(dropped)));
+                start = lane_value(start, 0);
+                if (key[i] == experts) {
+                    rank[i] = __builtin_amdgcn_mbcnt_hi(
+                        static_cast<uint32_t>(dropped >> 32),
+                        __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(dropped), start));
                 }
             }
-            const uint32_t incl = wave_inclusive_sum(total);
-            if (lane == 63) wave_total[0][wave] = incl;
-            if constexpr (TABLE) {
-                const uint32_t ahead = group_sum_u32<64>(before);
-                if (lane == 0) wave_total[1][wave] = ahead;
+        }
+        __syncthreads();
+
+        // Where each key starts in the tile: an exclusive scan of its counts.
+        uint32_t in_tile = 0, used_in_tile;
+        if (tid < experts) {
+#pragma unroll
+            for (uint32_t w = 0; w < kPlaceWaves; ++w) in_tile += count[w * keys + tid];
+        }
+        const uint32_t local = scan(in_tile, wave_total[0], used_in_tile);
+        if (tile == lo) {
+            // And in the whole: the same scan of the totals.  The dropped
+            // slots of earlier chunks are what is left of those chunks.
+            uint32_t used = used_in_tile, start = local, ahead = 0;
+            if constexpr (TABLE != kNoTable) {
+                start = scan(total, wave_total[1], used);
+                __syncthreads();
+                scan(before, wave_total[1], ahead);
             }
-            __syncthreads();
-            const uint32_t others = lane < kPlaceWaves ? wave_total[0][lane] : 0u;
-            const uint32_t prior = group_sum_u32<64>(lane < wave ? others : 0u);
-            const uint32_t sum = group_sum_u32<64>(others);
-            uint32_t ahead = 0;
-            if constexpr (TABLE) ahead = group_sum_u32<64>(lane < kPlaceWaves ? wave_total[1][lane] : 0u);
-            const uint32_t start = prior + incl - total;
-            if (threadIdx.x < experts) base[threadIdx.x] = start + before;
-            if (threadIdx.x == 0) base[experts] = sum + static_cast<uint32_t>(lo) - ahead;
+            if (tid < experts) base[tid] = start + before;
+            if (tid == 0) base[experts] = used + static_cast<uint32_t>(lo) - ahead;
             if (blockIdx.x == 0) {
-                if (threadIdx.x < experts) offsets[threadIdx.x] = static_cast<int32_t>(start);
-                if (threadIdx.x == 0) offsets[experts] = static_cast<int32_t>(sum);
+                if (tid < experts) offsets[tid] = static_cast<int32_t>(start);
+                if (tid == 0) offsets[experts] = static_cast<int32_t>(used);
             }
             __syncthreads();
         }
-        // Each wave's first place per key; the next tile starts behind the last.
-        for (uint32_t e = threadIdx.x; e < keys; e += kPlaceBlock) {
-            uint32_t run = base[e], c[kPlaceWaves];
+        // The waves' starts of each key in the tile.
+        for (uint32_t e = tid; e < keys; e += kPlaceBlock) {
+            uint32_t run = e < experts ? local : used_in_tile, c[kPlaceWaves];
 #pragma unroll
-            for (int w = 0; w < kPlaceWaves; ++w) c[w] = count[w * keys + e];
+            for (uint32_t w = 0; w < kPlaceWaves; ++w) c[w] = count[w * keys + e];
+            const uint32_t at = base[e] - run;
+            delta[e] = at;
 #pragma unroll
-            for (int w = 0; w < kPlaceWaves; ++w) {
+            for (uint32_t w = 0; w < kPlaceWaves; ++w) {
                 count[w * keys + e] = run;
                 run += c[w];
             }
-            base[e] = run;
+            base[e] = at + run;
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            const size_t slot = tile + (static_cast<size_t>(wave) * ITEMS + i) * 64 + lane;
-            if (slot < hi) {
-                const uint32_t place = own[key[i]] + rank[i];
-                order[place] = static_cast<int32_t>(slot);
-                position[slot] = static_cast<int32_t>(key[i] == experts ? ~place : place);
+            const uint32_t slot = mine + i * 64;
+            if (key[i] <= experts) {
+                const uint32_t local_place = own[key[i]] + rank[i], place = local_place + delta[key[i]];
+                sorted[local_place] = slot | key[i] << 16;
+                position[tile + slot] = static_cast<int32_t>(key[i] == experts ? ~place : place);
+            }
+        }
+        const uint32_t here = hi - tile < kTile ? static_cast<uint32_t>(hi - tile) : kTile;
+        if (tile + kTile < hi) load_keys(tile + kTile);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            const uint32_t p = tid + i * kPlaceBlock;
+            if (p < here) {
+                const uint32_t v = sorted[p];
+                order[p + delta[v >> 16]] = static_cast<int32_t>(tile + (v & 0xFFFFu));
             }
         }
         __syncthreads();
