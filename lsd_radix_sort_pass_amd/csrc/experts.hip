@@ -56,21 +56,22 @@ bool disjoint(const Span *spans, int outputs, int all) {
 // ---------------------------------------------------------------------------
 // Routing
 // ---------------------------------------------------------------------------
-// Calls f(T{}, integral_constant G, integral_constant V) for a row of
-// `experts` logits held by G lanes, V each.
-template <class T, int G, class F>
-bool with_values(int per_lane, F &&f) {
-    if (per_lane <= 1) return f(T{}, std::integral_constant<int, G>{}, std::integral_constant<int, 1>{});
-    if (per_lane <= 2) return f(T{}, std::integral_constant<int, G>{}, std::integral_constant<int, 2>{});
-    if (per_lane <= 4) return f(T{}, std::integral_constant<int, G>{}, std::integral_constant<int, 4>{});
-    if (per_lane <= 8) return f(T{}, std::integral_constant<int, G>{}, std::integral_constant<int, 8>{});
-    return f(T{}, std::integral_constant<int, G>{}, std::integral_constant<int, 16>{});
-}
+template <int N>
+using IntC = std::integral_constant<int, N>;
 
-template <class T, class F>
-bool with_group(int experts, int k, F &&f) {
-    if (k <= 16 && experts <= 256) return with_values<T, 16>((experts + 15) / 16, f);
-    return with_values<T, 64>((experts + 63) / 64, f);
+// Calls f(IntC<V>) with the values a lane holds of a row that `per_lane` of
+// them cover.
+template <int MAX, class F>
+bool with_values(int per_lane, F &&f) {
+    if (per_lane <= 1) return f(IntC<1>{});
+    if (per_lane <= 2) return f(IntC<2>{});
+    if (per_lane <= 4) return f(IntC<4>{});
+    if (per_lane <= 8) return f(IntC<8>{});
+    if constexpr (MAX > 16) {
+        if (per_lane > 32) return f(IntC<64>{});
+        if (per_lane > 16) return f(IntC<32>{});
+    }
+    return f(IntC<16>{});
 }
 
 template <class F>
@@ -210,18 +211,18 @@ bool launch_rows(rs::RowWork<T> w, hipStream_t stream) {
         const unsigned grid = grid_for(units, static_cast<unsigned>(per_block), kMaxGrid);
         return launch_kernel(RS_KERNEL_ROWS, stream, [&] { run_kernel(kernel, grid, rs::kRowBlock, stream, w); });
     };
-    const auto dots = [&] {
-        return go(rs::dot_rows_kernel<T>, w.tokens * static_cast<size_t>(w.k), rs::kRowBlock / 64);
-    };
+    const bool weighted = w.weights != nullptr;
     if (vecs <= rs::kNarrow) {
         w.lanes = 1;
         while (w.lanes < vecs) w.lanes *= 2;
         const int per_block = rs::kRowBlock / w.lanes;
-        const bool ok = w.weights ? go(rs::narrow_rows_kernel<T, SPREAD, true>, w.tokens, per_block)
-                                  : go(rs::narrow_rows_kernel<T, SPREAD, false>, w.tokens, per_block);
-        return ok && (w.dots == nullptr || dots());
+        const auto narrow = [&](auto dots) {
+            constexpr bool kDots = decltype(dots)::value;
+            return weighted ? go(rs::narrow_rows_kernel<T, SPREAD, true, kDots>, w.tokens, per_block)
+                            : go(rs::narrow_rows_kernel<T, SPREAD, false, kDots>, w.tokens, per_block);
+        };
+        return w.dots ? narrow(std::true_type{}) : narrow(std::false_type{});
     }
-    const bool weighted = w.weights != nullptr;
     if (w.dots != nullptr && (SPREAD || w.k <= rs::kMaxBatch)) {
         return with_batch(w.k, [&](auto batch) {
             constexpr int B = decltype(batch)::value;
@@ -245,7 +246,8 @@ bool launch_rows(rs::RowWork<T> w, hipStream_t stream) {
     };
     // A spread without dots loads no rows: its batch only unrolls the stores.
     const bool ok = SPREAD ? plain(std::integral_constant<int, rs::kMaxBatch>{}) : with_batch(w.k, plain);
-    return ok && (w.dots == nullptr || dots());
+    const size_t slots = w.tokens * static_cast<size_t>(w.k);
+    return ok && (w.dots == nullptr || go(rs::dot_rows_kernel<T>, slots, rs::kRowBlock / 64));
 }
 
 bool launch_spread(int dtype, const void *x, size_t tokens, int width, size_t x_stride, const int32_t *position,
@@ -297,15 +299,27 @@ rs_status rs_route_topk(const void *logits, int dtype, size_t tokens, int expert
     if (!disjoint(spans, 2, 3)) return RS_ERROR_INVALID_VALUE;
     if (tokens == 0) return RS_SUCCESS;
     const bool ok = with_dtype(dtype, [&](auto zero) {
-        return with_group<decltype(zero)>(experts, k, [&](auto t, auto g, auto v) {
-            using T = decltype(t);
-            constexpr int G = decltype(g)::value, V = decltype(v)::value;
-            const unsigned grid = grid_for(tokens, rs::kRouteBlock / G, kMaxGrid);
+        using T = decltype(zero);
+        const auto go = [&](auto kernel, int lanes) {
+            const unsigned grid = grid_for(tokens, static_cast<unsigned>(rs::kRouteBlock / lanes), kMaxGrid);
             return launch_kernel(RS_KERNEL_ROUTE, stream, [&] {
-                run_kernel(rs::route_topk_kernel<T, G, V>, grid, rs::kRouteBlock, stream,
-                           static_cast<const T *>(logits), tokens, experts, stride, k, gate, renormalize, scale,
-                           weights_out, experts_out);
+                run_kernel(kernel, grid, rs::kRouteBlock, stream, static_cast<const T *>(logits), tokens, experts,
+                           stride, k, gate, renormalize, scale, weights_out, experts_out);
             });
+        };
+        const int by16 = (experts + 15) / 16, by64 = (experts + 63) / 64;
+        if (k <= rs::kFastChoices) {
+            return with_values<64>(by16, [&](auto v) {
+                return go(rs::route_topk_kernel<T, 16, decltype(v)::value, true>, 16);
+            });
+        }
+        if (k <= 16 && by16 <= 16) {
+            return with_values<16>(by16, [&](auto v) {
+                return go(rs::route_topk_kernel<T, 16, decltype(v)::value, false>, 16);
+            });
+        }
+        return with_values<16>(by64, [&](auto v) {
+            return go(rs::route_topk_kernel<T, 64, decltype(v)::value, false>, 64);
         });
     });
     return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
@@ -326,15 +340,23 @@ rs_status rs_route_topk_backward(const void *logits, int dtype, size_t tokens, i
     if (!disjoint(spans, 1, 4)) return RS_ERROR_INVALID_VALUE;
     if (tokens == 0) return RS_SUCCESS;
     const bool ok = with_dtype(dtype, [&](auto zero) {
-        return with_group<decltype(zero)>(experts, k, [&](auto t, auto g, auto v) {
-            using T = decltype(t);
-            constexpr int G = decltype(g)::value, V = decltype(v)::value;
-            const unsigned grid = grid_for(tokens, rs::kRouteBlock / G, kMaxGrid);
+        using T = decltype(zero);
+        const auto go = [&](auto kernel, int lanes) {
+            const unsigned grid = grid_for(tokens, static_cast<unsigned>(rs::kRouteBlock / lanes), kMaxGrid);
             return launch_kernel(RS_KERNEL_ROUTE, stream, [&] {
-                run_kernel(rs::route_topk_backward_kernel<T, G, V>, grid, rs::kRouteBlock, stream,
-                           static_cast<const T *>(logits), tokens, experts, stride, chosen, grad_weights, k, gate,
-                           renormalize, scale, static_cast<T *>(grad_logits), grad_stride);
+                run_kernel(kernel, grid, rs::kRouteBlock, stream, static_cast<const T *>(logits), tokens, experts,
+                           stride, chosen, grad_weights, k, gate, renormalize, scale, static_cast<T *>(grad_logits),
+                           grad_stride);
             });
+        };
+        const int by16 = (experts + 15) / 16, by64 = (experts + 63) / 64;
+        if (k <= 16 && by16 <= 16) {
+            return with_values<16>(by16, [&](auto v) {
+                return go(rs::route_topk_backward_kernel<T, 16, decltype(v)::value>, 16);
+            });
+        }
+        return with_values<16>(by64, [&](auto v) {
+            return go(rs::route_topk_backward_kernel<T, 64, decltype(v)::value>, 64);
         });
     });
     return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include <type_traits>
+#include <utility>
 
 #include "device.hpp"
 
@@ -81,10 +82,10 @@ __device__ __forceinline__ void store_some(T *p, int have, const float (&f)[N]) 
 // Reductions over a group of 16 or 64 consecutive lanes; every lane of the
 // group gets the result.  All 64 lanes of the wave must be active.
 // ---------------------------------------------------------------------------
+// (CTRL permutes the lanes of a row of 16: every lane has a source.)
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t x) {
-    return static_cast<uint32_t>(
-        __builtin_amdgcn_update_dpp(static_cast<int>(x), static_cast<int>(x), CTRL, 0xF, 0xF, false));
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, 0xF, 0xF, true));
 }
 
 template <int G, class F>
@@ -119,10 +120,11 @@ __device__ __forceinline__ uint32_t group_sum_u32(uint32_t x) {
     return group_reduce<G>(x, [](uint32_t a, uint32_t b) { return a + b; });
 }
 
+// NaN if a lane's x is one.
 template <int G>
 __device__ __forceinline__ float group_max(float x) {
     return __uint_as_float(group_reduce<G>(__float_as_uint(x), [](uint32_t a, uint32_t b) {
-        return __float_as_uint(__builtin_fmaxf(__uint_as_float(a), __uint_as_float(b)));
+        return __float_as_uint(__builtin_elementwise_maximum(__uint_as_float(a), __uint_as_float(b)));
     }));
 }
 
@@ -133,6 +135,23 @@ __device__ __forceinline__ float group_sum(float x) {
     }));
 }
 
+// Calls f with 1 .. 15, as constants: the rotations that bring every other
+// lane of a row of 16 past a lane (DPP row_ror).
+template <class F, int... I>
+__device__ __forceinline__ void for_rotations_of(F &&f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I + 1>{}), ...);
+}
+template <class F>
+__device__ __forceinline__ void for_rotations(F &&f) {
+    for_rotations_of(f, std::make_integer_sequence<int, 15>{});
+}
+
+// The value N lanes below in a row of 16 lanes, 0 before its first.
+template <int N>
+__device__ __forceinline__ uint32_t row_shifted(uint32_t x) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x110 + N, 0xF, 0xF, false));
+}
+
 // ---------------------------------------------------------------------------
 // Routing
 // ---------------------------------------------------------------------------
@@ -140,36 +159,16 @@ constexpr int kRouteBlock = 256;
 
 // Rank of a logit as an unsigned integer: a larger logit has a larger rank,
 // -0 equals +0, every NaN ranks above every number, and -inf (an expert that
-// the row may not use) has rank 0, below every finite value.  It keeps the
-// value: ranked_value undoes it.
-__device__ __forceinline__ uint32_t rank16(uint32_t bits, uint32_t inf) {
-    if (bits == 0x8000u) bits = 0;
-    if (bits == (inf | 0x8000u)) return 0;
-    if ((bits & 0x7FFFu) > inf) return 0xFFFFu;
-    return (bits & 0x8000u) ? (~bits & 0xFFFFu) : (bits | 0x8000u);
-}
-
-__device__ __forceinline__ uint32_t unrank16(uint32_t rank) {
-    return (rank & 0x8000u) ? (rank ^ 0x8000u) : (~rank & 0xFFFFu);
-}
-
+// the row may not use) has rank 0, below every finite value.
 __device__ __forceinline__ uint32_t rank_of(float x) {
-    uint32_t bits = __float_as_uint(x);
-    if (bits == 0x80000000u) bits = 0;
-    if (bits == 0xFF800000u) return 0;
-    if ((bits & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFFu;
+    const uint32_t bits = __float_as_uint(x + 0.0f);
+    if (x == -__builtin_inff()) return 0;
+    if (x != x) return 0xFFFFFFFFu;
     return (bits & 0x80000000u) ? ~bits : (bits | 0x80000000u);
 }
-__device__ __forceinline__ uint32_t rank_of(f16 x) { return rank16(__builtin_bit_cast(uint16_t, x), 0x7C00u); }
-__device__ __forceinline__ uint32_t rank_of(bf16 x) { return rank16(__builtin_bit_cast(uint16_t, x), 0x7F80u); }
 
-template <class T>
 __device__ __forceinline__ float ranked_value(uint32_t rank) {
-    if constexpr (sizeof(T) == 4) {
-        return __uint_as_float((rank & 0x80000000u) ? (rank ^ 0x80000000u) : ~rank);
-    } else {
-        return static_cast<float>(__builtin_bit_cast(T, static_cast<uint16_t>(unrank16(rank))));
-    }
+    return __uint_as_float((rank & 0x80000000u) ? (rank ^ 0x80000000u) : ~rank);
 }
 
 enum : int { kGateSoftmax = 0, kGateSigmoid = 1 };
@@ -181,105 +180,190 @@ __device__ __forceinline__ float sigmoid(float l) {
     return (l >= 0.0f || l != l ? 1.0f : e) / (1.0f + e);
 }
 
-// G lanes hold a row's logits, V each: lane g holds the elements
-// (c * G + g) * W + w of chunk c.  k rounds take the group's largest rank;
-// lane j keeps round j's winner, so k <= G.
-// 16-bit logits carry 0xFFFF - index below the rank: one maximum finds the
-// value and, among equals, the lowest index.  32-bit logits take a second
-// reduction for the index.
-template <class T, int G, int V>
+// exp(t) for t <= 0 that goes into a sum holding a 1: exp2 of t * log2(e) in
+// two parts, without the range steps of expf (a result below 2^-126 may be 0).
+__device__ __forceinline__ float exp_in_sum(float t) {
+    constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596303e-8f, kLn2 = 0.693147182f;
+    t = t < -200.0f ? -200.0f : t;  // keeps the parts finite (a NaN stays one)
+    const float hi = t * kLog2e;
+    const float lo = __builtin_fmaf(t, kLog2eRest, __builtin_fmaf(t, kLog2e, -hi));
+    const float e = __builtin_amdgcn_exp2f(hi);
+    return __builtin_fmaf(e, lo * kLn2, e);
+}
+
+// A row's logits in G lanes, V each: lane g holds the elements
+// (c * G + g) * W + w of chunk c.
+template <int G, int V, int W>
+__device__ __forceinline__ int held_index(int g, int v) {
+    return ((v / W) * G + g) * W + v % W;
+}
+
+// Loads a row so; -inf beyond its end.  No load waits for a branch: lanes beyond
+// the end read its last elements again, and a row whose length is no multiple
+// of an access is read by elements.
+template <class T, int G, int V, int W>
+__device__ __forceinline__ void hold_row(const T *row, int experts, int g, float (&x)[V]) {
+    if (experts % W == 0) {
+#pragma unroll
+        for (int c = 0; c < V / W; ++c) {
+            const int i0 = (c * G + g) * W;
+            float f[W];
+            load_vec<T, W>(row + (i0 < experts ? i0 : experts - W), f);
+#pragma unroll
+            for (int w = 0; w < W; ++w) x[c * W + w] = i0 < experts ? f[w] : -__builtin_inff();
+        }
+    } else {
+        T f[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int i = held_index<G, V, W>(g, v);
+            f[v] = row[i < experts ? i : experts - 1];
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            x[v] = held_index<G, V, W>(g, v) < experts ? static_cast<float>(f[v]) : -__builtin_inff();
+        }
+    }
+}
+
+// Rounds of taking the group's largest rank, at its lowest index: lane j keeps
+// round j's winner (rank 0: none was left), so k <= G.
+template <int G, int V, int W>
+__device__ __forceinline__ void choose_by_rounds(const float (&x)[V], int g, int k, uint32_t &my_rank,
+                                                 uint32_t &my_index) {
+    uint32_t rank[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) rank[v] = rank_of(x[v]);
+    my_rank = my_index = 0;
+    for (int j = 0; j < k; ++j) {
+        uint32_t best = rank[0], at = 0xFFFFFFFFu;
+#pragma unroll
+        for (int v = 1; v < V; ++v) best = rank[v] > best ? rank[v] : best;
+        best = group_max_u32<G>(best);
+#pragma unroll
+        for (int v = V - 1; v >= 0; --v) at = rank[v] == best ? static_cast<uint32_t>(held_index<G, V, W>(g, v)) : at;
+        at = group_min_u32<G>(at);
+#pragma unroll
+        for (int v = 0; v < V; ++v) rank[v] = static_cast<uint32_t>(held_index<G, V, W>(g, v)) == at ? 0u : rank[v];
+        my_rank = g == j ? best : my_rank;
+        my_index = g == j ? at : my_index;
+    }
+}
+
+// The k-th largest of the 16 lanes' maxima is at most the row's k-th largest
+// logit.  With k <= kFastChoices about 11 logits of a random row of any length
+// reach it (16 * (1/9 + ... + 1/16) for k = 8): they fit one to a lane, where
+// each counts the better ones (larger, or equal with a lower index).  The
+// lanes pass the indices of theirs through `room`.  Returns false, for every
+// lane of the wave, if a row of the wave has more than 16 such logits (many
+// equal ones, few that are not -inf) or a NaN.
+constexpr int kFastChoices = 8;
+
+template <class T, int V, int W>
+__device__ __forceinline__ bool choose_by_counts(const float (&x)[V], const T *row, int g, int k, uint32_t *room,
+                                                 float &value, uint32_t &index, int &slot, bool &taken) {
+    constexpr int G = 16;
+    constexpr int kWords = (V + 31) / 32;
+    float most = x[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) most = __builtin_elementwise_maximum(most, x[v]);
+    int above = 0;
+    for_rotations([&](auto by) {
+        above += __uint_as_float(dpp<0x120 + decltype(by)::value>(__float_as_uint(most))) > most ? 1 : 0;
+    });
+    constexpr float kInf = __builtin_inff(), kLowest = -3.402823466e38f;
+    const float kth = -group_max<G>(above < k ? -most : -kInf);  // NaN with a NaN in the row
+    const float least = kth == -kInf ? kLowest : kth;            // -inf is never chosen
+    uint32_t mask[kWords] = {};
+    int mine = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) mask[v / 32] |= x[v] >= least ? 1u << (v % 32) : 0u;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) mine += __popc(mask[i]);
+    int upto = mine;
+    upto += static_cast<int>(row_shifted<1>(static_cast<uint32_t>(upto)));
+    upto += static_cast<int>(row_shifted<2>(static_cast<uint32_t>(upto)));
+    upto += static_cast<int>(row_shifted<4>(static_cast<uint32_t>(upto)));
+    upto += static_cast<int>(row_shifted<8>(static_cast<uint32_t>(upto)));
+    if (__ballot((kth != kth) | (upto > G)) != 0) return false;
+    int put = upto - mine;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+        while (mask[i] != 0) {
+            const int v = __ffs(static_cast<int>(mask[i])) - 1 + 32 * i;
+            mask[i] &= mask[i] - 1;
+            room[put++] = static_cast<uint32_t>(held_index<G, V, W>(g, v));
+        }
+    }
+    const int total = static_cast<int>(group_max_u32<G>(static_cast<uint32_t>(upto)));
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const bool holds = g < total;
+    index = holds ? room[g] : 0u;
+    __builtin_amdgcn_wave_barrier();
+    value = holds ? static_cast<float>(row[index]) : 0.0f;  // read a moment ago
+    // Larger value, then lower index, as one number; 0 for no logit.
+    const uint64_t key = holds ? static_cast<uint64_t>(rank_of(value)) << 32 | (0xFFFFFFFFu - index) : 0u;
+    int better = 0;
+    for_rotations([&](auto by) {
+        constexpr int kCtrl = 0x120 + decltype(by)::value;
+        const uint64_t other = static_cast<uint64_t>(dpp<kCtrl>(static_cast<uint32_t>(key >> 32))) << 32 |
+                               dpp<kCtrl>(static_cast<uint32_t>(key));
+        better += other > key ? 1 : 0;
+    });
+    taken = holds & (better < k);
+    slot = taken ? better : holds ? k : g;  // lanes behind the last logit hold the slots left over
+    return true;
+}
+
+// The k largest logits of each row and their weights: a row in G lanes.
+template <class T, int G, int V, bool FAST>
 __global__ __launch_bounds__(kRouteBlock) void route_topk_kernel(const T *__restrict__ logits, size_t tokens,
                                                                  int experts, size_t stride, int k, int gate,
                                                                  int renormalize, float scale,
                                                                  float *__restrict__ weights,
                                                                  int32_t *__restrict__ chosen) {
+    static_assert(G == 16 || !FAST);
     constexpr int W = V < kVec<T> ? V : kVec<T>;
-    constexpr int C = V / W;
     constexpr int kRows = kRouteBlock / G;
-    constexpr bool kPacked = sizeof(T) == 2;
+    __shared__ uint32_t room[FAST ? kRows : 1][16];
     const int g = threadIdx.x % G;
     for (size_t first = static_cast<size_t>(blockIdx.x) * kRows; first < tokens;
          first += static_cast<size_t>(gridDim.x) * kRows) {
         const size_t mine = first + threadIdx.x / G;
         const bool live = mine < tokens;
         const T *row = logits + (live ? mine : tokens - 1) * stride;
+        float x[V];
+        hold_row<T, G, V, W>(row, experts, g, x);
 
-        uint32_t rank[V];
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int i0 = (c * G + g) * W;
-            T raw[W];
-            if (i0 + W <= experts) {
-                __builtin_memcpy(raw, row + i0, sizeof(raw));
-#pragma unroll
-                for (int w = 0; w < W; ++w) rank[c * W + w] = rank_of(raw[w]);
-            } else {
-#pragma unroll
-                for (int w = 0; w < W; ++w) rank[c * W + w] = i0 + w < experts ? rank_of(row[i0 + w]) : 0u;
-            }
-            if constexpr (kPacked) {
-#pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    const uint32_t r = rank[c * W + w];
-                    rank[c * W + w] = r ? (r << 16) | (0xFFFFu - static_cast<uint32_t>(i0 + w)) : 0u;
-                }
-            }
+        float l = 0.0f;
+        uint32_t index = 0;
+        int slot = g;
+        bool taken = false, done = false;
+        if constexpr (FAST) {
+            done = choose_by_counts<T, V, W>(x, row, g, k, room[threadIdx.x / G], l, index, slot, taken);
         }
-
-        const auto value = [&](uint32_t r) { return ranked_value<T>(kPacked ? r >> 16 : r); };
-        const auto best_of = [&]() {
-            uint32_t b = rank[0];
-#pragma unroll
-            for (int v = 1; v < V; ++v) b = rank[v] > b ? rank[v] : b;
-            return group_max_u32<G>(b);
-        };
-
-        uint32_t best = best_of();
-        const float top = value(best);
-        float total = 0.0f;  // softmax over the whole row: sum of exp(l - top)
-        if (gate == kGateSoftmax && !renormalize) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) total += rank[v] ? expf(value(rank[v]) - top) : 0.0f;
-            total = group_sum<G>(total);
+        if (!done) {
+            uint32_t rank;
+            choose_by_rounds<G, V, W>(x, g, k, rank, index);
+            slot = g;
+            taken = g < k && rank != 0;
+            l = ranked_value(rank);
         }
-
-        uint32_t my_rank = 0, my_index = 0;
-        for (int j = 0; j < k; ++j) {
-            if (j > 0) best = best_of();
-            if constexpr (kPacked) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) rank[v] = rank[v] == best ? 0u : rank[v];
-                if (g == j) {
-                    my_rank = best;
-                    my_index = 0xFFFFu - (best & 0xFFFFu);
-                }
-            } else {
-                uint32_t at = 0xFFFFFFFFu;
-#pragma unroll
-                for (int v = V - 1; v >= 0; --v) {
-                    const uint32_t i = static_cast<uint32_t>(((v / W) * G + g) * W + v % W);
-                    at = rank[v] == best ? i : at;
-                }
-                at = group_min_u32<G>(at);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const uint32_t i = static_cast<uint32_t>(((v / W) * G + g) * W + v % W);
-                    rank[v] = i == at ? 0u : rank[v];
-                }
-                if (g == j) {
-                    my_rank = best;
-                    my_index = at;
-                }
-            }
-        }
-
-        // Lane j < k: slot j.  Rank 0: no expert was left to choose.
-        const bool taken = g < k && my_rank != 0;
-        const float l = value(my_rank);
-        float w = 0.0f;
+        // The largest chosen logit is the row's.
+        const float top = group_max<G>(taken ? l : -__builtin_inff());
+        float w;
         if (gate == kGateSoftmax) {
             w = taken ? expf(l - top) : 0.0f;
-            if (renormalize) total = group_sum<G>(w);
+            float total;
+            if (renormalize) {
+                total = group_sum<G>(w);
+            } else {
+                total = 0.0f;
+#pragma unroll
+                for (int v = 0; v < V; ++v) total += x[v] == -__builtin_inff() ? 0.0f : exp_in_sum(x[v] - top);
+                total = group_sum<G>(total);
+            }
             w = w / total;
         } else if (!renormalize) {
             w = sigmoid(l);
@@ -291,10 +375,10 @@ __global__ __launch_bounds__(kRouteBlock) void route_topk_kernel(const T *__rest
             w = taken ? num / (1.0f + expf(-__builtin_fabsf(l))) : 0.0f;
             w = w / group_sum<G>(w);
         }
-        if (live && g < k) {
-            const size_t at = mine * static_cast<size_t>(k) + g;
+        if (live && slot < k) {
+            const size_t at = mine * static_cast<size_t>(k) + slot;
             weights[at] = taken ? w * scale : 0.0f;
-            chosen[at] = taken ? static_cast<int32_t>(my_index) : -1;
+            chosen[at] = taken ? static_cast<int32_t>(index) : -1;
         }
     }
 }
@@ -331,17 +415,10 @@ __global__ __launch_bounds__(kRouteBlock) void route_topk_backward_kernel(
         float p[V];
         float top = 0.0f, total = 1.0f;
         if (whole) {
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int i0 = (c * G + g) * W;
-                float f[W];
-                load_some<T, W>(row + i0, experts - i0, f);
-#pragma unroll
-                for (int w = 0; w < W; ++w) p[c * W + w] = i0 + w < experts ? f[w] : -__builtin_inff();
-            }
+            hold_row<T, G, V, W>(row, experts, g, p);
             top = p[0];
 #pragma unroll
-            for (int v = 1; v < V; ++v) top = __builtin_fmaxf(top, p[v]);
+            for (int v = 1; v < V; ++v) top = __builtin_elementwise_maximum(top, p[v]);
             top = group_max<G>(top);
             total = 0.0f;
 #pragma unroll
@@ -877,40 +954,53 @@ __global__ __launch_bounds__(kRowBlock) void wide_rows_kernel(const RowWork<T> a
 }
 
 // Rows of at most kNarrow 16-byte accesses: a.lanes threads (a power of two)
-// take a token's row, an access each.
-template <class T, bool SPREAD, bool WEIGHTED>
+// take a token's row, an access each, and add their products up in pairs.
+template <class T, bool SPREAD, bool WEIGHTED, bool DOTS>
 __global__ __launch_bounds__(kRowBlock) void narrow_rows_kernel(const RowWork<T> a) {
     constexpr int W = kVec<T>;
     const int per_block = kRowBlock / a.lanes;
-    const int col = static_cast<int>(threadIdx.x % a.lanes) * W;
-    const int have = a.width - col;
-    if (have <= 0) return;
+    const int lane = static_cast<int>(threadIdx.x) % a.lanes;
+    const int col = lane * W, have = a.width - col;  // have <= 0: a lane beyond the row
     for (size_t t = static_cast<size_t>(blockIdx.x) * per_block + threadIdx.x / a.lanes; t < a.tokens;
          t += static_cast<size_t>(gridDim.x) * per_block) {
-        float f[W], acc[W] = {};
-        if constexpr (SPREAD) load_some<T, W>(a.x + t * a.x_stride + col, have, f);
+        float x[W], acc[W] = {};
+        if constexpr (SPREAD || DOTS) load_some<T, W>(a.x + t * a.x_stride + col, have, x);
         for (int j = 0; j < a.k; ++j) {
             const size_t s = t * static_cast<size_t>(a.k) + j;
             const Slot slot = slot_of(a.position[s], a.num_rows);
-            if (slot.row < 0 || (!SPREAD && !slot.used)) continue;
+            const bool used = slot.row >= 0 && slot.used;
             const float w = WEIGHTED ? a.weights[s] : 1.0f;
             if constexpr (SPREAD) {
-                float v[W];
+                if (slot.row >= 0) {
+                    float v[W];
 #pragma unroll
-                for (int i = 0; i < W; ++i) v[i] = !slot.used ? 0.0f : WEIGHTED ? w * f[i] : f[i];
-                store_some<T, W>(a.rows_out + static_cast<size_t>(slot.row) * a.rows_out_stride + col, have, v);
-            } else {
-                load_some<T, W>(a.rows_in + static_cast<size_t>(slot.row) * a.rows_in_stride + col, have, f);
+                    for (int i = 0; i < W; ++i) v[i] = !slot.used ? 0.0f : WEIGHTED ? w * x[i] : x[i];
+                    store_some<T, W>(a.rows_out + static_cast<size_t>(slot.row) * a.rows_out_stride + col, have, v);
+                }
+            }
+            if constexpr (!SPREAD || DOTS) {
+                float dot = 0.0f;
+                if (used) {
+                    float f[W];
+                    load_some<T, W>(a.rows_in + static_cast<size_t>(slot.row) * a.rows_in_stride + col, have, f);
 #pragma unroll
-                for (int i = 0; i < W; ++i) acc[i] = WEIGHTED ? __builtin_fmaf(w, f[i], acc[i]) : acc[i] + f[i];
+                    for (int i = 0; i < W; ++i) {
+                        if constexpr (!SPREAD) acc[i] = WEIGHTED ? __builtin_fmaf(w, f[i], acc[i]) : acc[i] + f[i];
+                        if constexpr (DOTS) dot = __builtin_fmaf(x[i], f[i], dot);
+                    }
+                }
+                if constexpr (DOTS) {
+                    for (int step = a.lanes / 2; step > 0; step /= 2) dot += __shfl_xor(dot, step, 64);
+                    if (lane == 0) a.dots[s] = dot;
+                }
             }
         }
         if constexpr (!SPREAD) store_some<T, W>(a.out + t * a.out_stride + col, have, acc);
     }
 }
 
-// Dots alone, for the shapes that the kernel above does not join with them:
-// narrow rows, and joins of more than a batch.  A wave takes a slot.
+// Dots alone, for wide joins of more than a batch of slots, whose kernel does
+// not take them along.  A wave takes a slot.
 template <class T>
 __global__ __launch_bounds__(kRowBlock) void dot_rows_kernel(const RowWork<T> a) {
     constexpr int W = kVec<T>;
