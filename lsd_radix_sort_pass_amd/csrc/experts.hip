@@ -59,18 +59,27 @@ bool disjoint(const Span *spans, int outputs, int all) {
 template <int N>
 using IntC = std::integral_constant<int, N>;
 
+// Calls f(first row, rows, workgroups) for launches that cover `tokens` rows
+// of `lanes` threads each: one, until the threads of a launch reach 2^28.
+template <class F>
+bool in_parts(size_t tokens, int lanes, F &&f) {
+    const size_t per_group = static_cast<size_t>(rs::kRouteBlock / lanes), part = size_t{kMaxGrid} * per_group;
+    bool ok = true;
+    for (size_t from = 0; ok && from < tokens; from += part) {
+        const size_t rows = tokens - from < part ? tokens - from : part;
+        ok = f(from, rows, static_cast<unsigned>((rows + per_group - 1) / per_group));
+    }
+    return ok;
+}
+
 // Calls f(IntC<V>) with the values a lane holds of a row that `per_lane` of
 // them cover.
-template <int MAX, class F>
+template <class F>
 bool with_values(int per_lane, F &&f) {
     if (per_lane <= 1) return f(IntC<1>{});
     if (per_lane <= 2) return f(IntC<2>{});
     if (per_lane <= 4) return f(IntC<4>{});
     if (per_lane <= 8) return f(IntC<8>{});
-    if constexpr (MAX > 16) {
-        if (per_lane > 32) return f(IntC<64>{});
-        if (per_lane > 16) return f(IntC<32>{});
-    }
     return f(IntC<16>{});
 }
 
@@ -82,6 +91,13 @@ bool with_dtype(int dtype, F &&f) {
         default: return f(rs::bf16{});
     }
 }
+
+// Whether k choices among rows of `values` logits in each of `lanes` lanes are
+// counted rather than taken in rounds, whose time grows as k * (values + 3):
+// 2^22 float32 logits, in us, counted / in rounds: 64 experts, k = 4 10.1 / 9.2,
+// k = 6 10.4 / 10.9; 128 experts, k = 2 8.1 / 7.1, k = 4 8.1 / 8.4; 1024 experts,
+// k = 4 9.8 / 9.5, k = 8 9.8 / 12.4.
+bool by_counts(int k, int lanes, int values) { return 2 * k <= lanes && k * (values + 3) > 2 * lanes; }
 
 bool good_route(int dtype, size_t tokens, int experts, int k, int gate) {
     return dtype_bytes(dtype) != 0 && experts >= 1 && experts <= RS_MAX_EXPERTS && k >= 1 && k <= experts &&
@@ -300,27 +316,26 @@ rs_status rs_route_topk(const void *logits, int dtype, size_t tokens, int expert
     if (tokens == 0) return RS_SUCCESS;
     const bool ok = with_dtype(dtype, [&](auto zero) {
         using T = decltype(zero);
-        const auto go = [&](auto kernel, int lanes) {
-            const unsigned grid = grid_for(tokens, static_cast<unsigned>(rs::kRouteBlock / lanes), kMaxGrid);
-            return launch_kernel(RS_KERNEL_ROUTE, stream, [&] {
-                run_kernel(kernel, grid, rs::kRouteBlock, stream, static_cast<const T *>(logits), tokens, experts,
-                           stride, k, gate, renormalize, scale, weights_out, experts_out);
+        const auto go = [&](auto kernel, int lanes, bool counts) {
+            return in_parts(tokens, lanes, [&](size_t from, size_t rows, unsigned grid) {
+                return launch_kernel(RS_KERNEL_ROUTE, stream, [&] {
+                    run_kernel(kernel, grid, rs::kRouteBlock, stream, static_cast<const T *>(logits) + from * stride,
+                               rows, experts, stride, k, gate, renormalize, scale, counts, weights_out + from * k,
+                               experts_out + from * k);
+                });
             });
         };
-        const int by16 = (experts + 15) / 16, by64 = (experts + 63) / 64;
-        if (k <= rs::kFastChoices) {
-            return with_values<64>(by16, [&](auto v) {
-                return go(rs::route_topk_kernel<T, 16, decltype(v)::value, true>, 16);
+        // At most 16 logits a lane, and two lanes a choice.
+        const auto with_lanes = [&](auto lanes) {
+            constexpr int kLanes = decltype(lanes)::value;
+            return with_values((experts + kLanes - 1) / kLanes, [&](auto v) {
+                constexpr int kValues = decltype(v)::value;
+                return go(rs::route_topk_kernel<T, kLanes, kValues>, kLanes, by_counts(k, kLanes, kValues));
             });
-        }
-        if (k <= 16 && by16 <= 16) {
-            return with_values<16>(by16, [&](auto v) {
-                return go(rs::route_topk_kernel<T, 16, decltype(v)::value, false>, 16);
-            });
-        }
-        return with_values<16>(by64, [&](auto v) {
-            return go(rs::route_topk_kernel<T, 64, decltype(v)::value, false>, 64);
-        });
+        };
+        if (k <= 8 && experts <= 256) return with_lanes(IntC<16>{});
+        if (k <= 16 && experts <= 512) return with_lanes(IntC<32>{});
+        return with_lanes(IntC<64>{});
     });
     return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
 }
@@ -342,20 +357,21 @@ rs_status rs_route_topk_backward(const void *logits, int dtype, size_t tokens, i
     const bool ok = with_dtype(dtype, [&](auto zero) {
         using T = decltype(zero);
         const auto go = [&](auto kernel, int lanes) {
-            const unsigned grid = grid_for(tokens, static_cast<unsigned>(rs::kRouteBlock / lanes), kMaxGrid);
-            return launch_kernel(RS_KERNEL_ROUTE, stream, [&] {
-                run_kernel(kernel, grid, rs::kRouteBlock, stream, static_cast<const T *>(logits), tokens, experts,
-                           stride, chosen, grad_weights, k, gate, renormalize, scale, static_cast<T *>(grad_logits),
-                           grad_stride);
+            return in_parts(tokens, lanes, [&](size_t from, size_t rows, unsigned grid) {
+                return launch_kernel(RS_KERNEL_ROUTE, stream, [&] {
+                    run_kernel(kernel, grid, rs::kRouteBlock, stream, static_cast<const T *>(logits) + from * stride,
+                               rows, experts, stride, chosen + from * k, grad_weights + from * k, k, gate, renormalize,
+                               scale, static_cast<T *>(grad_logits) + from * grad_stride, grad_stride);
+                });
             });
         };
         const int by16 = (experts + 15) / 16, by64 = (experts + 63) / 64;
         if (k <= 16 && by16 <= 16) {
-            return with_values<16>(by16, [&](auto v) {
+            return with_values(by16, [&](auto v) {
                 return go(rs::route_topk_backward_kernel<T, 16, decltype(v)::value>, 16);
             });
         }
-        return with_values<16>(by64, [&](auto v) {
+        return with_values(by64, [&](auto v) {
             return go(rs::route_topk_backward_kernel<T, 64, decltype(v)::value>, 64);
         });
     });

@@ -79,7 +79,7 @@ __device__ __forceinline__ void store_some(T *p, int have, const float (&f)[N]) 
 }
 
 // ---------------------------------------------------------------------------
-// Reductions over a group of 16 or 64 consecutive lanes; every lane of the
+// Reductions over a group of 16, 32 or 64 consecutive lanes; every lane of the
 // group gets the result.  All 64 lanes of the wave must be active.
 // ---------------------------------------------------------------------------
 // (CTRL permutes the lanes of a row of 16: every lane has a source.)
@@ -90,11 +90,12 @@ __device__ __forceinline__ uint32_t dpp(uint32_t x) {
 
 template <int G, class F>
 __device__ __forceinline__ uint32_t group_reduce(uint32_t x, F f) {
-    static_assert(G == 16 || G == 64);
+    static_assert(G == 16 || G == 32 || G == 64);
     x = f(x, dpp<0xB1>(x));   // quad_perm: lane ^ 1
     x = f(x, dpp<0x4E>(x));   // quad_perm: lane ^ 2
     x = f(x, dpp<0x141>(x));  // row_half_mirror: the other quad of 8
     x = f(x, dpp<0x140>(x));  // row_mirror: the other half of 16
+    if constexpr (G == 32) x = f(x, static_cast<uint32_t>(__shfl_xor(static_cast<int>(x), 16)));
     if constexpr (G == 64) {
         const uint32_t a = f(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), 0)),
                              static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), 16)));
@@ -135,21 +136,49 @@ __device__ __forceinline__ float group_sum(float x) {
     }));
 }
 
-// Calls f with 1 .. 15, as constants: the rotations that bring every other
-// lane of a row of 16 past a lane (DPP row_ror).
-template <class F, int... I>
-__device__ __forceinline__ void for_rotations_of(F &&f, std::integer_sequence<int, I...>) {
-    (f(std::integral_constant<int, I + 1>{}), ...);
+// The sum of f(x of lane b) over the other lanes b of a group of G: the group's
+// rows of 16 lanes take turns, each rotated past the lane (DPP row_ror).
+template <int BY>
+__device__ __forceinline__ uint32_t rotated(uint32_t x) {
+    return dpp<0x120 + BY>(x);
 }
-template <class F>
-__device__ __forceinline__ void for_rotations(F &&f) {
-    for_rotations_of(f, std::make_integer_sequence<int, 15>{});
+template <int BY>
+__device__ __forceinline__ uint64_t rotated(uint64_t x) {
+    return static_cast<uint64_t>(dpp<0x120 + BY>(static_cast<uint32_t>(x >> 32))) << 32 |
+           dpp<0x120 + BY>(static_cast<uint32_t>(x));
+}
+template <class U, class F, int... I>
+__device__ __forceinline__ int sum_rotated(const U &x, F &&f, std::integer_sequence<int, I...>) {
+    return (f(rotated<I + 1>(x)) + ...);
+}
+template <int G, class U, class F>
+__device__ __forceinline__ int sum_over_others(const U &x, F &&f) {
+    int sum = sum_rotated(x, f, std::make_integer_sequence<int, 15>{});
+#pragma unroll
+    for (int row = 16; row < G; row += 16) {
+        const U other = __shfl_xor(x, row);
+        sum += f(other) + sum_rotated(other, f, std::make_integer_sequence<int, 15>{});
+    }
+    return sum;
 }
 
-// The value N lanes below in a row of 16 lanes, 0 before its first.
-template <int N>
-__device__ __forceinline__ uint32_t row_shifted(uint32_t x) {
-    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x110 + N, 0xF, 0xF, false));
+// The sum of x up to each lane of its group of G.
+template <int G>
+__device__ __forceinline__ uint32_t group_inclusive_sum(uint32_t x) {
+    if constexpr (G == 64) return wave_inclusive_sum(x);
+    const auto below = [](uint32_t y, auto ctrl, auto rows) {
+        return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(y), decltype(ctrl)::value,
+                                                                 decltype(rows)::value, 0xF, false));
+    };
+    using All = std::integral_constant<int, 0xF>;
+    x += below(x, std::integral_constant<int, 0x111>{}, All{});  // row_shr 1, 2, 4, 8
+    x += below(x, std::integral_constant<int, 0x112>{}, All{});
+    x += below(x, std::integral_constant<int, 0x114>{}, All{});
+    x += below(x, std::integral_constant<int, 0x118>{}, All{});
+    if constexpr (G == 32) {  // row_bcast15 into rows 1 and 3
+        x += below(x, std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});
+    }
+    return x;
 }
 
 // ---------------------------------------------------------------------------
@@ -250,27 +279,60 @@ __device__ __forceinline__ void choose_by_rounds(const float (&x)[V], int g, int
     }
 }
 
-// The k-th largest of the 16 lanes' maxima is at most the row's k-th largest
-// logit.  With k <= kFastChoices about 11 logits of a random row of any length
-// reach it (16 * (1/9 + ... + 1/16) for k = 8): they fit one to a lane, where
-// each counts the better ones (larger, or equal with a lower index).  The
-// lanes pass the indices of theirs through `room`.  Returns false, for every
-// lane of the wave, if a row of the wave has more than 16 such logits (many
-// equal ones, few that are not -inf) or a NaN.
-constexpr int kFastChoices = 8;
+// Orders the `total` logits whose indices are in room[0 .. total): N to a lane,
+// where each counts the better ones (larger, or equal with a lower index).
+// Lane j < k gets the j-th best, if there is one.
+template <class T, int G, int N>
+__device__ __forceinline__ void place_by_counts(const T *row, int g, int k, int total, uint32_t *room, float &value,
+                                                uint32_t &index, bool &taken) {
+    uint64_t key[N];  // larger value, then lower index, as one number; 0 for no logit
+    int better[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const bool holds = g + n * G < total;
+        const uint32_t i = holds ? room[g + n * G] : 0u;
+        key[n] = holds ? static_cast<uint64_t>(rank_of(static_cast<float>(row[i]))) << 32 | (0xFFFFFFFFu - i) : 0u;
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        better[n] = 0;
+#pragma unroll
+        for (int m = 0; m < N; ++m) {
+            const auto above = [&](uint64_t other) { return other > key[n] ? 1 : 0; };
+            better[n] += sum_over_others<G>(key[m], above) + (m != n ? above(key[m]) : 0);
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        if (g + n * G < total) room[better[n]] = 0xFFFFFFFFu - static_cast<uint32_t>(key[n]);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    taken = g < k && g < total;
+    index = taken ? room[g] : 0u;
+    value = taken ? static_cast<float>(row[index]) : 0.0f;
+    __builtin_amdgcn_wave_barrier();
+}
 
-template <class T, int V, int W>
+// The k-th largest of the G lanes' maxima is at most the row's k-th largest
+// logit.  With k <= G / 2 few logits of a random row of any length reach it, 11
+// for k = 8 of 16 lanes (16 * (1/9 + ... + 1/16)), 22 for 16 of 32, 44 for 32 of
+// 64: they mostly fit one to a lane.  Rows of 16 lanes, which exceed that the most
+// often (1% of them at k = 8), have room for two to a lane; for larger groups
+// the registers of a second one would halve the waves in flight (8192 x 1024, k
+// = 32: 19.3 us without, 33.6 with).  The lanes pass the indices of theirs
+// through `room`.  Returns false, for every lane of the wave, if a row of the
+// wave has more such logits (many equal ones, few that are not -inf) or a NaN.
+template <class T, int G, int V, int W>
 __device__ __forceinline__ bool choose_by_counts(const float (&x)[V], const T *row, int g, int k, uint32_t *room,
-                                                 float &value, uint32_t &index, int &slot, bool &taken) {
-    constexpr int G = 16;
+                                                 float &value, uint32_t &index, bool &taken) {
     constexpr int kWords = (V + 31) / 32;
     float most = x[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) most = __builtin_elementwise_maximum(most, x[v]);
-    int above = 0;
-    for_rotations([&](auto by) {
-        above += __uint_as_float(dpp<0x120 + decltype(by)::value>(__float_as_uint(most))) > most ? 1 : 0;
-    });
+    const int above = sum_over_others<G>(__float_as_uint(most),
+                                         [&](uint32_t other) { return __uint_as_float(other) > most ? 1 : 0; });
     constexpr float kInf = __builtin_inff(), kLowest = -3.402823466e38f;
     const float kth = -group_max<G>(above < k ? -most : -kInf);  // NaN with a NaN in the row
     const float least = kth == -kInf ? kLowest : kth;            // -inf is never chosen
@@ -280,12 +342,9 @@ __device__ __forceinline__ bool choose_by_counts(const float (&x)[V], const T *r
     for (int v = 0; v < V; ++v) mask[v / 32] |= x[v] >= least ? 1u << (v % 32) : 0u;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) mine += __popc(mask[i]);
-    int upto = mine;
-    upto += static_cast<int>(row_shifted<1>(static_cast<uint32_t>(upto)));
-    upto += static_cast<int>(row_shifted<2>(static_cast<uint32_t>(upto)));
-    upto += static_cast<int>(row_shifted<4>(static_cast<uint32_t>(upto)));
-    upto += static_cast<int>(row_shifted<8>(static_cast<uint32_t>(upto)));
-    if (__ballot((kth != kth) | (upto > G)) != 0) return false;
+    const int upto = static_cast<int>(group_inclusive_sum<G>(static_cast<uint32_t>(mine)));
+    constexpr int kRoom = G == 16 ? 2 * G : G;
+    if (__ballot((kth != kth) | (upto > kRoom)) != 0) return false;
     int put = upto - mine;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
@@ -298,88 +357,70 @@ __device__ __forceinline__ bool choose_by_counts(const float (&x)[V], const T *r
     const int total = static_cast<int>(group_max_u32<G>(static_cast<uint32_t>(upto)));
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    const bool holds = g < total;
-    index = holds ? room[g] : 0u;
-    __builtin_amdgcn_wave_barrier();
-    value = holds ? static_cast<float>(row[index]) : 0.0f;  // read a moment ago
-    // Larger value, then lower index, as one number; 0 for no logit.
-    const uint64_t key = holds ? static_cast<uint64_t>(rank_of(value)) << 32 | (0xFFFFFFFFu - index) : 0u;
-    int better = 0;
-    for_rotations([&](auto by) {
-        constexpr int kCtrl = 0x120 + decltype(by)::value;
-        const uint64_t other = static_cast<uint64_t>(dpp<kCtrl>(static_cast<uint32_t>(key >> 32))) << 32 |
-                               dpp<kCtrl>(static_cast<uint32_t>(key));
-        better += other > key ? 1 : 0;
-    });
-    taken = holds & (better < k);
-    slot = taken ? better : holds ? k : g;  // lanes behind the last logit hold the slots left over
+    if (kRoom == G || __ballot(total > G) == 0) {
+        place_by_counts<T, G, 1>(row, g, k, total, room, value, index, taken);
+    } else {
+        place_by_counts<T, G, kRoom / G>(row, g, k, total, room, value, index, taken);
+    }
     return true;
 }
 
-// The k largest logits of each row and their weights: a row in G lanes.
-template <class T, int G, int V, bool FAST>
+// The k largest logits of each row and their weights: a row in G lanes, slot j
+// in lane j.  counts: choose_by_counts is tried first (k <= G / 2).
+template <class T, int G, int V>
 __global__ __launch_bounds__(kRouteBlock) void route_topk_kernel(const T *__restrict__ logits, size_t tokens,
                                                                  int experts, size_t stride, int k, int gate,
-                                                                 int renormalize, float scale,
+                                                                 int renormalize, float scale, bool counts,
                                                                  float *__restrict__ weights,
                                                                  int32_t *__restrict__ chosen) {
-    static_assert(G == 16 || !FAST);
     constexpr int W = V < kVec<T> ? V : kVec<T>;
     constexpr int kRows = kRouteBlock / G;
-    __shared__ uint32_t room[FAST ? kRows : 1][16];
+    __shared__ uint32_t room[kRows][2 * G];
     const int g = threadIdx.x % G;
-    for (size_t first = static_cast<size_t>(blockIdx.x) * kRows; first < tokens;
-         first += static_cast<size_t>(gridDim.x) * kRows) {
-        const size_t mine = first + threadIdx.x / G;
-        const bool live = mine < tokens;
-        const T *row = logits + (live ? mine : tokens - 1) * stride;
-        float x[V];
-        hold_row<T, G, V, W>(row, experts, g, x);
+    const size_t mine = static_cast<size_t>(blockIdx.x) * kRows + threadIdx.x / G;
+    const bool live = mine < tokens;
+    const T *row = logits + (live ? mine : tokens - 1) * stride;
+    float x[V];
+    hold_row<T, G, V, W>(row, experts, g, x);
 
-        float l = 0.0f;
-        uint32_t index = 0;
-        int slot = g;
-        bool taken = false, done = false;
-        if constexpr (FAST) {
-            done = choose_by_counts<T, V, W>(x, row, g, k, room[threadIdx.x / G], l, index, slot, taken);
-        }
-        if (!done) {
-            uint32_t rank;
-            choose_by_rounds<G, V, W>(x, g, k, rank, index);
-            slot = g;
-            taken = g < k && rank != 0;
-            l = ranked_value(rank);
-        }
-        // The largest chosen logit is the row's.
-        const float top = group_max<G>(taken ? l : -__builtin_inff());
-        float w;
-        if (gate == kGateSoftmax) {
-            w = taken ? expf(l - top) : 0.0f;
-            float total;
-            if (renormalize) {
-                total = group_sum<G>(w);
-            } else {
-                total = 0.0f;
-#pragma unroll
-                for (int v = 0; v < V; ++v) total += x[v] == -__builtin_inff() ? 0.0f : exp_in_sum(x[v] - top);
-                total = group_sum<G>(total);
-            }
-            w = w / total;
-        } else if (!renormalize) {
-            w = sigmoid(l);
+    float l = 0.0f;
+    uint32_t index = 0;
+    bool taken = false;
+    if (!counts || !choose_by_counts<T, G, V, W>(x, row, g, k, room[threadIdx.x / G], l, index, taken)) {
+        uint32_t rank;
+        choose_by_rounds<G, V, W>(x, g, k, rank, index);
+        taken = g < k && rank != 0;
+        l = ranked_value(rank);
+    }
+    // The largest chosen logit is the row's.
+    const float top = group_max<G>(taken ? l : -__builtin_inff());
+    float w;
+    if (gate == kGateSoftmax) {
+        w = taken ? expf(l - top) : 0.0f;
+        float total;
+        if (renormalize) {
+            total = group_sum<G>(w);
         } else {
-            // sigmoid(l) = exp(min(l, 0)) / (1 + exp(-|l|)): the common factor
-            // exp(min(top, 0)) cancels, so very negative rows keep their ratios.
-            const float shift = __builtin_fminf(top, 0.0f);
-            const float num = l != l ? l : expf(__builtin_fminf(l, 0.0f) - shift);
-            w = taken ? num / (1.0f + expf(-__builtin_fabsf(l))) : 0.0f;
-            w = w / group_sum<G>(w);
+            total = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) total += x[v] == -__builtin_inff() ? 0.0f : exp_in_sum(x[v] - top);
+            total = group_sum<G>(total);
         }
-        if (live && slot < k) {
-            const size_t at = mine * static_cast<size_t>(k) + slot;
-            weights[at] = taken ? w * scale : 0.0f;
-            chosen[at] = taken ? static_cast<int32_t>(index) : -1;
-        }
+        w = w / total;
+    } else if (!renormalize) {
+        w = sigmoid(l);
+    } else {
+        // sigmoid(l) = exp(min(l, 0)) / (1 + exp(-|l|)): the common factor
+        // exp(min(top, 0)) cancels, so very negative rows keep their ratios.
+        const float shift = __builtin_fminf(top, 0.0f);
+        const float num = l != l ? l : expf(__builtin_fminf(l, 0.0f) - shift);
+        w = taken ? num / (1.0f + expf(-__builtin_fabsf(l))) : 0.0f;
+        w = w / group_sum<G>(w);
+    }
+    if (live && g < k) {
+        const size_t at = mine * static_cast<size_t>(k) + g;
+        weights[at] = taken ? w * scale : 0.0f;
+        chosen[at] = taken ? static_cast<int32_t>(index) : -1;
     }
 }
 
@@ -405,95 +446,91 @@ __global__ __launch_bounds__(kRouteBlock) void route_topk_backward_kernel(
     const int g = threadIdx.x % G;
     const int sub = threadIdx.x / G;
     const bool whole = gate == kGateSoftmax && !renormalize;
-    for (size_t first = static_cast<size_t>(blockIdx.x) * kRows; first < tokens;
-         first += static_cast<size_t>(gridDim.x) * kRows) {
-        const size_t mine = first + sub;
-        const bool live = mine < tokens;
-        const size_t r = live ? mine : tokens - 1;
-        const T *row = logits + r * stride;
+    const size_t mine = static_cast<size_t>(blockIdx.x) * kRows + sub;
+    const bool live = mine < tokens;
+    const size_t r = live ? mine : tokens - 1;
+    const T *row = logits + r * stride;
 
-        float p[V];
-        float top = 0.0f, total = 1.0f;
-        if (whole) {
-            hold_row<T, G, V, W>(row, experts, g, p);
-            top = p[0];
+    float p[V];
+    float top = 0.0f, total = 1.0f;
+    if (whole) {
+        hold_row<T, G, V, W>(row, experts, g, p);
+        top = p[0];
 #pragma unroll
-            for (int v = 1; v < V; ++v) top = __builtin_elementwise_maximum(top, p[v]);
-            top = group_max<G>(top);
-            total = 0.0f;
+        for (int v = 1; v < V; ++v) top = __builtin_elementwise_maximum(top, p[v]);
+        top = group_max<G>(top);
+        total = 0.0f;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                p[v] = p[v] == -__builtin_inff() ? 0.0f : expf(p[v] - top);
-                total += p[v];
-            }
-            total = group_sum<G>(total);
+        for (int v = 0; v < V; ++v) {
+            p[v] = p[v] == -__builtin_inff() ? 0.0f : expf(p[v] - top);
+            total += p[v];
         }
+        total = group_sum<G>(total);
+    }
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
+    for (int c = 0; c < C; ++c) {
 #pragma unroll
-            for (int w = 0; w < W; ++w) terms[sub][(c * G + g) * W + w] = 0.0f;
-        }
+        for (int w = 0; w < W; ++w) terms[sub][(c * G + g) * W + w] = 0.0f;
+    }
 
-        int32_t s = -1;
-        float h = 0.0f, l = -__builtin_inff();
-        if (g < k) {
-            s = chosen[r * static_cast<size_t>(k) + g];
-            if (static_cast<uint32_t>(s) < static_cast<uint32_t>(experts)) {
-                l = static_cast<float>(row[s]);
-                h = grad_weights[r * static_cast<size_t>(k) + g];
-            }
+    int32_t s = -1;
+    float h = 0.0f, l = -__builtin_inff();
+    if (g < k) {
+        s = chosen[r * static_cast<size_t>(k) + g];
+        if (static_cast<uint32_t>(s) < static_cast<uint32_t>(experts)) {
+            l = static_cast<float>(row[s]);
+            h = grad_weights[r * static_cast<size_t>(k) + g];
         }
-        const bool taken = l != -__builtin_inff();  // a slot without an expert adds nothing
-        float d = 0.0f, mean = 0.0f;
-        if (whole) {
-            mean = group_sum<G>(taken ? h * (expf(l - top) / total) : 0.0f);
-            d = h;
-        } else if (!renormalize) {
-            d = h * sigmoid(l) * sigmoid(-l);
+    }
+    const bool taken = l != -__builtin_inff();  // a slot without an expert adds nothing
+    float d = 0.0f, mean = 0.0f;
+    if (whole) {
+        mean = group_sum<G>(taken ? h * (expf(l - top) / total) : 0.0f);
+        d = h;
+    } else if (!renormalize) {
+        d = h * sigmoid(l) * sigmoid(-l);
+    } else {
+        float best = group_max<G>(taken ? l : -__builtin_inff());
+        float u;
+        if (gate == kGateSoftmax) {
+            u = taken ? expf(l - best) : 0.0f;
         } else {
-            float best = group_max<G>(taken ? l : -__builtin_inff());
-            float u;
-            if (gate == kGateSoftmax) {
-                u = taken ? expf(l - best) : 0.0f;
+            best = __builtin_fminf(best, 0.0f);
+            const float num = l != l ? l : expf(__builtin_fminf(l, 0.0f) - best);
+            u = taken ? num / (1.0f + expf(-__builtin_fabsf(l))) : 0.0f;
+        }
+        u = u / group_sum<G>(u);
+        mean = group_sum<G>(taken ? h * u : 0.0f);
+        d = u * (h - mean);
+        if (gate == kGateSigmoid) d *= sigmoid(-l);
+    }
+    if (!taken) d = 0.0f;
+    // Slots that chose the same expert each store the sum of all of them.
+    float sum = 0.0f;
+    for (int j = 0; j < k; ++j) {
+        const int sj = __shfl(s, j, G);
+        const float dj = __shfl(d, j, G);
+        sum += sj == s ? dj : 0.0f;
+    }
+    __syncthreads();
+    if (taken) terms[sub][s] = sum;
+    __syncthreads();
+    T *out = grad_logits + r * grad_stride;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int i0 = (c * G + g) * W;
+        float f[W];
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float a = terms[sub][i0 + w];
+            if (whole) {
+                const float q = p[c * W + w] / total;
+                f[w] = p[c * W + w] == 0.0f ? 0.0f : scale * (q * (a - mean));
             } else {
-                best = __builtin_fminf(best, 0.0f);
-                const float num = l != l ? l : expf(__builtin_fminf(l, 0.0f) - best);
-                u = taken ? num / (1.0f + expf(-__builtin_fabsf(l))) : 0.0f;
+                f[w] = scale * a;
             }
-            u = u / group_sum<G>(u);
-            mean = group_sum<G>(taken ? h * u : 0.0f);
-            d = u * (h - mean);
-            if (gate == kGateSigmoid) d *= sigmoid(-l);
         }
-        if (!taken) d = 0.0f;
-        // Slots that chose the same expert each store the sum of all of them.
-        float sum = 0.0f;
-        for (int j = 0; j < k; ++j) {
-            const int sj = __shfl(s, j, G);
-            const float dj = __shfl(d, j, G);
-            sum += sj == s ? dj : 0.0f;
-        }
-        __syncthreads();
-        if (taken) terms[sub][s] = sum;
-        __syncthreads();
-        T *out = grad_logits + r * grad_stride;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int i0 = (c * G + g) * W;
-            float f[W];
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const float a = terms[sub][i0 + w];
-                if (whole) {
-                    const float q = p[c * W + w] / total;
-                    f[w] = p[c * W + w] == 0.0f ? 0.0f : scale * (q * (a - mean));
-                } else {
-                    f[w] = scale * a;
-                }
-            }
-            if (live && i0 < experts) store_some<T, W>(out + i0, experts - i0, f);
-        }
-        __syncthreads();
+        if (live && i0 < experts) store_some<T, W>(out + i0, experts - i0, f);
     }
 }
 
