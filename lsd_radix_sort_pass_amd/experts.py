@@ -41,6 +41,7 @@ MAX_CHOICES = 64        # RS_MAX_CHOICES
 
 _ROW_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}      # rs_dtype
 _GATES = {"softmax": 0, "sigmoid": 1}                                      # rs_gate
+_I32, _F32, _U8 = (torch.int32,), (torch.float32,), (torch.uint8,)
 _SORT_FN = {torch.int32: "rs_sort_experts_i32", torch.int64: "rs_sort_experts_i64"}
 
 
@@ -53,7 +54,8 @@ class ExpertOrder(NamedTuple):
     offsets: torch.Tensor
 
 
-def _tensor(t, name, dtypes, dim, device=None) -> torch.Tensor:
+def _refuse(t, name, dtypes, dim, device, shape, rows) -> None:
+    """Raises what is wrong with a tensor that failed the checks below."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -65,73 +67,78 @@ def _tensor(t, name, dtypes, dim, device=None) -> torch.Tensor:
         raise ValueError(f"{name} must have {dim} dimensions (got {t.dim()})")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires a gradient, which this call does not record: use it in a "
                          "torch.autograd.Function or under torch.no_grad()")
-    return t
-
-
-def _rows(t, name, device=None, dtype=None, shape=None) -> torch.Tensor:
-    """A 2-D float tensor with consecutive elements in a row, any row stride."""
-    _tensor(t, name, _ROW_DTYPES if dtype is None else (dtype,), 2, device)
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape} (got {tuple(t.shape)})")
-    if t.shape[1] > 1 and t.stride(1) != 1 and t.shape[0]:
-        raise ValueError(f"{name} must have consecutive elements in each row")
-    return t
-
-
-def _flat(t, name, dtypes, device, shape=None, dim=None) -> torch.Tensor:
-    _tensor(t, name, dtypes, dim, device)
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape} (got {tuple(t.shape)})")
-    if not t.is_contiguous():
+    if rows:
+        if t.shape[1] > 1 and t.stride(1) != 1 and t.shape[0]:
+            raise ValueError(f"{name} must have consecutive elements in each row")
+    elif not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t
+
+
+def _rows(t, name, device=None, dtypes=_ROW_DTYPES, shape=None) -> None:
+    """Checks a 2-D float tensor with consecutive elements in a row, any row
+    stride."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == 2 and t.is_contiguous()
+            and not t.requires_grad and (device is None or t.device == device)
+            and (shape is None or t.shape == shape)):
+        _refuse(t, name, dtypes, 2, device, shape, True)
+
+
+def _flat(t, name, dtypes, device, shape=None, dim=None) -> None:
+    """Checks a contiguous tensor."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.is_contiguous()
+            and not t.requires_grad and (device is None or t.device == device)
+            and (shape is None or t.shape == shape) and (dim is None or t.dim() == dim)):
+        _refuse(t, name, dtypes, dim, device, shape, False)
 
 
 def _places(position, weights, device) -> Tuple[int, int]:
     """(tokens, k) of a call's places, with its weights checked against them."""
-    _flat(position, "position", (torch.int32,), device, dim=2)
+    _flat(position, "position", _I32, device, None, 2)
     if weights is not None:
-        _flat(weights, "weights", (torch.float32,), device, tuple(position.shape))
-    return position.shape[0], position.shape[1]
+        _flat(weights, "weights", _F32, device, position.shape)
+    return position.shape
 
 
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-class _Call:
-    """Device, stream and allocation of one call: its tensors belong to the
-    stream it runs on, and its kernels are launched on that stream's device."""
+# The current stream's handle of a device, without making a Stream of it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, device, stream, *inputs):
-        self._guards = []
-        if device.index != torch.cuda.current_device():
-            self._guards.append(torch.cuda.device(device))
-        if stream is not None and stream != torch.cuda.current_stream(device):
-            if stream.device != device:
-                raise ValueError(f"stream must belong to {device} (got {stream.device})")
-            self._guards.append(torch.cuda.stream(stream))
-            for t in inputs:
+
+def _elsewhere(device, stream) -> bool:
+    """Whether a call has to change the current device or stream first."""
+    return stream is not None or device.index != torch.cuda.current_device()
+
+
+@contextlib.contextmanager
+def _on(device, stream, *tensors):
+    """Makes device, and stream if given, current, so that what a call
+    allocates belongs to them, and keeps the call's tensors from reuse until
+    the stream is done with them."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream must belong to {device} (got {stream.device})")
+    with torch.cuda.device(device):
+        if stream is None or stream == torch.cuda.current_stream():
+            yield
+            return
+        with torch.cuda.stream(stream):
+            for t in tensors:
                 if t is not None:
                     t.record_stream(stream)
-        self.handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-
-    def run(self, body):
-        if not self._guards:
-            return body(self.handle)
-        with contextlib.ExitStack() as stack:
-            for guard in self._guards:
-                stack.enter_context(guard)
-            return body(self.handle)
+            yield
 
 
-def _ok(code: int, name: str) -> None:
-    if code != _lib.RS_SUCCESS:
-        from . import RadixSortError
-        raise RadixSortError(code, name)
+def _fail(code: int, name: str) -> None:
+    from . import RadixSortError
+    raise RadixSortError(code, name)
 
 
 def _gate(mode) -> int:
@@ -162,19 +169,20 @@ def route_topk(logits: torch.Tensor, k: int, mode: str = "softmax", renormalize:
     tokens, experts = logits.shape
     k, gate, device = _choices(k, experts), _gate(mode), logits.device
     if weights_out is not None:
-        _flat(weights_out, "weights_out", (torch.float32,), device, (tokens, k))
+        _flat(weights_out, "weights_out", _F32, device, (tokens, k))
     if experts_out is not None:
-        _flat(experts_out, "experts_out", (torch.int32,), device, (tokens, k))
-    call = _Call(device, stream, logits, weights_out, experts_out)
-
-    def body(handle):
-        w = torch.empty((tokens, k), dtype=torch.float32, device=device) if weights_out is None else weights_out
-        e = torch.empty((tokens, k), dtype=torch.int32, device=device) if experts_out is None else experts_out
-        _ok(_lib.load().rs_route_topk(logits.data_ptr(), _ROW_DTYPES[logits.dtype], tokens, experts,
-                                      logits.stride(0), k, gate, 1 if renormalize else 0, scale, w.data_ptr(),
-                                      e.data_ptr(), handle), "rs_route_topk")
-        return w, e
-    return call.run(body)
+        _flat(experts_out, "experts_out", _I32, device, (tokens, k))
+    if _elsewhere(device, stream):
+        with _on(device, stream, logits, weights_out, experts_out):
+            return route_topk(logits, k, mode, renormalize, scale, weights_out, experts_out)
+    w = torch.empty((tokens, k), dtype=torch.float32, device=device) if weights_out is None else weights_out
+    e = torch.empty((tokens, k), dtype=torch.int32, device=device) if experts_out is None else experts_out
+    code = _lib.load().rs_route_topk(logits.data_ptr(), _ROW_DTYPES[logits.dtype], tokens, experts, logits.stride(0),
+                                     k, gate, 1 if renormalize else 0, scale, w.data_ptr(), e.data_ptr(),
+                                     _raw_stream(device.index))
+    if code:
+        _fail(code, "rs_route_topk")
+    return w, e
 
 
 def route_topk_backward(logits: torch.Tensor, experts: torch.Tensor, grad_weights: torch.Tensor,
@@ -187,23 +195,24 @@ def route_topk_backward(logits: torch.Tensor, experts: torch.Tensor, grad_weight
     _rows(logits, "logits")
     tokens, count = logits.shape
     device, gate = logits.device, _gate(mode)
-    _flat(experts, "experts", (torch.int32,), device, dim=2)
+    _flat(experts, "experts", _I32, device, None, 2)
     k = _choices(experts.shape[1], count)
     if experts.shape[0] != tokens:
         raise ValueError("experts must have a row for each row of logits")
-    _flat(grad_weights, "grad_weights", (torch.float32,), device, (tokens, k))
+    _flat(grad_weights, "grad_weights", _F32, device, (tokens, k))
     if out is not None:
-        _rows(out, "out", device, logits.dtype, (tokens, count))
-    call = _Call(device, stream, logits, experts, grad_weights, out)
-
-    def body(handle):
-        grad = torch.empty((tokens, count), dtype=logits.dtype, device=device) if out is None else out
-        _ok(_lib.load().rs_route_topk_backward(logits.data_ptr(), _ROW_DTYPES[logits.dtype], tokens, count,
-                                               logits.stride(0), experts.data_ptr(), grad_weights.data_ptr(), k,
-                                               gate, 1 if renormalize else 0, scale, grad.data_ptr(),
-                                               grad.stride(0), handle), "rs_route_topk_backward")
-        return grad
-    return call.run(body)
+        _rows(out, "out", device, (logits.dtype,), (tokens, count))
+    if _elsewhere(device, stream):
+        with _on(device, stream, logits, experts, grad_weights, out):
+            return route_topk_backward(logits, experts, grad_weights, mode, renormalize, scale, out)
+    grad = torch.empty((tokens, count), dtype=logits.dtype, device=device) if out is None else out
+    code = _lib.load().rs_route_topk_backward(logits.data_ptr(), _ROW_DTYPES[logits.dtype], tokens, count,
+                                              logits.stride(0), experts.data_ptr(), grad_weights.data_ptr(), k, gate,
+                                              1 if renormalize else 0, scale, grad.data_ptr(), grad.stride(0),
+                                              _raw_stream(device.index))
+    if code:
+        _fail(code, "rs_route_topk_backward")
+    return grad
 
 
 def temp_bytes_experts(n: int, num_experts: int) -> int:
@@ -226,33 +235,34 @@ def sort_experts(experts: torch.Tensor, num_experts: int, first_expert: int = 0,
     n, device, num = experts.numel(), experts.device, int(num_experts)
     if not 1 <= num <= MAX_EXPERTS:
         raise ValueError(f"num_experts must be between 1 and {MAX_EXPERTS} (got {num})")
-    if not 0 <= int(first_expert) <= 2**31 - num:
-        raise ValueError(f"first_expert must be between 0 and 2^31 - num_experts (got {first_expert})")
+    first = int(first_expert)
+    if not 0 <= first <= 2**31 - num:
+        raise ValueError(f"first_expert must be between 0 and 2^31 - num_experts (got {first})")
     if order_out is not None:
-        _flat(order_out, "order_out", (torch.int32,), device, (n,))
+        _flat(order_out, "order_out", _I32, device, (n,))
     if position_out is not None:
-        _flat(position_out, "position_out", (torch.int32,), device, tuple(experts.shape))
+        _flat(position_out, "position_out", _I32, device, experts.shape)
     if offsets_out is not None:
-        _flat(offsets_out, "offsets_out", (torch.int32,), device, (num + 1,))
+        _flat(offsets_out, "offsets_out", _I32, device, (num + 1,))
     if temp is not None:
-        _flat(temp, "temp", (torch.uint8,), device)
-    call = _Call(device, stream, experts, order_out, position_out, offsets_out, temp)
+        _flat(temp, "temp", _U8, device)
+    if _elsewhere(device, stream):
+        with _on(device, stream, experts, order_out, position_out, offsets_out, temp):
+            return sort_experts(experts, num, first_expert, order_out, position_out, offsets_out, temp)
+    lib = _lib.load()
+    order = torch.empty(n, dtype=torch.int32, device=device) if order_out is None else order_out
+    position = torch.empty(experts.shape, dtype=torch.int32, device=device) if position_out is None else position_out
+    offsets = torch.empty(num + 1, dtype=torch.int32, device=device) if offsets_out is None else offsets_out
+    if temp is None:
+        need = lib.rs_temp_bytes_experts(n, num)
+        temp = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     name = _SORT_FN[experts.dtype]
-
-    def body(handle):
-        lib = _lib.load()
-        new = lambda shape: torch.empty(shape, dtype=torch.int32, device=device)
-        order = new(n) if order_out is None else order_out
-        position = new(experts.shape) if position_out is None else position_out
-        offsets = new(num + 1) if offsets_out is None else offsets_out
-        store = temp
-        if store is None:
-            need = int(lib.rs_temp_bytes_experts(n, num))
-            store = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-        _ok(getattr(lib, name)(experts.data_ptr(), n, int(first_expert), num, order.data_ptr(), position.data_ptr(),
-                               offsets.data_ptr(), _ptr(store), 0 if store is None else store.numel(), handle), name)
-        return ExpertOrder(order, position, offsets)
-    return call.run(body)
+    code = getattr(lib, name)(experts.data_ptr(), n, first, num, order.data_ptr(), position.data_ptr(),
+                              offsets.data_ptr(), _ptr(temp), 0 if temp is None else temp.numel(),
+                              _raw_stream(device.index))
+    if code:
+        _fail(code, name)
+    return ExpertOrder(order, position, offsets)
 
 
 def dispatch_rows(x: torch.Tensor, position: torch.Tensor, weights: Optional[torch.Tensor] = None,
@@ -268,21 +278,23 @@ def dispatch_rows(x: torch.Tensor, position: torch.Tensor, weights: Optional[tor
     _rows(x, "x")
     device = x.device
     tokens, k = _places(position, weights, device)
-    if x.shape[0] != tokens:
+    count, width = x.shape
+    if count != tokens:
         raise ValueError("position must have a row for each row of x")
     if out is not None:
-        _rows(out, "out", device, x.dtype)
-        if out.shape[1] != x.shape[1]:
+        _rows(out, "out", device, (x.dtype,))
+        if out.shape[1] != width:
             raise ValueError("out must have the width of x")
-    call = _Call(device, stream, x, position, weights, out)
-
-    def body(handle):
-        rows = torch.empty((tokens * k, x.shape[1]), dtype=x.dtype, device=device) if out is None else out
-        _ok(_lib.load().rs_dispatch_rows(x.data_ptr(), _ROW_DTYPES[x.dtype], tokens, x.shape[1], x.stride(0),
-                                         position.data_ptr(), _ptr(weights), k, rows.data_ptr(), rows.shape[0],
-                                         rows.stride(0), handle), "rs_dispatch_rows")
-        return rows
-    return call.run(body)
+    if _elsewhere(device, stream):
+        with _on(device, stream, x, position, weights, out):
+            return dispatch_rows(x, position, weights, out)
+    rows = torch.empty((tokens * k, width), dtype=x.dtype, device=device) if out is None else out
+    code = _lib.load().rs_dispatch_rows(x.data_ptr(), _ROW_DTYPES[x.dtype], tokens, width, x.stride(0),
+                                        position.data_ptr(), _ptr(weights), k, rows.data_ptr(), rows.shape[0],
+                                        rows.stride(0), _raw_stream(device.index))
+    if code:
+        _fail(code, "rs_dispatch_rows")
+    return rows
 
 
 def dispatch_rows_backward(grad_rows: torch.Tensor, position: torch.Tensor, x: Optional[torch.Tensor] = None,
@@ -294,29 +306,31 @@ def dispatch_rows_backward(grad_rows: torch.Tensor, position: torch.Tensor, x: O
     with x given also grad_weights (T, k) float32, as a pair.  weights are the
     forward call's."""
     _rows(grad_rows, "grad_rows")
-    device, width = grad_rows.device, grad_rows.shape[1]
+    device = grad_rows.device
+    count, width = grad_rows.shape
     tokens, k = _places(position, weights, device)
     if x is not None:
-        _rows(x, "x", device, grad_rows.dtype, (tokens, width))
+        _rows(x, "x", device, (grad_rows.dtype,), (tokens, width))
     elif grad_weights_out is not None:
         raise ValueError("grad_weights_out needs x")
     if out is not None:
-        _rows(out, "out", device, grad_rows.dtype, (tokens, width))
+        _rows(out, "out", device, (grad_rows.dtype,), (tokens, width))
     if grad_weights_out is not None:
-        _flat(grad_weights_out, "grad_weights_out", (torch.float32,), device, (tokens, k))
-    call = _Call(device, stream, grad_rows, position, x, weights, out, grad_weights_out)
-
-    def body(handle):
-        grad = torch.empty((tokens, width), dtype=grad_rows.dtype, device=device) if out is None else out
-        dots = grad_weights_out
-        if x is not None and dots is None:
-            dots = torch.empty((tokens, k), dtype=torch.float32, device=device)
-        _ok(_lib.load().rs_dispatch_rows_backward(
-            grad_rows.data_ptr(), _ROW_DTYPES[grad_rows.dtype], grad_rows.shape[0], grad_rows.stride(0),
-            position.data_ptr(), _ptr(weights), k, _ptr(x), 0 if x is None else x.stride(0), grad.data_ptr(),
-            grad.stride(0), _ptr(dots), tokens, width, handle), "rs_dispatch_rows_backward")
-        return grad if x is None else (grad, dots)
-    return call.run(body)
+        _flat(grad_weights_out, "grad_weights_out", _F32, device, (tokens, k))
+    if _elsewhere(device, stream):
+        with _on(device, stream, grad_rows, position, x, weights, out, grad_weights_out):
+            return dispatch_rows_backward(grad_rows, position, x, weights, out, grad_weights_out)
+    grad = torch.empty((tokens, width), dtype=grad_rows.dtype, device=device) if out is None else out
+    dots = grad_weights_out
+    if x is not None and dots is None:
+        dots = torch.empty((tokens, k), dtype=torch.float32, device=device)
+    code = _lib.load().rs_dispatch_rows_backward(
+        grad_rows.data_ptr(), _ROW_DTYPES[grad_rows.dtype], count, grad_rows.stride(0), position.data_ptr(),
+        _ptr(weights), k, _ptr(x), 0 if x is None else x.stride(0), grad.data_ptr(), grad.stride(0), _ptr(dots),
+        tokens, width, _raw_stream(device.index))
+    if code:
+        _fail(code, "rs_dispatch_rows_backward")
+    return grad if x is None else (grad, dots)
 
 
 def combine_rows(rows: torch.Tensor, position: torch.Tensor, weights: Optional[torch.Tensor] = None,
@@ -328,19 +342,21 @@ def combine_rows(rows: torch.Tensor, position: torch.Tensor, weights: Optional[t
     rows (n, H) float32, float16 or bfloat16, position (T, k) int32, weights
     (T, k) float32; out (T, H) in the dtype of rows, summed in float32."""
     _rows(rows, "rows")
-    device, width = rows.device, rows.shape[1]
+    device = rows.device
+    count, width = rows.shape
     tokens, k = _places(position, weights, device)
     if out is not None:
-        _rows(out, "out", device, rows.dtype, (tokens, width))
-    call = _Call(device, stream, rows, position, weights, out)
-
-    def body(handle):
-        res = torch.empty((tokens, width), dtype=rows.dtype, device=device) if out is None else out
-        _ok(_lib.load().rs_combine_rows(rows.data_ptr(), _ROW_DTYPES[rows.dtype], rows.shape[0], rows.stride(0),
-                                        position.data_ptr(), _ptr(weights), k, res.data_ptr(), tokens, width,
-                                        res.stride(0), handle), "rs_combine_rows")
-        return res
-    return call.run(body)
+        _rows(out, "out", device, (rows.dtype,), (tokens, width))
+    if _elsewhere(device, stream):
+        with _on(device, stream, rows, position, weights, out):
+            return combine_rows(rows, position, weights, out)
+    res = torch.empty((tokens, width), dtype=rows.dtype, device=device) if out is None else out
+    code = _lib.load().rs_combine_rows(rows.data_ptr(), _ROW_DTYPES[rows.dtype], count, rows.stride(0),
+                                       position.data_ptr(), _ptr(weights), k, res.data_ptr(), tokens, width,
+                                       res.stride(0), _raw_stream(device.index))
+    if code:
+        _fail(code, "rs_combine_rows")
+    return res
 
 
 def combine_rows_backward(grad_out: torch.Tensor, position: torch.Tensor, rows: Optional[torch.Tensor] = None,
@@ -361,23 +377,24 @@ def combine_rows_backward(grad_out: torch.Tensor, position: torch.Tensor, rows: 
     count = tokens * k if out is None else out.shape[0]
     if rows is not None:
         count = rows.shape[0]
-        _rows(rows, "rows", device, grad_out.dtype, (count, width))
+        _rows(rows, "rows", device, (grad_out.dtype,), (count, width))
     elif grad_weights_out is not None:
         raise ValueError("grad_weights_out needs rows")
     if out is not None:
-        _rows(out, "out", device, grad_out.dtype, (count, width))
+        _rows(out, "out", device, (grad_out.dtype,), (count, width))
     if grad_weights_out is not None:
-        _flat(grad_weights_out, "grad_weights_out", (torch.float32,), device, (tokens, k))
-    call = _Call(device, stream, grad_out, position, rows, weights, out, grad_weights_out)
-
-    def body(handle):
-        grad = torch.empty((count, width), dtype=grad_out.dtype, device=device) if out is None else out
-        dots = grad_weights_out
-        if rows is not None and dots is None:
-            dots = torch.empty((tokens, k), dtype=torch.float32, device=device)
-        _ok(_lib.load().rs_combine_rows_backward(
-            grad_out.data_ptr(), _ROW_DTYPES[grad_out.dtype], tokens, width, grad_out.stride(0),
-            position.data_ptr(), _ptr(weights), k, _ptr(rows), 0 if rows is None else rows.stride(0),
-            grad.data_ptr(), grad.stride(0), count, _ptr(dots), handle), "rs_combine_rows_backward")
-        return grad if rows is None else (grad, dots)
-    return call.run(body)
+        _flat(grad_weights_out, "grad_weights_out", _F32, device, (tokens, k))
+    if _elsewhere(device, stream):
+        with _on(device, stream, grad_out, position, rows, weights, out, grad_weights_out):
+            return combine_rows_backward(grad_out, position, rows, weights, out, grad_weights_out)
+    grad = torch.empty((count, width), dtype=grad_out.dtype, device=device) if out is None else out
+    dots = grad_weights_out
+    if rows is not None and dots is None:
+        dots = torch.empty((tokens, k), dtype=torch.float32, device=device)
+    code = _lib.load().rs_combine_rows_backward(
+        grad_out.data_ptr(), _ROW_DTYPES[grad_out.dtype], tokens, width, grad_out.stride(0), position.data_ptr(),
+        _ptr(weights), k, _ptr(rows), 0 if rows is None else rows.stride(0), grad.data_ptr(), grad.stride(0), count,
+        _ptr(dots), _raw_stream(device.index))
+    if code:
+        _fail(code, "rs_combine_rows_backward")
+    return grad if rows is None else (grad, dots)
