@@ -860,7 +860,8 @@ constexpr int kMaxBatch = 8;  // slots of a token whose rows are in flight toget
 // same for a whole wave: its places and weights are scalars.
 // Without dots a wave takes one chunk of 64 columns of a token.  With dots the
 // LANES threads take the whole row, chunk after chunk, since their products
-// meet at the end; a join with dots holds one batch (k <= BATCH).
+// meet at the end, AT_ONCE chunks in flight together; a join with dots holds one
+// batch (k <= BATCH).
 // The loads of a batch are issued without a branch between them, which would
 // wait for the one before: an unused slot reads a used one's row.
 // The last access of a row is moved back to end with it where the width is no
@@ -868,22 +869,21 @@ constexpr int kMaxBatch = 8;  // slots of a token whose rows are in flight toget
 // result, and counted once in the products.
 constexpr int kNarrow = 32;
 
-template <class T, int LANES, int BATCH, bool SPREAD, bool WEIGHTED, bool DOTS>
+template <class T, int LANES, int BATCH, int AT_ONCE, bool SPREAD, bool WEIGHTED, bool DOTS>
 __global__ __launch_bounds__(kRowBlock) void wide_rows_kernel(const RowWork<T> a) {
     constexpr int W = kVec<T>;
     using Vec = typename VecOf<T, W>::type;
     constexpr int kPer = kRowBlock / LANES;
     constexpr int kWaves = LANES / 64;
-    static_assert(LANES == 64 || (DOTS && LANES == kRowBlock));
+    static_assert((LANES == 64 && AT_ONCE == 1) || (DOTS && LANES == kRowBlock));
     __shared__ float partial[kWaves > 1 ? BATCH : 1][kWaves > 1 ? kWaves : 1];
     const int lane = threadIdx.x % LANES;
     const int group = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / LANES);
     const size_t units = DOTS ? a.tokens : a.tokens * static_cast<size_t>(a.chunks);
-    const int vecs = (a.width + W - 1) / W;
-    for (size_t u = static_cast<size_t>(blockIdx.x) * kPer + group; u < units;
-         u += static_cast<size_t>(gridDim.x) * kPer) {
-        const size_t t = DOTS ? u : u / static_cast<unsigned>(a.chunks);
-        const int first = DOTS ? 0 : static_cast<int>(u % static_cast<unsigned>(a.chunks));
+    for (size_t unit = static_cast<size_t>(blockIdx.x) * kPer + group; unit < units;
+         unit += static_cast<size_t>(gridDim.x) * kPer) {
+        const size_t t = DOTS ? unit : unit / static_cast<unsigned>(a.chunks);
+        const int first = DOTS ? 0 : static_cast<int>(unit % static_cast<unsigned>(a.chunks));
         float acc[W] = {};
         for (int j0 = 0; j0 < a.k; j0 += BATCH) {
             // Lane i of each wave loads slot j0 + i; the wave reads them as scalars.
@@ -904,31 +904,43 @@ __global__ __launch_bounds__(kRowBlock) void wide_rows_kernel(const RowWork<T> a
                 some = slot[i].used ? slot[i].row : some;
             }
             float dot[BATCH] = {};
-            for (int c = first; c < (DOTS ? a.chunks : first + 1); ++c) {
-                const int vec = c * LANES + lane;
-                if (vec < vecs) {
-                    const int begin = vec * W;
-                    const int col = begin + W <= a.width ? begin : a.width - W;
-                    Vec raw[BATCH];
-                    if constexpr (!SPREAD || DOTS) {
-                        if (some >= 0) {
+            for (int c = first; c < (DOTS ? a.chunks : first + 1); c += AT_ONCE) {
+                int begin[AT_ONCE], col[AT_ONCE];
+                Vec raw[AT_ONCE][BATCH];
+                float x[AT_ONCE][W];
+#pragma unroll
+                for (int u = 0; u < AT_ONCE; ++u) {
+                    // Lanes behind the end read the last access, for nothing.
+                    begin[u] = ((c + u) * LANES + lane) * W;
+                    col[u] = begin[u] + W <= a.width ? begin[u] : a.width - W;
+                    if constexpr (SPREAD || DOTS) load_vec<T, W>(a.x + t * a.x_stride + col[u], x[u]);
+                }
+                if constexpr (!SPREAD || DOTS) {
+                    if (some >= 0) {
+#pragma unroll
+                        for (int u = 0; u < AT_ONCE; ++u) {
 #pragma unroll
                             for (int i = 0; i < BATCH; ++i) {
                                 const auto row = static_cast<size_t>(slot[i].used ? slot[i].row : some);
-                                raw[i] = *reinterpret_cast<const Vec *>(a.rows_in + row * a.rows_in_stride + col);
+                                raw[u][i] = *reinterpret_cast<const Vec *>(a.rows_in + row * a.rows_in_stride + col[u]);
                             }
                         }
                     }
-                    float x[W];
-                    if constexpr (SPREAD || DOTS) load_vec<T, W>(a.x + t * a.x_stride + col, x);
-                    if constexpr (SPREAD) {
+                }
+#pragma unroll
+                for (int u = 0; u < AT_ONCE; ++u) {
+                    const bool live = begin[u] < a.width;
+                    if (SPREAD && live) {
 #pragma unroll
                         for (int i = 0; i < BATCH; ++i) {
                             if (slot[i].row < 0) continue;
                             float v[W];
 #pragma unroll
-                            for (int e = 0; e < W; ++e) v[e] = !slot[i].used ? 0.0f : WEIGHTED ? w[i] * x[e] : x[e];
-                            store_vec<T, W>(a.rows_out + static_cast<size_t>(slot[i].row) * a.rows_out_stride + col, v);
+                            for (int e = 0; e < W; ++e) {
+                                v[e] = !slot[i].used ? 0.0f : WEIGHTED ? w[i] * x[u][e] : x[u][e];
+                            }
+                            store_vec<T, W>(a.rows_out + static_cast<size_t>(slot[i].row) * a.rows_out_stride + col[u],
+                                            v);
                         }
                     }
 #pragma unroll
@@ -936,7 +948,7 @@ __global__ __launch_bounds__(kRowBlock) void wide_rows_kernel(const RowWork<T> a
                         if ((SPREAD && !DOTS) || !slot[i].used) continue;
                         float f[W];
 #pragma unroll
-                        for (int e = 0; e < W; ++e) f[e] = static_cast<float>(raw[i][e]);
+                        for (int e = 0; e < W; ++e) f[e] = static_cast<float>(raw[u][i][e]);
                         if constexpr (!SPREAD) {
 #pragma unroll
                             for (int e = 0; e < W; ++e) {
@@ -944,20 +956,20 @@ __global__ __launch_bounds__(kRowBlock) void wide_rows_kernel(const RowWork<T> a
                             }
                         }
                         if constexpr (DOTS) {
-                            if (col == begin) {
+                            if (col[u] == begin[u]) {
 #pragma unroll
-                                for (int e = 0; e < W; ++e) dot[i] = __builtin_fmaf(x[e], f[e], dot[i]);
+                                for (int e = 0; e < W; ++e) dot[i] = __builtin_fmaf(x[u][e], f[e], dot[i]);
                             } else {
 #pragma unroll
                                 for (int e = 0; e < W; ++e) {
-                                    if (col + e >= begin) dot[i] = __builtin_fmaf(x[e], f[e], dot[i]);
+                                    if (col[u] + e >= begin[u]) dot[i] = __builtin_fmaf(x[u][e], f[e], dot[i]);
                                 }
                             }
                         }
                     }
                     if constexpr (!SPREAD) {
                         if (DOTS || j0 + BATCH >= a.k) {
-                            store_vec<T, W>(a.out + t * a.out_stride + col, acc);
+                            if (live) store_vec<T, W>(a.out + t * a.out_stride + col[u], acc);
 #pragma unroll
                             for (int e = 0; e < W; ++e) acc[e] = 0.0f;
                         }
