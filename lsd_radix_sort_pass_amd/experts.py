@@ -41,6 +41,7 @@ MAX_CHOICES = 64        # RS_MAX_CHOICES
 
 _ROW_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}      # rs_dtype
 _GATES = {"softmax": 0, "sigmoid": 1}                                      # rs_gate
+_Tensor = torch.Tensor
 _I32, _F32, _U8 = (torch.int32,), (torch.float32,), (torch.uint8,)
 _SORT_FN = {torch.int32: "rs_sort_experts_i32", torch.int64: "rs_sort_experts_i64"}
 
@@ -82,16 +83,16 @@ def _refuse(t, name, dtypes, dim, device, shape, rows) -> None:
 def _rows(t, name, device=None, dtypes=_ROW_DTYPES, shape=None) -> None:
     """Checks a 2-D float tensor with consecutive elements in a row, any row
     stride."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == 2 and t.is_contiguous()
-            and not t.requires_grad and (device is None or t.device == device)
+    if not (isinstance(t, _Tensor) and t.dtype in dtypes and t.dim() == 2 and t.is_contiguous()
+            and not t.requires_grad and (t.is_cuda if device is None else t.get_device() == device.index)
             and (shape is None or t.shape == shape)):
         _refuse(t, name, dtypes, 2, device, shape, True)
 
 
 def _flat(t, name, dtypes, device, shape=None, dim=None) -> None:
     """Checks a contiguous tensor."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.is_contiguous()
-            and not t.requires_grad and (device is None or t.device == device)
+    if not (isinstance(t, _Tensor) and t.dtype in dtypes and t.is_contiguous() and not t.requires_grad
+            and (t.is_cuda if device is None else t.get_device() == device.index)
             and (shape is None or t.shape == shape) and (dim is None or t.dim() == dim)):
         _refuse(t, name, dtypes, dim, device, shape, False)
 
@@ -175,8 +176,8 @@ def route_topk(logits: torch.Tensor, k: int, mode: str = "softmax", renormalize:
     if _elsewhere(device, stream):
         with _on(device, stream, logits, weights_out, experts_out):
             return route_topk(logits, k, mode, renormalize, scale, weights_out, experts_out)
-    w = torch.empty((tokens, k), dtype=torch.float32, device=device) if weights_out is None else weights_out
-    e = torch.empty((tokens, k), dtype=torch.int32, device=device) if experts_out is None else experts_out
+    w = torch.empty(tokens, k, dtype=torch.float32, device=device) if weights_out is None else weights_out
+    e = torch.empty(tokens, k, dtype=torch.int32, device=device) if experts_out is None else experts_out
     code = _lib.load().rs_route_topk(logits.data_ptr(), _ROW_DTYPES[logits.dtype], tokens, experts, logits.stride(0),
                                      k, gate, 1 if renormalize else 0, scale, w.data_ptr(), e.data_ptr(),
                                      _raw_stream(device.index))
@@ -205,7 +206,7 @@ def route_topk_backward(logits: torch.Tensor, experts: torch.Tensor, grad_weight
     if _elsewhere(device, stream):
         with _on(device, stream, logits, experts, grad_weights, out):
             return route_topk_backward(logits, experts, grad_weights, mode, renormalize, scale, out)
-    grad = torch.empty((tokens, count), dtype=logits.dtype, device=device) if out is None else out
+    grad = logits.new_empty(tokens, count) if out is None else out
     code = _lib.load().rs_route_topk_backward(logits.data_ptr(), _ROW_DTYPES[logits.dtype], tokens, count,
                                               logits.stride(0), experts.data_ptr(), grad_weights.data_ptr(), k, gate,
                                               1 if renormalize else 0, scale, grad.data_ptr(), grad.stride(0),
@@ -251,7 +252,7 @@ def sort_experts(experts: torch.Tensor, num_experts: int, first_expert: int = 0,
             return sort_experts(experts, num, first_expert, order_out, position_out, offsets_out, temp)
     lib = _lib.load()
     order = torch.empty(n, dtype=torch.int32, device=device) if order_out is None else order_out
-    position = torch.empty(experts.shape, dtype=torch.int32, device=device) if position_out is None else position_out
+    position = torch.empty_like(experts, dtype=torch.int32) if position_out is None else position_out
     offsets = torch.empty(num + 1, dtype=torch.int32, device=device) if offsets_out is None else offsets_out
     if temp is None:
         need = lib.rs_temp_bytes_experts(n, num)
@@ -288,7 +289,7 @@ def dispatch_rows(x: torch.Tensor, position: torch.Tensor, weights: Optional[tor
     if _elsewhere(device, stream):
         with _on(device, stream, x, position, weights, out):
             return dispatch_rows(x, position, weights, out)
-    rows = torch.empty((tokens * k, width), dtype=x.dtype, device=device) if out is None else out
+    rows = x.new_empty(tokens * k, width) if out is None else out
     code = _lib.load().rs_dispatch_rows(x.data_ptr(), _ROW_DTYPES[x.dtype], tokens, width, x.stride(0),
                                         position.data_ptr(), _ptr(weights), k, rows.data_ptr(), rows.shape[0],
                                         rows.stride(0), _raw_stream(device.index))
@@ -320,10 +321,10 @@ def dispatch_rows_backward(grad_rows: torch.Tensor, position: torch.Tensor, x: O
     if _elsewhere(device, stream):
         with _on(device, stream, grad_rows, position, x, weights, out, grad_weights_out):
             return dispatch_rows_backward(grad_rows, position, x, weights, out, grad_weights_out)
-    grad = torch.empty((tokens, width), dtype=grad_rows.dtype, device=device) if out is None else out
+    grad = grad_rows.new_empty(tokens, width) if out is None else out
     dots = grad_weights_out
     if x is not None and dots is None:
-        dots = torch.empty((tokens, k), dtype=torch.float32, device=device)
+        dots = torch.empty(tokens, k, dtype=torch.float32, device=device)
     code = _lib.load().rs_dispatch_rows_backward(
         grad_rows.data_ptr(), _ROW_DTYPES[grad_rows.dtype], count, grad_rows.stride(0), position.data_ptr(),
         _ptr(weights), k, _ptr(x), 0 if x is None else x.stride(0), grad.data_ptr(), grad.stride(0), _ptr(dots),
@@ -350,7 +351,7 @@ def combine_rows(rows: torch.Tensor, position: torch.Tensor, weights: Optional[t
     if _elsewhere(device, stream):
         with _on(device, stream, rows, position, weights, out):
             return combine_rows(rows, position, weights, out)
-    res = torch.empty((tokens, width), dtype=rows.dtype, device=device) if out is None else out
+    res = rows.new_empty(tokens, width) if out is None else out
     code = _lib.load().rs_combine_rows(rows.data_ptr(), _ROW_DTYPES[rows.dtype], count, rows.stride(0),
                                        position.data_ptr(), _ptr(weights), k, res.data_ptr(), tokens, width,
                                        res.stride(0), _raw_stream(device.index))
@@ -387,10 +388,10 @@ def combine_rows_backward(grad_out: torch.Tensor, position: torch.Tensor, rows: 
     if _elsewhere(device, stream):
         with _on(device, stream, grad_out, position, rows, weights, out, grad_weights_out):
             return combine_rows_backward(grad_out, position, rows, weights, out, grad_weights_out)
-    grad = torch.empty((count, width), dtype=grad_out.dtype, device=device) if out is None else out
+    grad = grad_out.new_empty(count, width) if out is None else out
     dots = grad_weights_out
     if rows is not None and dots is None:
-        dots = torch.empty((tokens, k), dtype=torch.float32, device=device)
+        dots = torch.empty(tokens, k, dtype=torch.float32, device=device)
     code = _lib.load().rs_combine_rows_backward(
         grad_out.data_ptr(), _ROW_DTYPES[grad_out.dtype], tokens, width, grad_out.stride(0), position.data_ptr(),
         _ptr(weights), k, _ptr(rows), 0 if rows is None else rows.stride(0), grad.data_ptr(), grad.stride(0), count,
