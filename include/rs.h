@@ -296,8 +296,8 @@ rs_status rs_sort_keys_u32_noalloc(const uint32_t *keys_in, uint32_t *keys_out, 
  * Weights, chosen experts, places and offsets are contiguous.  Sums and gates
  * are computed in float32 and rounded once, to nearest even, where the result
  * is 16 bits wide; every sum has a fixed order, so results repeat bit for bit.
- * Outputs may not overlap an input or another output.  The calls allocate
- * nothing, only enqueue on `stream` (of the current device), keep no state
+ * An output's address range, from its first row to its last, may not overlap
+ * that of an input or another output.  The calls allocate nothing, only enqueue on `stream` (of the current device), keep no state
  * and can be captured into a graph.  Argument errors are reported before any
  * HIP call, as for the sorts: RS_ERROR_INVALID_VALUE for a NULL or misaligned
  * pointer, a size outside the stated limits, an unknown type or gate, or an
@@ -350,8 +350,9 @@ rs_status rs_sort_experts_i64(const int64_t *ids, size_t n, int first, int exper
  * (weights NULL: x[t]), and zeros for a dropped slot, so the places of
  * rs_sort_experts fill every row.  position: as rs_sort_experts writes it; a
  * place at or beyond num_rows is skipped, a row that no slot names is left as
- * it was, and one that several name holds one of theirs.  1 <= k <=
- * RS_MAX_CHOICES, 1 <= width <= RS_MAX_ROW_WIDTH, num_rows <= RS_MAX_SLOTS. */
+ * it was, and one that several name (never so after rs_sort_experts) gets each
+ * element from any of them.  1 <= k <= RS_MAX_CHOICES, 1 <= width <=
+ * RS_MAX_ROW_WIDTH, num_rows <= RS_MAX_SLOTS. */
 rs_status rs_dispatch_rows(const void *x, int dtype, size_t tokens, int width, size_t x_stride,
                            const int32_t *position, const float *weights, int k, void *rows, size_t num_rows,
                            size_t rows_stride, hipStream_t stream);

@@ -155,3 +155,16 @@ def test_oracle_gradient_matches_differences(mode, renorm):
             up[t, i] += h
             down[t, i] -= h
             assert abs((loss(up) - loss(down)) / (2 * h) - grad[t, i]) < 1e-7
+
+
+def test_oracle_rows_are_each_other_transposed():
+    """<spread(x), y> = <x, join(y)> for any x and y, and the products are the
+    derivative of either side in the weights."""
+    rng = np.random.default_rng(4)
+    T, k, H = 7, 3, 5
+    position = rng.permutation(T * k).reshape(T, k)
+    position = np.where(rng.random((T, k)) < 0.3, ~position, position)
+    w, x, y = rng.normal(size=(T, k)), rng.normal(size=(T, H)), rng.normal(size=(T * k, H))
+    there = (eo.spread(x, position, w, np.zeros((T * k, H))) * y).sum()
+    assert abs(there - (x * eo.join(y, position, w)[0]).sum()) < 1e-12
+    assert abs(there - (w * eo.dots(x, y, position)[0]).sum()) < 1e-12

@@ -172,6 +172,28 @@ def test_route_many_rows():
     assert (w.double() - exact).abs().max().item() < 40 * eo.U32
 
 
+@pytest.mark.parametrize("E,k", [(256, 8), (255, 7), (64, 8), (512, 16), (400, 12), (1024, 32), (1000, 8), (1024, 64)])
+def test_route_choice_over_many_rows(E, k):
+    """Rows enough for every way of choosing, among them rows with more
+    candidates than lanes and rows with a few values that repeat.  Weights
+    (softmax over the row) within 20 + E / 16 half steps and the differences
+    from the maximum, below 40 here."""
+    T = 8192
+    note(f"route_topk T={T} E={E} k={k}")
+    logits = torch.randn(T, E, device="cuda") * 2
+    logits[::5] = (logits[::5] * 2).round() / 2
+    logits[1::97] = float("-inf")
+    logits[1::97, 3:3 + k // 2] = 1.5
+    for dtype in DTYPES.values():
+        l = logits.to(dtype)
+        w, e = rs.route_topk(l, k)
+        top = torch.argsort(l.float(), dim=1, descending=True, stable=True)[:, :k]
+        barred = torch.gather(l, 1, top) == float("-inf")
+        assert torch.equal(e.long(), top.masked_fill(barred, -1))
+        exact = torch.gather(torch.softmax(l.double(), 1), 1, top)
+        assert ((w.double() - exact).abs() <= exact * eo.U32 * (60 + E / 16) + 2.0 ** -125).all()
+
+
 # ---------------------------------------------------------------------------
 # Slots sorted by expert
 # ---------------------------------------------------------------------------
@@ -216,21 +238,23 @@ def test_sort_experts_shapes_of_input():
     check_sort(torch.from_numpy(edge).cuda(), 2**31 - 2, 2)
 
 
-@pytest.mark.parametrize("n", [2_097_152, 2_097_153, 5_000_011])
-def test_sort_experts_many(n):
-    """More slots than the workgroups hold in one tile each: numpy's stable
-    sort as the definition."""
-    note(f"sort_experts n={n}")
+@pytest.mark.parametrize("experts", [9, 128, 257, 1024])
+@pytest.mark.parametrize("n", [262_144, 1_048_577, 2_097_152, 2_097_153, 5_000_011])
+def test_sort_experts_many(n, experts):
+    """Tables of few and many counts, one tile and several for a workgroup:
+    numpy's stable sort as the definition."""
+    note(f"sort_experts n={n} experts={experts}")
     rng = np.random.default_rng(n)
-    ids = rng.integers(-3, 300, n).astype(np.int32)
-    res = rs.sort_experts(torch.from_numpy(ids).cuda(), 257)
-    key = np.where((ids < 0) | (ids >= 257), 257, ids)
+    ids = rng.integers(-3, experts + 43, n).astype(np.int64 if n % 2 else np.int32)
+    ids[n // 3:n // 3 + 20_000] = -1
+    res = rs.sort_experts(torch.from_numpy(ids).cuda(), experts)
+    key = np.where((ids < 0) | (ids >= experts), experts, ids)
     order = np.argsort(key, kind="stable")
     place = np.empty(n, dtype=np.int64)
     place[order] = np.arange(n)
     assert np.array_equal(host(res.order), order)
-    assert np.array_equal(host(res.position), np.where(key == 257, ~place, place))
-    assert np.array_equal(host(res.offsets), np.searchsorted(key[order], np.arange(258)))
+    assert np.array_equal(host(res.position), np.where(key == experts, ~place, place))
+    assert np.array_equal(host(res.offsets), np.searchsorted(key[order], np.arange(experts + 1)))
 
 
 def test_sort_experts_temp_and_outputs():
@@ -629,3 +653,22 @@ def test_results_repeat():
     for name in buf[0]:
         if name != "temp":
             assert torch.equal(buf[0][name], buf[1][name]), name
+
+
+def test_kernel_timing():
+    """The calls' launches are timed under their own kernel kinds."""
+    note("kernel timing")
+    from lsd_radix_sort_pass_amd import _lib
+    logits, x = torch.randn(64, 16, device="cuda"), torch.randn(64, 256, device="cuda")
+    rs.prof_reset()
+    rs.prof_enable(True)
+    try:
+        w, e = rs.route_topk(logits, 2)
+        s = rs.sort_experts(e, 16)
+        rs.combine_rows(rs.dispatch_rows(x, s.position), s.position, w)
+        rs.sort_experts(torch.zeros(100_000, dtype=torch.int32, device="cuda"), 16)
+    finally:
+        rs.prof_enable(False)
+    assert [rs.prof_summary(kind)[0] for kind in (_lib.RS_KERNEL_ROUTE, _lib.RS_KERNEL_EXPERT, _lib.RS_KERNEL_ROWS)] \
+        == [1, 3, 2]
+    rs.prof_reset()
