@@ -10,14 +10,13 @@ import argparse
 import os
 import subprocess
 import sys
-import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "librs.so")
-SOURCES = [os.path.join(CSRC, "rs.hip"), os.path.join(CSRC, "experts.hip")]
+SOURCES = [os.path.join(CSRC, "librs.hip")]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -25,6 +24,7 @@ HIPCC_FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
+    "-shared",
     "-Wall",
     # Packed FP32 instructions are kept out of every code object.
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -40,30 +40,15 @@ def hipcc() -> str:
 
 def build(save_temps: str | None = None, verbose: bool = False) -> str:
     out_tmp = LIB + ".tmp"
-    with tempfile.TemporaryDirectory() as objects:
-        cwd = PKG
-        extra = []
-        if save_temps:
-            os.makedirs(save_temps, exist_ok=True)
-            extra = ["-save-temps"]
-            cwd = save_temps
-        # One object per source, compiled side by side, then linked.
-        jobs, objs = [], []
-        for source in SOURCES:
-            obj = os.path.join(objects, os.path.basename(source) + ".o")
-            cmd = [hipcc(), *extra, *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", "-o", obj, source]
-            if verbose:
-                print(" ".join(cmd), flush=True)
-            jobs.append((cmd, subprocess.Popen(cmd, cwd=cwd)))
-            objs.append(obj)
-        codes = [(cmd, job.wait()) for cmd, job in jobs]
-        for cmd, code in codes:
-            if code != 0:
-                raise subprocess.CalledProcessError(code, cmd)
-        link = [hipcc(), f"--offload-arch={ARCH}", "-fPIC", "-shared", "-o", out_tmp, *objs]
-        if verbose:
-            print(" ".join(link), flush=True)
-        subprocess.run(link, check=True, cwd=PKG)
+    cmd = [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-o", out_tmp, *SOURCES]
+    cwd = PKG
+    if save_temps:
+        os.makedirs(save_temps, exist_ok=True)
+        cmd.insert(1, "-save-temps")
+        cwd = save_temps
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True, cwd=cwd)
     os.replace(out_tmp, LIB)
     return LIB
 

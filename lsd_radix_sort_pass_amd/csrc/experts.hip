@@ -1,20 +1,11 @@
 // experts.hip -- C ABI of the mixture-of-experts calls (routing, slots sorted
 // by expert, rows dispatched and combined): argument checks and launches.
-#include <hip/hip_runtime.h>
-
-#include <stdint.h>
-
+// Compiled behind rs.hip (librs.hip), whose helpers it uses.
 #include "experts.hpp"
-#include "launch.hpp"
-#include "rs.h"
-#include "rs_prof.h"
 
 namespace {
 
-using namespace rs_host;
-
 constexpr unsigned kMaxGrid = 1u << 20;  // workgroups; the kernels stride over the rest
-constexpr size_t kTempAlign = 256;
 
 int dtype_bytes(int dtype) {
     switch (dtype) {
@@ -141,7 +132,7 @@ size_t expert_temp(size_t n, int experts) {
     if (n <= kOneGroup) return 0;
     // The table, and a row of totals.
     const size_t bytes = (size_t{expert_plan(n).chunks} + 1) * rs::table_stride(static_cast<uint32_t>(experts)) * 4;
-    return (bytes + kTempAlign - 1) / kTempAlign * kTempAlign;
+    return align_up(bytes);
 }
 
 bool good_experts(size_t n, int experts) {
