@@ -102,7 +102,7 @@ bool good_route(int dtype, size_t tokens, int experts, int k, int gate) {
 // Up to kOneGroup slots one workgroup places them all: 8192 slots of 256
 // experts take it 6 us, the two launches below 8.4; 12000 slots would take 8.7
 // (16 slots a thread) against 8.5.  Above, the slots are cut into at most
-// kMaxChunks chunks of whole tiles (one per CU), counted by one launch and
+// rs::kMaxChunks chunks of whole tiles (one per CU), counted by one launch and
 // placed by another, which sums the table of counts itself while that has at
 // most kSumWords words, since every workgroup reads it: 2^18 slots of 256
 // experts (64 KiB) 10.5 us against 12.1 with a launch that scans it between
@@ -111,7 +111,6 @@ bool good_route(int dtype, size_t tokens, int experts, int k, int gate) {
 constexpr size_t kOneGroup = 8 * rs::kPlaceBlock;
 constexpr int kTileItems = 4;
 constexpr size_t kTile = size_t{kTileItems} * rs::kPlaceBlock;
-constexpr size_t kMaxChunks = 256;
 constexpr size_t kSumWords = 32768;
 
 struct ExpertPlan {
@@ -122,7 +121,7 @@ struct ExpertPlan {
 ExpertPlan expert_plan(size_t n) {
     ExpertPlan p;
     const size_t tiles = (n + kTile - 1) / kTile;
-    const size_t per_chunk = (tiles + kMaxChunks - 1) / kMaxChunks;
+    const size_t per_chunk = (tiles + rs::kMaxChunks - 1) / rs::kMaxChunks;
     p.chunk = (per_chunk ? per_chunk : 1) * kTile;
     p.chunks = static_cast<unsigned>(n ? (n + p.chunk - 1) / p.chunk : 1);
     return p;

@@ -566,15 +566,16 @@ __global__ __launch_bounds__(kPlaceBlock) void expert_count_kernel(const ID *__r
     for (uint32_t e = threadIdx.x; e < stride; e += kPlaceBlock) count[e] = 0;
     __syncthreads();
     for (size_t tile = lo + threadIdx.x; tile < hi; tile += static_cast<size_t>(kPlaceBlock) * ITEMS) {
-        uint32_t key[ITEMS];
+        ID id[ITEMS];  // all in flight: beyond the chunk the last slot, not counted
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             const size_t slot = tile + static_cast<size_t>(i) * kPlaceBlock;
-            key[i] = slot < hi ? expert_key(ids[slot], first, experts) : experts;
+            id[i] = ids[slot < hi ? slot : hi - 1];
         }
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            if (key[i] < experts) atomicAdd(&count[key[i]], 1u);
+            const uint32_t key = expert_key(id[i], first, experts);
+            if (key < experts && tile + static_cast<size_t>(i) * kPlaceBlock < hi) atomicAdd(&count[key], 1u);
         }
     }
     __syncthreads();
@@ -585,46 +586,38 @@ __global__ __launch_bounds__(kPlaceBlock) void expert_count_kernel(const ID *__r
 
 // Exclusive sums of each expert's column of the table, in place, and the
 // columns' totals.  A workgroup takes 64 columns; a thread four of them over
-// consecutive rows, 64 threads per column.
-constexpr int kScanQuads = 16;
-constexpr int kScanSplits = kPlaceBlock / kScanQuads;
+// kScanRows consecutive rows, held in registers.
+constexpr uint32_t kMaxChunks = 256;  // rows of the table
+constexpr uint32_t kScanQuads = 16;
+constexpr uint32_t kScanSplits = kPlaceBlock / kScanQuads;
+constexpr uint32_t kScanRows = kMaxChunks / kScanSplits;
 
 __global__ __launch_bounds__(kPlaceBlock) void expert_scan_kernel(uint32_t *__restrict__ table, uint32_t chunks,
                                                                   uint32_t experts, uint32_t *__restrict__ totals) {
     __shared__ uint4 sums[kScanSplits][kScanQuads];
     const uint32_t stride = table_stride(experts) / 4;
     const uint32_t q = threadIdx.x % kScanQuads, split = threadIdx.x / kScanQuads;
-    const uint32_t quad = blockIdx.x * kScanQuads + q;
-    const uint32_t rows = (chunks + kScanSplits - 1) / kScanSplits;
-    const uint32_t lo = split * rows, hi = lo + rows < chunks ? lo + rows : chunks;
-    uint4 *const column = reinterpret_cast<uint4 *>(table) + quad;
-    const bool mine = quad < stride;
+    const uint32_t quad = blockIdx.x * kScanQuads + q, lo = split * kScanRows;
+    uint4 *const column = reinterpret_cast<uint4 *>(table) + (quad < stride ? quad : stride - 1);
     const auto add = [](uint4 &a, const uint4 &b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; };
-    constexpr int kHold = 4;  // rows kept in registers between the two passes
-    uint4 held[kHold], sum = make_uint4(0, 0, 0, 0);
+    uint4 held[kScanRows], sum = make_uint4(0, 0, 0, 0), run = sum;
 #pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-        held[i] = mine && lo + i < hi ? column[static_cast<size_t>(lo + i) * stride] : make_uint4(0, 0, 0, 0);
+    for (uint32_t i = 0; i < kScanRows; ++i) {
+        held[i] = column[static_cast<size_t>(lo + i < chunks ? lo + i : chunks - 1) * stride];
     }
 #pragma unroll
-    for (int i = 0; i < kHold; ++i) add(sum, held[i]);
-    if (mine) {
-        for (uint32_t b = lo + kHold; b < hi; ++b) add(sum, column[static_cast<size_t>(b) * stride]);
+    for (uint32_t i = 0; i < kScanRows; ++i) {
+        if (lo + i >= chunks) held[i] = make_uint4(0, 0, 0, 0);
+        add(sum, held[i]);
     }
     sums[split][q] = sum;
     __syncthreads();
-    uint4 run = make_uint4(0, 0, 0, 0);
     for (uint32_t i = 0; i < split; ++i) add(run, sums[i][q]);
-    if (!mine) return;
+    if (quad >= stride) return;
 #pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-        if (lo + i < hi) column[static_cast<size_t>(lo + i) * stride] = run;
+    for (uint32_t i = 0; i < kScanRows; ++i) {
+        if (lo + i < chunks) column[static_cast<size_t>(lo + i) * stride] = run;
         add(run, held[i]);
-    }
-    for (uint32_t b = lo + kHold; b < hi; ++b) {
-        const uint4 c = column[static_cast<size_t>(b) * stride];
-        column[static_cast<size_t>(b) * stride] = run;
-        add(run, c);
     }
     if (split == kScanSplits - 1) reinterpret_cast<uint4 *>(totals)[quad] = run;
 }
@@ -669,10 +662,17 @@ __global__ __launch_bounds__(kPlaceBlock) void expert_place_kernel(const ID *__r
     uint32_t key[ITEMS], rank[ITEMS];
     const uint32_t mine = wave * 64 * ITEMS + lane;  // the thread's first slot in a tile
     const auto load_keys = [&](size_t tile) {
+        ID id[ITEMS] = {};  // all in flight: beyond the chunk the last slot, not used
+        if (tile < hi) {
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) {
+                const size_t slot = tile + mine + i * 64;
+                id[i] = ids[slot < hi ? slot : hi - 1];
+            }
+        }
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            const size_t slot = tile + mine + i * 64;
-            key[i] = slot < hi ? expert_key(ids[slot], first, experts) : 0xFFFFFFFFu;
+            key[i] = tile + mine + i * 64 < hi ? expert_key(id[i], first, experts) : 0xFFFFFFFFu;
         }
     };
     // The workgroup's sum of x below this thread, and all of it.
@@ -694,14 +694,22 @@ __global__ __launch_bounds__(kPlaceBlock) void expert_place_kernel(const ID *__r
         uint32_t quads = 16;
         while (quads * 4 < stride) quads *= 2;
         const uint32_t splits = kPlaceBlock / quads, quad = tid % quads, split = tid / quads;
+        const uint4 *const column = reinterpret_cast<const uint4 *>(table) + (quad * 4 < stride ? quad : 0);
         uint4 all = make_uint4(0, 0, 0, 0), ahead = make_uint4(0, 0, 0, 0);
-        if (quad * 4 < stride) {
-#pragma unroll 8
-            for (uint32_t b = split; b < gridDim.x; b += splits) {
-                const uint4 c = reinterpret_cast<const uint4 *>(table)[static_cast<size_t>(b) * (stride / 4) + quad];
-                const uint32_t m = b < blockIdx.x ? 0xFFFFFFFFu : 0u;
-                all.x += c.x, all.y += c.y, all.z += c.z, all.w += c.w;
-                ahead.x += c.x & m, ahead.y += c.y & m, ahead.z += c.z & m, ahead.w += c.w & m;
+        constexpr uint32_t kRows = 8;  // in flight: beyond the table its last row, not added
+        for (uint32_t b = split; b < gridDim.x; b += kRows * splits) {
+            uint4 c[kRows];
+#pragma unroll
+            for (uint32_t i = 0; i < kRows; ++i) {
+                const uint32_t row = b + i * splits < gridDim.x ? b + i * splits : gridDim.x - 1;
+                c[i] = column[static_cast<size_t>(row) * (stride / 4)];
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < kRows; ++i) {
+                const uint32_t m = b + i * splits < gridDim.x ? 0xFFFFFFFFu : 0u;
+                const uint32_t m2 = b + i * splits < blockIdx.x ? 0xFFFFFFFFu : 0u;
+                all.x += c[i].x & m, all.y += c[i].y & m, all.z += c[i].z & m, all.w += c[i].w & m;
+                ahead.x += c[i].x & m2, ahead.y += c[i].y & m2, ahead.z += c[i].z & m2, ahead.w += c[i].w & m2;
             }
         }
         const auto meet = [&](const uint4 &part) {

@@ -114,9 +114,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _elsewhere(device, stream) -> bool:
-    """Whether a call has to change the current device or stream first."""
-    return stream is not None or device.index != torch.cuda.current_device()
+# The current device; a call asks only once it has a device tensor.
+_current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 @contextlib.contextmanager
@@ -142,17 +141,12 @@ def _fail(code: int, name: str) -> None:
     raise RadixSortError(code, name)
 
 
-def _gate(mode) -> int:
-    if mode not in _GATES:
-        raise ValueError(f"mode must be one of {', '.join(_GATES)} (got {mode!r})")
-    return _GATES[mode]
+def _refuse_mode(mode) -> None:
+    raise ValueError(f"mode must be one of {', '.join(_GATES)} (got {mode!r})")
 
 
-def _choices(k, experts) -> int:
-    k = int(k)
-    if not 1 <= k <= min(experts, MAX_CHOICES):
-        raise ValueError(f"k must be between 1 and min(experts, {MAX_CHOICES}) (got {k} of {experts} experts)")
-    return k
+def _refuse_k(k, experts) -> None:
+    raise ValueError(f"k must be between 1 and min(experts, {MAX_CHOICES}) (got {k} of {experts} experts)")
 
 
 def route_topk(logits: torch.Tensor, k: int, mode: str = "softmax", renormalize: bool = False, scale: float = 1.0,
@@ -168,18 +162,22 @@ def route_topk(logits: torch.Tensor, k: int, mode: str = "softmax", renormalize:
     bars the row from an expert; slots without one get expert -1, weight 0."""
     _rows(logits, "logits")
     tokens, experts = logits.shape
-    k, gate, device = _choices(k, experts), _gate(mode), logits.device
+    device = logits.device
+    if not 1 <= k <= experts or k > MAX_CHOICES:
+        _refuse_k(k, experts)
+    if mode not in _GATES:
+        _refuse_mode(mode)
     if weights_out is not None:
         _flat(weights_out, "weights_out", _F32, device, (tokens, k))
     if experts_out is not None:
         _flat(experts_out, "experts_out", _I32, device, (tokens, k))
-    if _elsewhere(device, stream):
+    if stream is not None or device.index != _current():
         with _on(device, stream, logits, weights_out, experts_out):
             return route_topk(logits, k, mode, renormalize, scale, weights_out, experts_out)
     w = torch.empty(tokens, k, dtype=torch.float32, device=device) if weights_out is None else weights_out
     e = torch.empty(tokens, k, dtype=torch.int32, device=device) if experts_out is None else experts_out
     code = _lib.load().rs_route_topk(logits.data_ptr(), _ROW_DTYPES[logits.dtype], tokens, experts, logits.stride(0),
-                                     k, gate, 1 if renormalize else 0, scale, w.data_ptr(), e.data_ptr(),
+                                     k, _GATES[mode], 1 if renormalize else 0, scale, w.data_ptr(), e.data_ptr(),
                                      _raw_stream(device.index))
     if code:
         _fail(code, "rs_route_topk")
@@ -195,21 +193,25 @@ def route_topk_backward(logits: torch.Tensor, experts: torch.Tensor, grad_weight
     call's."""
     _rows(logits, "logits")
     tokens, count = logits.shape
-    device, gate = logits.device, _gate(mode)
+    device = logits.device
     _flat(experts, "experts", _I32, device, None, 2)
-    k = _choices(experts.shape[1], count)
-    if experts.shape[0] != tokens:
+    rows, k = experts.shape
+    if not 1 <= k <= count or k > MAX_CHOICES:
+        _refuse_k(k, count)
+    if mode not in _GATES:
+        _refuse_mode(mode)
+    if rows != tokens:
         raise ValueError("experts must have a row for each row of logits")
     _flat(grad_weights, "grad_weights", _F32, device, (tokens, k))
     if out is not None:
         _rows(out, "out", device, (logits.dtype,), (tokens, count))
-    if _elsewhere(device, stream):
+    if stream is not None or device.index != _current():
         with _on(device, stream, logits, experts, grad_weights, out):
             return route_topk_backward(logits, experts, grad_weights, mode, renormalize, scale, out)
     grad = logits.new_empty(tokens, count) if out is None else out
     code = _lib.load().rs_route_topk_backward(logits.data_ptr(), _ROW_DTYPES[logits.dtype], tokens, count,
-                                              logits.stride(0), experts.data_ptr(), grad_weights.data_ptr(), k, gate,
-                                              1 if renormalize else 0, scale, grad.data_ptr(), grad.stride(0),
+                                              logits.stride(0), experts.data_ptr(), grad_weights.data_ptr(), k,
+                                              _GATES[mode], 1 if renormalize else 0, scale, grad.data_ptr(), grad.stride(0),
                                               _raw_stream(device.index))
     if code:
         _fail(code, "rs_route_topk_backward")
@@ -247,7 +249,7 @@ def sort_experts(experts: torch.Tensor, num_experts: int, first_expert: int = 0,
         _flat(offsets_out, "offsets_out", _I32, device, (num + 1,))
     if temp is not None:
         _flat(temp, "temp", _U8, device)
-    if _elsewhere(device, stream):
+    if stream is not None or device.index != _current():
         with _on(device, stream, experts, order_out, position_out, offsets_out, temp):
             return sort_experts(experts, num, first_expert, order_out, position_out, offsets_out, temp)
     lib = _lib.load()
@@ -286,7 +288,7 @@ def dispatch_rows(x: torch.Tensor, position: torch.Tensor, weights: Optional[tor
         _rows(out, "out", device, (x.dtype,))
         if out.shape[1] != width:
             raise ValueError("out must have the width of x")
-    if _elsewhere(device, stream):
+    if stream is not None or device.index != _current():
         with _on(device, stream, x, position, weights, out):
             return dispatch_rows(x, position, weights, out)
     rows = x.new_empty(tokens * k, width) if out is None else out
@@ -318,7 +320,7 @@ def dispatch_rows_backward(grad_rows: torch.Tensor, position: torch.Tensor, x: O
         _rows(out, "out", device, (grad_rows.dtype,), (tokens, width))
     if grad_weights_out is not None:
         _flat(grad_weights_out, "grad_weights_out", _F32, device, (tokens, k))
-    if _elsewhere(device, stream):
+    if stream is not None or device.index != _current():
         with _on(device, stream, grad_rows, position, x, weights, out, grad_weights_out):
             return dispatch_rows_backward(grad_rows, position, x, weights, out, grad_weights_out)
     grad = grad_rows.new_empty(tokens, width) if out is None else out
@@ -348,7 +350,7 @@ def combine_rows(rows: torch.Tensor, position: torch.Tensor, weights: Optional[t
     tokens, k = _places(position, weights, device)
     if out is not None:
         _rows(out, "out", device, (rows.dtype,), (tokens, width))
-    if _elsewhere(device, stream):
+    if stream is not None or device.index != _current():
         with _on(device, stream, rows, position, weights, out):
             return combine_rows(rows, position, weights, out)
     res = rows.new_empty(tokens, width) if out is None else out
@@ -385,7 +387,7 @@ def combine_rows_backward(grad_out: torch.Tensor, position: torch.Tensor, rows: 
         _rows(out, "out", device, (grad_out.dtype,), (count, width))
     if grad_weights_out is not None:
         _flat(grad_weights_out, "grad_weights_out", _F32, device, (tokens, k))
-    if _elsewhere(device, stream):
+    if stream is not None or device.index != _current():
         with _on(device, stream, grad_out, position, rows, weights, out, grad_weights_out):
             return combine_rows_backward(grad_out, position, rows, weights, out, grad_weights_out)
     grad = grad_out.new_empty(count, width) if out is None else out
