@@ -100,18 +100,18 @@ bool good_route(int dtype, size_t tokens, int experts, int k, int gate) {
 // Slots sorted by expert
 // ---------------------------------------------------------------------------
 // Up to kOneGroup slots one workgroup places them all: 8192 slots of 256
-// experts take it 6 us, the two launches below 8.4; 12000 slots would take 8.7
-// (16 slots a thread) against 8.5.  Above, the slots are cut into at most
+// experts take it 6.1 us, the two launches below 8.0; for 12000 slots (16 a
+// thread) it would take 8.7, as they do.  Above, the slots are cut into at most
 // rs::kMaxChunks chunks of whole tiles (one per CU), counted by one launch and
 // placed by another, which sums the table of counts itself while that has at
 // most kSumWords words, since every workgroup reads it: 2^18 slots of 256
-// experts (64 KiB) 10.5 us against 12.1 with a launch that scans it between
-// the two, 2^20 slots of 128 experts (128 KiB) 13.7 against 14.4, but of 256
-// experts (256 KiB) 16.8 against 15.3.
+// experts (64 KiB) 9.6 us against 11.9 with a launch that scans it between the
+// two, 2^20 slots of 256 experts (256 KiB) 13.4 against 14.5, but of 320 experts
+// 15.9 against 14.9 and of 1024 experts 23.3 against 17.2.
 constexpr size_t kOneGroup = 8 * rs::kPlaceBlock;
 constexpr int kTileItems = 4;
 constexpr size_t kTile = size_t{kTileItems} * rs::kPlaceBlock;
-constexpr size_t kSumWords = 32768;
+constexpr size_t kSumWords = 65536;
 
 struct ExpertPlan {
     size_t chunk = 0;
