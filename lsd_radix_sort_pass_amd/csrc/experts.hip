@@ -32,7 +32,8 @@ constexpr size_t kMaxStride = size_t{1} << 40;
 bool good_rows(const void *p, size_t count, int width, size_t stride, size_t elem, bool output) {
     if (!good(p, count, elem)) return false;
     if (count <= 1) return true;
-    return stride <= kMaxStride && (!output || stride >= static_cast<size_t>(width));
+    if (stride > kMaxStride || (count - 1) > (size_t{1} << 62) / ((stride + 1) * elem)) return false;
+    return !output || stride >= static_cast<size_t>(width);
 }
 
 bool disjoint(const Span *spans, int outputs, int all) {

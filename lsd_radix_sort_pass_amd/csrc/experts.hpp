@@ -209,7 +209,7 @@ __device__ __forceinline__ float sigmoid(float l) {
     return (l >= 0.0f || l != l ? 1.0f : e) / (1.0f + e);
 }
 
-// exp(t) for t <= 0 that goes into a sum holding a 1: exp2 of t * log2(e) in
+// exp(t) for t <= 0 as a share of a sum that holds a 1: exp2 of t * log2(e) in
 // two parts, without the range steps of expf (a result below 2^-126 may be 0).
 __device__ __forceinline__ float exp_in_sum(float t) {
     constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596303e-8f, kLn2 = 0.693147182f;
@@ -327,7 +327,7 @@ __device__ __forceinline__ void place_by_counts(const T *row, int g, int k, int 
 template <class T, int G, int V, int W>
 __device__ __forceinline__ bool choose_by_counts(const float (&x)[V], const T *row, int g, int k, uint32_t *room,
                                                  float &value, uint32_t &index, bool &taken) {
-    constexpr int kWords = (V + 31) / 32;
+    static_assert(V <= 32);
     float most = x[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) most = __builtin_elementwise_maximum(most, x[v]);
@@ -336,23 +336,16 @@ __device__ __forceinline__ bool choose_by_counts(const float (&x)[V], const T *r
     constexpr float kInf = __builtin_inff(), kLowest = -3.402823466e38f;
     const float kth = -group_max<G>(above < k ? -most : -kInf);  // NaN with a NaN in the row
     const float least = kth == -kInf ? kLowest : kth;            // -inf is never chosen
-    uint32_t mask[kWords] = {};
-    int mine = 0;
+    uint32_t mask = 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) mask[v / 32] |= x[v] >= least ? 1u << (v % 32) : 0u;
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) mine += __popc(mask[i]);
+    for (int v = 0; v < V; ++v) mask |= x[v] >= least ? 1u << v : 0u;
+    const int mine = __popc(mask);
     const int upto = static_cast<int>(group_inclusive_sum<G>(static_cast<uint32_t>(mine)));
     constexpr int kRoom = G == 16 ? 2 * G : G;
     if (__ballot((kth != kth) | (upto > kRoom)) != 0) return false;
     int put = upto - mine;
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-        while (mask[i] != 0) {
-            const int v = __ffs(static_cast<int>(mask[i])) - 1 + 32 * i;
-            mask[i] &= mask[i] - 1;
-            room[put++] = static_cast<uint32_t>(held_index<G, V, W>(g, v));
-        }
+    for (; mask != 0; mask &= mask - 1) {
+        room[put++] = static_cast<uint32_t>(held_index<G, V, W>(g, __ffs(static_cast<int>(mask)) - 1));
     }
     const int total = static_cast<int>(group_max_u32<G>(static_cast<uint32_t>(upto)));
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -462,7 +455,7 @@ __global__ __launch_bounds__(kRouteBlock) void route_topk_backward_kernel(
         total = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            p[v] = p[v] == -__builtin_inff() ? 0.0f : expf(p[v] - top);
+            p[v] = p[v] == -__builtin_inff() ? 0.0f : exp_in_sum(p[v] - top);
             total += p[v];
         }
         total = group_sum<G>(total);

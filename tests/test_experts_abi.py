@@ -28,7 +28,8 @@ def test_route_checks(lib):
     for bad in (dict(dtype=3), dict(dtype=-1), dict(experts=0), dict(experts=1025, stride=1025), dict(k=0), dict(k=17),
                 dict(k=65, experts=128, stride=128), dict(gate=2), dict(gate=-1), dict(logits=None), dict(weights=None),
                 dict(chosen=None), dict(logits=A + 1), dict(weights=B + 2), dict(chosen=C + 2), dict(weights=A + 8),
-                dict(chosen=B), dict(tokens=2**31), dict(stride=2**41), dict(tokens=0, experts=0)):
+                dict(chosen=B), dict(tokens=2**31), dict(stride=2**41), dict(tokens=0, experts=0),
+                dict(tokens=2**29, k=1, stride=2**40)):        # no address range holds the rows
         assert call(**bad) == INVALID, bad
 
     def back(logits=A, dtype=BF16, tokens=T, experts=16, k=K, gate=1, chosen=B, g=C, grad=D, grad_stride=16):
