@@ -210,6 +210,15 @@ bool with_batch(int k, F &&f) {
     return f(std::integral_constant<int, 8>{});
 }
 
+// The one batch of a join with dots.
+template <class F>
+bool with_whole_batch(int k, F &&f) {
+    if (k <= rs::kMaxBatch) return with_batch(k, f);
+    if (k <= 10) return f(std::integral_constant<int, 10>{});
+    if (k <= 12) return f(std::integral_constant<int, 12>{});
+    return f(std::integral_constant<int, rs::kMaxJoinBatch>{});
+}
+
 // Calls f(IntC<U>) with the chunks that are in flight together in batches of B
 // slots: at most 8 accesses, evenly over the rounds, since a lane behind the
 // row's end still reads.  float32 rows of 4096, two slots: 65.1 us for 4093
@@ -248,8 +257,8 @@ bool launch_rows(rs::RowWork<T> w, hipStream_t stream) {
         };
         return w.dots ? narrow(std::true_type{}) : narrow(std::false_type{});
     }
-    if (w.dots != nullptr && (SPREAD || w.k <= rs::kMaxBatch)) {
-        return with_batch(w.k, [&](auto batch) {
+    if (w.dots != nullptr && (SPREAD || w.k <= rs::kMaxJoinBatch)) {
+        const auto whole = [&](auto batch) {
             constexpr int B = decltype(batch)::value;
             if (vecs <= 64) {
                 w.chunks = 1;
@@ -263,7 +272,8 @@ bool launch_rows(rs::RowWork<T> w, hipStream_t stream) {
                 return weighted ? go(rs::wide_rows_kernel<T, L, B, U, SPREAD, true, true>, w.tokens, 1)
                                 : go(rs::wide_rows_kernel<T, L, B, U, SPREAD, false, true>, w.tokens, 1);
             });
-        });
+        };
+        return SPREAD ? with_batch(w.k, whole) : with_whole_batch(w.k, whole);
     }
     w.chunks = (vecs + 63) / 64;
     const size_t units = w.tokens * static_cast<size_t>(w.chunks);

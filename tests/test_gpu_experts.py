@@ -277,7 +277,7 @@ def test_sort_experts_temp_and_outputs():
 # Rows
 # ---------------------------------------------------------------------------
 SHAPES = [(1, 1, 1), (1, 8, 7168), (5, 3, 7), (33, 2, 129), (64, 6, 2048), (7, 64, 33), (150, 4, 1537), (2, 5, 20001),
-          (301, 1, 8), (16, 7, 2880)]
+          (301, 1, 8), (16, 7, 2880), (9, 10, 513), (5, 12, 2051), (4, 16, 1100), (3, 17, 1030), (6, 9, 300)]
 
 
 def make_places(rng, T, k, dropped):
