@@ -42,7 +42,7 @@ MAX_CHOICES = 64        # RS_MAX_CHOICES
 _ROW_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}      # rs_dtype
 _GATES = {"softmax": 0, "sigmoid": 1}                                      # rs_gate
 _Tensor = torch.Tensor
-_I32, _F32, _U8 = (torch.int32,), (torch.float32,), (torch.uint8,)
+_I32, _F32 = torch.int32, torch.float32
 _SORT_FN = {torch.int32: "rs_sort_experts_i32", torch.int64: "rs_sort_experts_i64"}
 
 
@@ -80,29 +80,32 @@ def _refuse(t, name, dtypes, dim, device, shape, rows) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
+# The checks of the usual tensor in one expression; the rest is _refuse's.
 def _rows(t, name, device=None, dtypes=_ROW_DTYPES, shape=None) -> None:
     """Checks a 2-D float tensor with consecutive elements in a row, any row
     stride."""
-    if not (isinstance(t, _Tensor) and t.dtype in dtypes and t.dim() == 2 and t.is_contiguous()
-            and not t.requires_grad and (t.is_cuda if device is None else t.get_device() == device.index)
+    if not (type(t) is _Tensor and t.dtype in dtypes and t.dim() == 2 and t.is_contiguous() and not t.requires_grad
+            and (t.is_cuda if device is None else t.get_device() == device.index)
             and (shape is None or t.shape == shape)):
         _refuse(t, name, dtypes, 2, device, shape, True)
 
 
-def _flat(t, name, dtypes, device, shape=None, dim=None) -> None:
-    """Checks a contiguous tensor."""
-    if not (isinstance(t, _Tensor) and t.dtype in dtypes and t.is_contiguous() and not t.requires_grad
-            and (t.is_cuda if device is None else t.get_device() == device.index)
-            and (shape is None or t.shape == shape) and (dim is None or t.dim() == dim)):
-        _refuse(t, name, dtypes, dim, device, shape, False)
+def _flat(t, name, dtype, device, shape) -> None:
+    """Checks a contiguous tensor of a shape."""
+    if not (type(t) is _Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and not t.requires_grad and t.get_device() == device.index):
+        _refuse(t, name, (dtype,), None, device, shape, False)
 
 
-def _places(position, weights, device) -> Tuple[int, int]:
+def _places(position, weights, device, name="position") -> Tuple[int, int]:
     """(tokens, k) of a call's places, with its weights checked against them."""
-    _flat(position, "position", _I32, device, None, 2)
+    if not (type(position) is _Tensor and position.dtype is _I32 and position.dim() == 2 and position.is_contiguous()
+            and position.get_device() == device.index):
+        _refuse(position, name, (_I32,), 2, device, None, False)
+    shape = position.shape
     if weights is not None:
-        _flat(weights, "weights", _F32, device, position.shape)
-    return position.shape
+        _flat(weights, "weights", _F32, device, shape)
+    return shape
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -194,8 +197,7 @@ def route_topk_backward(logits: torch.Tensor, experts: torch.Tensor, grad_weight
     _rows(logits, "logits")
     tokens, count = logits.shape
     device = logits.device
-    _flat(experts, "experts", _I32, device, None, 2)
-    rows, k = experts.shape
+    rows, k = _places(experts, None, device, "experts")
     if not 1 <= k <= count or k > MAX_CHOICES:
         _refuse_k(k, count)
     if mode not in _GATES:
@@ -234,7 +236,8 @@ def sort_experts(experts: torch.Tensor, num_experts: int, first_expert: int = 0,
     of any other number are dropped: they sort last, and position holds ~place
     for them.  Returns ExpertOrder(order (n,), position (the shape of experts),
     offsets (num_experts + 1,)), all int32."""
-    _flat(experts, "experts", _SORT_FN, None)
+    if not (type(experts) is _Tensor and experts.dtype in _SORT_FN and experts.is_cuda and experts.is_contiguous()):
+        _refuse(experts, "experts", _SORT_FN, None, None, None, False)
     n, device, num = experts.numel(), experts.device, int(num_experts)
     if not 1 <= num <= MAX_EXPERTS:
         raise ValueError(f"num_experts must be between 1 and {MAX_EXPERTS} (got {num})")
@@ -248,7 +251,7 @@ def sort_experts(experts: torch.Tensor, num_experts: int, first_expert: int = 0,
     if offsets_out is not None:
         _flat(offsets_out, "offsets_out", _I32, device, (num + 1,))
     if temp is not None:
-        _flat(temp, "temp", _U8, device)
+        _flat(temp, "temp", torch.uint8, device, getattr(temp, "shape", None))
     if stream is not None or device.index != _current():
         with _on(device, stream, experts, order_out, position_out, offsets_out, temp):
             return sort_experts(experts, num, first_expert, order_out, position_out, offsets_out, temp)

@@ -642,6 +642,55 @@ def test_other_streams():
             assert torch.equal(a, b)
 
 
+def test_two_threads():
+    """Two host threads, a stream each, at once."""
+    note("two threads")
+    import threading
+    T, E, k, H = 1500, 40, 6, 300
+    inputs = [[torch.randn(T, c, device="cuda").bfloat16() for c in (E, H, H)] for _ in range(2)]
+    want = [layer_buffers(T, E, k, H) for _ in range(2)]
+    for p, b in zip(inputs, want):
+        run_layer(p[0], p[1], p[2], k, E, b)
+    torch.cuda.synchronize()
+    got = [[layer_buffers(T, E, k, H) for _ in range(5)] for _ in range(2)]
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for b in got[i]:
+                    run_layer(*inputs[i], k, E, b)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:      # reported below: a thread's own is only printed
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for i in range(2):
+        for b in got[i]:
+            for name in b:
+                if name != "temp":
+                    assert torch.equal(b[name], want[i][name]), name
+
+
+def test_parameters_under_no_grad():
+    """Parameters and tensors that want a gradient, where none is recorded."""
+    note("parameters")
+    x = torch.nn.Parameter(torch.randn(6, 32, device="cuda"))
+    pos = torch.randperm(12, device="cuda").to(torch.int32).reshape(6, 2)
+    w = torch.rand(6, 2, device="cuda", requires_grad=True)
+    with pytest.raises(ValueError, match="gradient"):
+        rs.dispatch_rows(x, pos, w)
+    with torch.no_grad():
+        rows = rs.dispatch_rows(x, pos, w)
+        assert torch.equal(rows, rs.dispatch_rows(x.detach(), pos, w.detach()))
+        assert not rows.requires_grad
+
+
 def test_results_repeat():
     note("results repeat")
     T, E, k, H = 3000, 128, 8, 1000
