@@ -237,6 +237,8 @@ bool with_at_once(int chunks, F &&f) {
     return f(IntC<1>{});
 }
 
+constexpr size_t kLastLevelBytes = size_t{1} << 28;  // the memory-side cache of an MI355X
+
 // Enqueues the spread or the join of w, with its dots if w.dots is set.
 template <bool SPREAD, class T>
 bool launch_rows(rs::RowWork<T> w, hipStream_t stream) {
@@ -257,6 +259,8 @@ bool launch_rows(rs::RowWork<T> w, hipStream_t stream) {
         };
         return w.dots ? narrow(std::true_type{}) : narrow(std::false_type{});
     }
+    const size_t arrays = w.tokens + w.num_rows * (SPREAD && w.dots != nullptr ? 2 : 1);  // rows in all
+    w.once = arrays * static_cast<size_t>(w.width) >= kLastLevelBytes / sizeof(T);
     if (w.dots != nullptr && (SPREAD || w.k <= rs::kMaxJoinBatch)) {
         const auto whole = [&](auto batch) {
             constexpr int B = decltype(batch)::value;

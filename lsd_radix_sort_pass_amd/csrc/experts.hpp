@@ -859,6 +859,7 @@ struct RowWork {
     int k;
     int lanes;   // narrow rows: threads of a row
     int chunks;  // wide rows: rounds of the lanes that cover a row
+    bool once;   // wide rows: rows_in is read past the caches' keeping
 };
 
 constexpr int kMaxBatch = 8;       // slots of a token whose rows are in flight together
@@ -878,9 +879,15 @@ constexpr int kMaxJoinBatch = 16;  // in a join with dots, which holds all of th
 // multiple of the access: its first elements are computed twice, to the same
 // result, and counted once in the products.
 // Bound by memory, which a plain copy moves at 4.9 - 5.4 TB/s: bfloat16 spread
-// 16384 x 8 x 4096 217 us (5.6 TB/s), join 236 us (5.1), spread with dots
-// 8192 x 8 x 2048 117 us (4.9), join with dots 67 us (5.0).  Row by row instead of
+// 16384 x 8 x 4096 217 us (5.6 TB/s), join 206 us (5.9), spread with dots
+// 8192 x 8 x 2048 117 us (4.9), join with dots 60 us (5.6).  Row by row instead of
 // in batches the join took 262 us, dots in a pass of their own 144 in all.
+// a.once reads rows_in with non-temporal loads, where the rows do not fit the
+// last-level cache anyway: what the writes before and after leave there lasts
+// longer.  Joins gain 12% so (234 -> 206 us), and a spread with dots gains it in
+// the kernel that reads its result next (110 -> 98 us for both, 4093 x 2 x 4099
+// float32); rows that fit are better kept (45 -> 47 us for 2048 x 8 x 2048).
+// Non-temporal stores help the call alone and cost the next one as much.
 constexpr int kNarrow = 32;
 
 template <class T, int LANES, int BATCH, int AT_ONCE, bool SPREAD, bool WEIGHTED, bool DOTS>
@@ -930,16 +937,18 @@ __global__ __launch_bounds__(kRowBlock) void wide_rows_kernel(const RowWork<T> a
                     if constexpr (SPREAD || DOTS) load_vec<T, W>(a.x + t * a.x_stride + col[u], x[u]);
                 }
                 if constexpr (!SPREAD || DOTS) {
-                    if (some >= 0) {
+                    const auto load_rows = [&](auto load) {
 #pragma unroll
                         for (int u = 0; u < AT_ONCE; ++u) {
 #pragma unroll
                             for (int i = 0; i < BATCH; ++i) {
                                 const auto row = static_cast<size_t>(slot[i].used ? slot[i].row : some);
-                                raw[u][i] = *reinterpret_cast<const Vec *>(a.rows_in + row * a.rows_in_stride + col[u]);
+                                raw[u][i] = load(reinterpret_cast<const Vec *>(a.rows_in + row * a.rows_in_stride + col[u]));
                             }
                         }
-                    }
+                    };
+                    if (some >= 0 && a.once) load_rows([](const Vec *p) { return __builtin_nontemporal_load(p); });
+                    if (some >= 0 && !a.once) load_rows([](const Vec *p) { return *p; });
                 }
 #pragma unroll
                 for (int u = 0; u < AT_ONCE; ++u) {
