@@ -266,25 +266,40 @@ bool launch_rows(rs::RowWork<T> w, hipStream_t stream) {
             constexpr int B = decltype(batch)::value;
             if (vecs <= 64) {
                 w.chunks = 1;
-                return weighted ? go(rs::wide_rows_kernel<T, 64, B, 1, SPREAD, true, true>, w.tokens, rs::kRowBlock / 64)
-                                : go(rs::wide_rows_kernel<T, 64, B, 1, SPREAD, false, true>, w.tokens, rs::kRowBlock / 64);
+                return weighted ? go(rs::wide_rows_kernel<T, 64, B, 1, SPREAD, true, true, false>, w.tokens, rs::kRowBlock / 64)
+                                : go(rs::wide_rows_kernel<T, 64, B, 1, SPREAD, false, true, false>, w.tokens, rs::kRowBlock / 64);
             }
             constexpr int L = rs::kRowBlock;
             w.chunks = (vecs + L - 1) / L;
             return with_at_once<B>(w.chunks, [&](auto at_once) {
                 constexpr int U = decltype(at_once)::value;
-                return weighted ? go(rs::wide_rows_kernel<T, L, B, U, SPREAD, true, true>, w.tokens, 1)
-                                : go(rs::wide_rows_kernel<T, L, B, U, SPREAD, false, true>, w.tokens, 1);
+                return weighted ? go(rs::wide_rows_kernel<T, L, B, U, SPREAD, true, true, false>, w.tokens, 1)
+                                : go(rs::wide_rows_kernel<T, L, B, U, SPREAD, false, true, false>, w.tokens, 1);
             });
         };
         return SPREAD ? with_batch(w.k, whole) : with_whole_batch(w.k, whole);
     }
+    constexpr int kWaves = rs::kRowBlock / 64;
+    constexpr size_t kMaxGridY = 65535;
     w.chunks = (vecs + 63) / 64;
-    const size_t units = w.tokens * static_cast<size_t>(w.chunks);
+    w.side = w.chunks >= 3 ? 2 : w.chunks - 1;
+    static_assert(kWaves == 4);
+    const size_t per_block = kWaves >> w.side, blocks = (w.tokens + per_block - 1) / per_block;
+    const dim3 grid(static_cast<unsigned>((w.chunks + (1 << w.side) - 1) >> w.side),
+                    static_cast<unsigned>(blocks < kMaxGridY ? blocks : kMaxGridY));
     const auto plain = [&](auto batch) {
         constexpr int B = decltype(batch)::value;
-        return weighted ? go(rs::wide_rows_kernel<T, 64, B, 1, SPREAD, true, false>, units, rs::kRowBlock / 64)
-                        : go(rs::wide_rows_kernel<T, 64, B, 1, SPREAD, false, false>, units, rs::kRowBlock / 64);
+        const auto run = [&](auto kernel) {
+            return launch_kernel(RS_KERNEL_ROWS, stream, [&] { run_kernel(kernel, grid, rs::kRowBlock, stream, w); });
+        };
+        if constexpr (!SPREAD) {
+            if (w.once) {
+                return weighted ? run(rs::wide_rows_kernel<T, 64, B, 1, false, true, false, true>)
+                                : run(rs::wide_rows_kernel<T, 64, B, 1, false, false, false, true>);
+            }
+        }
+        return weighted ? run(rs::wide_rows_kernel<T, 64, B, 1, SPREAD, true, false, false>)
+                        : run(rs::wide_rows_kernel<T, 64, B, 1, SPREAD, false, false, false>);
     };
     // A spread without dots loads no rows: its batch only unrolls the stores.
     const bool ok = SPREAD ? plain(std::integral_constant<int, rs::kMaxBatch>{}) : with_batch(w.k, plain);

@@ -859,6 +859,7 @@ struct RowWork {
     int k;
     int lanes;   // narrow rows: threads of a row
     int chunks;  // wide rows: rounds of the lanes that cover a row
+    int side;    // wide rows without dots: log2 of the waves side by side
     bool once;   // wide rows: rows_in is read past the caches' keeping
 };
 
@@ -882,7 +883,8 @@ constexpr int kMaxJoinBatch = 16;  // in a join with dots, which holds all of th
 // 16384 x 8 x 4096 217 us (5.6 TB/s), join 206 us (5.9), spread with dots
 // 8192 x 8 x 2048 117 us (4.9), join with dots 60 us (5.6).  Row by row instead of
 // in batches the join took 262 us, dots in a pass of their own 144 in all.
-// a.once reads rows_in with non-temporal loads, where the rows do not fit the
+// a.once (ONCE without dots, where the branch would cost a small join 0.3 us of
+// 3.5) reads rows_in with non-temporal loads, where the rows do not fit the
 // last-level cache anyway: what the writes before and after leave there lasts
 // longer.  Joins gain 12% so (234 -> 206 us), and a spread with dots gains it in
 // the kernel that reads its result next (110 -> 98 us for both, 4093 x 2 x 4099
@@ -890,7 +892,7 @@ constexpr int kMaxJoinBatch = 16;  // in a join with dots, which holds all of th
 // Non-temporal stores help the call alone and cost the next one as much.
 constexpr int kNarrow = 32;
 
-template <class T, int LANES, int BATCH, int AT_ONCE, bool SPREAD, bool WEIGHTED, bool DOTS>
+template <class T, int LANES, int BATCH, int AT_ONCE, bool SPREAD, bool WEIGHTED, bool DOTS, bool ONCE>
 __global__ __launch_bounds__(kRowBlock) void wide_rows_kernel(const RowWork<T> a) {
     constexpr int W = kVec<T>;
     using Vec = typename VecOf<T, W>::type;
@@ -900,11 +902,13 @@ __global__ __launch_bounds__(kRowBlock) void wide_rows_kernel(const RowWork<T> a
     __shared__ float partial[kWaves > 1 ? BATCH : 1][kWaves > 1 ? kWaves : 1];
     const int lane = threadIdx.x % LANES;
     const int group = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / LANES);
-    const size_t units = DOTS ? a.tokens : a.tokens * static_cast<size_t>(a.chunks);
-    for (size_t unit = static_cast<size_t>(blockIdx.x) * kPer + group; unit < units;
-         unit += static_cast<size_t>(gridDim.x) * kPer) {
-        const size_t t = DOTS ? unit : unit / static_cast<unsigned>(a.chunks);
-        const int first = DOTS ? 0 : static_cast<int>(unit % static_cast<unsigned>(a.chunks));
+    // Workgroup (x, y): without dots chunks x * 2^side ... and tokens y * (kPer /
+    // 2^side) ..., 2^side waves side by side in a row; with dots tokens alone.
+    const int side = DOTS ? 0 : a.side;
+    const int first = DOTS ? 0 : static_cast<int>(blockIdx.x << side) + (group & ((1 << side) - 1));
+    if (first >= a.chunks) return;
+    const size_t block = DOTS ? blockIdx.x : blockIdx.y, blocks = DOTS ? gridDim.x : gridDim.y;
+    for (size_t t = block * (kPer >> side) + (group >> side); t < a.tokens; t += blocks * (kPer >> side)) {
         float acc[W] = {};
         for (int j0 = 0; j0 < a.k; j0 += BATCH) {
             // Lane i of each wave loads slot j0 + i; the wave reads them as scalars.
@@ -947,8 +951,15 @@ __global__ __launch_bounds__(kRowBlock) void wide_rows_kernel(const RowWork<T> a
                             }
                         }
                     };
-                    if (some >= 0 && a.once) load_rows([](const Vec *p) { return __builtin_nontemporal_load(p); });
-                    if (some >= 0 && !a.once) load_rows([](const Vec *p) { return *p; });
+                    const auto past = [](const Vec *p) { return __builtin_nontemporal_load(p); };
+                    const auto kept = [](const Vec *p) { return *p; };
+                    if constexpr (DOTS) {
+                        if (some >= 0 && a.once) load_rows(past);
+                        if (some >= 0 && !a.once) load_rows(kept);
+                    } else if (some >= 0) {
+                        if constexpr (ONCE) load_rows(past);
+                        if constexpr (!ONCE) load_rows(kept);
+                    }
                 }
 #pragma unroll
                 for (int u = 0; u < AT_ONCE; ++u) {
