@@ -631,9 +631,9 @@ __global__ __launch_bounds__(kPlaceBlock) void expert_scan_kernel(uint32_t *__re
 // in lane order, which the lane order test pins.  Dropped slots, often a long
 // run of padding, are ranked by a ballot instead of 64 adds to one address.
 // A tile's slots are put in key order in LDS, so that order is written in
-// runs (without, 2^20 slots of 256 experts took 14.8 us, 7.4 with).  KEYS >=
-// experts sizes the LDS.  Bound by the chain of round trips: ids and table, LDS
-// counts, scans, writes: 9.0 us for 2^20 slots of 128 experts (12 MiB).
+// runs (the sort of 2^20 slots of 256 experts takes 13.4 us so, 16.1 without).
+// KEYS >= experts sizes the LDS.  Bound by the chain of round trips: ids and
+// table, LDS counts, scans, writes: 8.9 us for 2^20 slots of 128 experts (12 MiB).
 enum : int {
     kNoTable = 0,  // one workgroup that holds every slot in one tile
     kCounts = 1,   // every chunk's counts are in the table: each workgroup sums them
@@ -1085,7 +1085,7 @@ __global__ __launch_bounds__(kRowBlock) void narrow_rows_kernel(const RowWork<T>
 
 // Dots alone, for wide joins of more than kMaxJoinBatch slots, whose kernel does
 // not take them along (10 slots would take 157 us so for 8192 x 2048 bfloat16,
-// 79 in one pass).  A wave takes a slot.
+// 72 in one pass).  A wave takes a slot.
 template <class T>
 __global__ __launch_bounds__(kRowBlock) void dot_rows_kernel(const RowWork<T> a) {
     constexpr int W = kVec<T>;
