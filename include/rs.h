@@ -377,11 +377,19 @@ rs_status rs_combine_rows(const void *rows, int dtype, size_t num_rows, size_t r
 /* Its gradients: grad_rows[place of (t, j)] = w[t][j] * grad_out[t], zeros for
  * a dropped slot (every row of rs_sort_experts's places is written), and, if
  * grad_weights is given, grad_weights[t][j] = <grad_out[t], rows[place]>, 0 for
- * a dropped slot (rows may be NULL otherwise). */
+ * a dropped slot (rows may be NULL otherwise).  As in rs_dispatch_rows a row
+ * that no slot names is left as it was. */
 rs_status rs_combine_rows_backward(const void *grad_out, int dtype, size_t tokens, int width, size_t grad_out_stride,
                                    const int32_t *position, const float *weights, int k, const void *rows,
                                    size_t rows_stride, void *grad_rows, size_t grad_rows_stride, size_t num_rows,
                                    float *grad_weights, hipStream_t stream);
+
+/* The same, with zeros in the rows that no slot names, whose gradient that is:
+ * every row is written. */
+rs_status rs_combine_rows_backward_all(const void *grad_out, int dtype, size_t tokens, int width,
+                                       size_t grad_out_stride, const int32_t *position, const float *weights, int k,
+                                       const void *rows, size_t rows_stride, void *grad_rows, size_t grad_rows_stride,
+                                       size_t num_rows, float *grad_weights, hipStream_t stream);
 
 /* Static, NUL-terminated description of a status code. */
 const char *rs_status_string(rs_status status);

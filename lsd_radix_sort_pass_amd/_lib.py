@@ -74,6 +74,7 @@ SIGNATURES = {
     "rs_dispatch_rows_backward": (_I, [_VP, _I, _SZ, _SZ, _VP, _VP, _I, _VP, _SZ, _VP, _SZ, _VP, _SZ, _I, _VP]),
     "rs_combine_rows": (_I, [_VP, _I, _SZ, _SZ, _VP, _VP, _I, _VP, _SZ, _I, _SZ, _VP]),
     "rs_combine_rows_backward": (_I, [_VP, _I, _SZ, _I, _SZ, _VP, _VP, _I, _VP, _SZ, _VP, _SZ, _SZ, _VP, _VP]),
+    "rs_combine_rows_backward_all": (_I, [_VP, _I, _SZ, _I, _SZ, _VP, _VP, _I, _VP, _SZ, _VP, _SZ, _SZ, _VP, _VP]),
     "rs_status_string": (ctypes.c_char_p, [_I]),
     "rs_prof_enable": (_I, [_I]),
     "rs_prof_reset": (None, []),

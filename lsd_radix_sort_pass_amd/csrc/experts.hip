@@ -1,6 +1,8 @@
 // experts.hip -- C ABI of the mixture-of-experts calls (routing, slots sorted
 // by expert, rows dispatched and combined): argument checks and launches.
 // Compiled behind rs.hip (librs.hip), whose helpers it uses.
+#include <algorithm>
+
 #include "experts.hpp"
 
 namespace {
@@ -243,8 +245,10 @@ constexpr size_t kLastLevelBytes = size_t{1} << 28;  // the memory-side cache of
 template <bool SPREAD, class T>
 bool launch_rows(rs::RowWork<T> w, hipStream_t stream) {
     const int vecs = (w.width + rs::kVec<T> - 1) / rs::kVec<T>;
+    const size_t clearing = w.clear_rows ? (w.num_rows + w.clear_rows - 1) / w.clear_rows : 0;  // workgroups
     const auto go = [&](auto kernel, size_t units, int per_block) {
-        const unsigned grid = grid_for(units, static_cast<unsigned>(per_block), kMaxGrid);
+        w.clearing = static_cast<unsigned>(clearing);
+        const unsigned grid = w.clearing + grid_for(units, static_cast<unsigned>(per_block), kMaxGrid);
         return launch_kernel(RS_KERNEL_ROWS, stream, [&] { run_kernel(kernel, grid, rs::kRowBlock, stream, w); });
     };
     const bool weighted = w.weights != nullptr;
@@ -285,8 +289,10 @@ bool launch_rows(rs::RowWork<T> w, hipStream_t stream) {
     w.side = w.chunks >= 3 ? 2 : w.chunks - 1;
     static_assert(kWaves == 4);
     const size_t per_block = kWaves >> w.side, blocks = (w.tokens + per_block - 1) / per_block;
-    const dim3 grid(static_cast<unsigned>((w.chunks + (1 << w.side) - 1) >> w.side),
-                    static_cast<unsigned>(blocks < kMaxGridY ? blocks : kMaxGridY));
+    const auto across = static_cast<unsigned>((w.chunks + (1 << w.side) - 1) >> w.side);
+    w.clearing = static_cast<unsigned>((clearing + across - 1) / across);
+    const size_t most = kMaxGridY - w.clearing;
+    const dim3 grid(across, w.clearing + static_cast<unsigned>(blocks < most ? blocks : most));
     const auto plain = [&](auto batch) {
         constexpr int B = decltype(batch)::value;
         const auto run = [&](auto kernel) {
@@ -307,9 +313,43 @@ bool launch_rows(rs::RowWork<T> w, hipStream_t stream) {
     return ok && (w.dots == nullptr || go(rs::dot_rows_kernel<T>, slots, rs::kRowBlock / 64));
 }
 
+// Whether the rows that no slot names are cleared by kClearGroups groups of the
+// spread's own launch, which read all places each while the spread takes its
+// time, or all rows are by a launch before.  Not at all / beside / before, in us,
+// bfloat16, k = 8, with dots: 2048 x 128 9.1 / 9.1 / 11.3, 8192 x 128 12.7 / 14.0 /
+// 17.6, 32768 x 128 32 / 51 / 44, 32768 x 256 59 / 65 / 78, 8192 x 2048 91 / 91 / 126;
+// without: 3000 x 128 6.5 / 6.5 / 8.8, 8192 x 128 7 / 13 / 11, 32768 x 256 25 / 49 /
+// 44, 32768 x 512 51 / 69 / 87, 32768 x 1024 106 / 108 / 181.  More slots than 2^22
+// would not fit the groups' bits.
+constexpr size_t kClearGroups = 64;
+bool clear_beside(size_t slots, size_t num_rows, size_t row_bytes, bool dots) {
+    if (num_rows > slots || slots > kClearGroups * rs::kClearRows) return false;
+    return slots <= (size_t{1} << 16) || row_bytes >= (dots ? 512 : 1024);
+}
+
+// Enqueues zeros in whole rows.
+bool launch_clear(int dtype, void *rows, size_t num_rows, int width, size_t stride, hipStream_t stream) {
+    return with_dtype(dtype, [&](auto zero) {
+        using T = decltype(zero);
+        const int vecs = (width + rs::kVec<T> - 1) / rs::kVec<T>;
+        int lanes = 1;
+        while (lanes < vecs && lanes < rs::kRowBlock) lanes *= 2;
+        const unsigned grid = grid_for(num_rows, static_cast<unsigned>(rs::kRowBlock / lanes), kMaxGrid);
+        return launch_kernel(RS_KERNEL_ROWS, stream, [&] {
+            run_kernel(rs::clear_rows_kernel<T>, grid, rs::kRowBlock, stream, static_cast<T *>(rows), num_rows, width,
+                       stride, lanes);
+        });
+    });
+}
+
+// all: rows that no slot names are cleared.
 bool launch_spread(int dtype, const void *x, size_t tokens, int width, size_t x_stride, const int32_t *position,
                    const float *weights, int k, void *rows, size_t num_rows, size_t rows_stride, const void *rows_in,
-                   size_t rows_in_stride, float *dots, hipStream_t stream) {
+                   size_t rows_in_stride, float *dots, bool all, hipStream_t stream) {
+    const size_t row_bytes = static_cast<size_t>(width) * static_cast<size_t>(dtype_bytes(dtype));
+    const bool clear = all && num_rows != 0;
+    const bool beside = clear && clear_beside(tokens * static_cast<size_t>(k), num_rows, row_bytes, dots != nullptr);
+    if (clear && !beside && !launch_clear(dtype, rows, num_rows, width, rows_stride, stream)) return false;
     if (tokens == 0 || (num_rows == 0 && dots == nullptr)) return true;
     return with_dtype(dtype, [&](auto zero) {
         using T = decltype(zero);
@@ -319,6 +359,10 @@ bool launch_spread(int dtype, const void *x, size_t tokens, int width, size_t x_
         w.rows_out = static_cast<T *>(rows), w.rows_out_stride = rows_stride;
         w.dots = dots, w.position = position, w.weights = weights;
         w.tokens = tokens, w.num_rows = num_rows, w.width = width, w.k = k;
+        if (beside) {
+            const size_t groups = std::min(kClearGroups, (num_rows + 255) / 256);
+            w.clear_rows = static_cast<uint32_t>((num_rows + 32 * groups - 1) / (32 * groups) * 32);
+        }
         return launch_rows<true>(w, stream);
     });
 }
@@ -337,6 +381,32 @@ bool launch_join(int dtype, const void *rows, size_t num_rows, size_t rows_strid
         w.tokens = tokens, w.num_rows = num_rows, w.width = width, w.k = k;
         return launch_rows<false>(w, stream);
     });
+}
+
+rs_status combine_backward(const void *grad_out, int dtype, size_t tokens, int width, size_t grad_out_stride,
+                           const int32_t *position, const float *weights, int k, const void *rows, size_t rows_stride,
+                           void *grad_rows, size_t grad_rows_stride, size_t num_rows, float *grad_weights, bool all,
+                           hipStream_t stream) {
+    if (!good_shape(dtype, tokens, width, k, num_rows)) return RS_ERROR_INVALID_VALUE;
+    const size_t elem = static_cast<size_t>(dtype_bytes(dtype)), slots = tokens * static_cast<size_t>(k);
+    if (!good_rows(grad_out, tokens, width, grad_out_stride, elem, false) || !good(position, slots, 4) ||
+        !good_rows(grad_rows, num_rows, width, grad_rows_stride, elem, true) || (weights && !aligned(weights, 4))) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    const bool dots = grad_weights != nullptr;
+    if (dots && (!aligned(grad_weights, 4) || !good_rows(rows, num_rows, width, rows_stride, elem, false))) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    const auto w = static_cast<size_t>(width);
+    const Span spans[] = {span_of(grad_rows, span_bytes(num_rows, w, grad_rows_stride, elem)),
+                          span_of(grad_weights, dots ? slots * 4 : 0),
+                          span_of(grad_out, span_bytes(tokens, w, grad_out_stride, elem)),
+                          span_of(position, slots * 4), span_of(weights, weights ? slots * 4 : 0),
+                          span_of(rows, dots ? span_bytes(num_rows, w, rows_stride, elem) : 0)};
+    if (!disjoint(spans, 2, 6)) return RS_ERROR_INVALID_VALUE;
+    const bool ok = launch_spread(dtype, grad_out, tokens, width, grad_out_stride, position, weights, k, grad_rows,
+                                  num_rows, grad_rows_stride, rows, rows_stride, grad_weights, all, stream);
+    return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
 }
 
 }  // namespace
@@ -448,7 +518,7 @@ rs_status rs_dispatch_rows(const void *x, int dtype, size_t tokens, int width, s
                           span_of(weights, weights ? slots * 4 : 0)};
     if (!disjoint(spans, 1, 4)) return RS_ERROR_INVALID_VALUE;
     const bool ok = launch_spread(dtype, x, tokens, width, x_stride, position, weights, k, rows, num_rows, rows_stride,
-                                  nullptr, 0, nullptr, stream);
+                                  nullptr, 0, nullptr, false, stream);
     return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
 }
 
@@ -489,26 +559,16 @@ rs_status rs_combine_rows_backward(const void *grad_out, int dtype, size_t token
                                    const int32_t *position, const float *weights, int k, const void *rows,
                                    size_t rows_stride, void *grad_rows, size_t grad_rows_stride, size_t num_rows,
                                    float *grad_weights, hipStream_t stream) {
-    if (!good_shape(dtype, tokens, width, k, num_rows)) return RS_ERROR_INVALID_VALUE;
-    const size_t elem = static_cast<size_t>(dtype_bytes(dtype)), slots = tokens * static_cast<size_t>(k);
-    if (!good_rows(grad_out, tokens, width, grad_out_stride, elem, false) || !good(position, slots, 4) ||
-        !good_rows(grad_rows, num_rows, width, grad_rows_stride, elem, true) || (weights && !aligned(weights, 4))) {
-        return RS_ERROR_INVALID_VALUE;
-    }
-    const bool dots = grad_weights != nullptr;
-    if (dots && (!aligned(grad_weights, 4) || !good_rows(rows, num_rows, width, rows_stride, elem, false))) {
-        return RS_ERROR_INVALID_VALUE;
-    }
-    const auto w = static_cast<size_t>(width);
-    const Span spans[] = {span_of(grad_rows, span_bytes(num_rows, w, grad_rows_stride, elem)),
-                          span_of(grad_weights, dots ? slots * 4 : 0),
-                          span_of(grad_out, span_bytes(tokens, w, grad_out_stride, elem)),
-                          span_of(position, slots * 4), span_of(weights, weights ? slots * 4 : 0),
-                          span_of(rows, dots ? span_bytes(num_rows, w, rows_stride, elem) : 0)};
-    if (!disjoint(spans, 2, 6)) return RS_ERROR_INVALID_VALUE;
-    const bool ok = launch_spread(dtype, grad_out, tokens, width, grad_out_stride, position, weights, k, grad_rows,
-                                  num_rows, grad_rows_stride, rows, rows_stride, grad_weights, stream);
-    return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
+    return combine_backward(grad_out, dtype, tokens, width, grad_out_stride, position, weights, k, rows, rows_stride,
+                            grad_rows, grad_rows_stride, num_rows, grad_weights, false, stream);
+}
+
+rs_status rs_combine_rows_backward_all(const void *grad_out, int dtype, size_t tokens, int width, size_t grad_out_stride,
+                                       const int32_t *position, const float *weights, int k, const void *rows,
+                                       size_t rows_stride, void *grad_rows, size_t grad_rows_stride, size_t num_rows,
+                                       float *grad_weights, hipStream_t stream) {
+    return combine_backward(grad_out, dtype, tokens, width, grad_out_stride, position, weights, k, rows, rows_stride,
+                            grad_rows, grad_rows_stride, num_rows, grad_weights, true, stream);
 }
 
 }  // extern "C"

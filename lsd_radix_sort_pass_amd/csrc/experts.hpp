@@ -861,10 +861,85 @@ struct RowWork {
     int chunks;  // wide rows: rounds of the lanes that cover a row
     int side;    // wide rows without dots: log2 of the waves side by side
     bool once;   // wide rows: rows_in is read past the caches' keeping
+    unsigned clearing;    // spread: leading workgroups (lines of them in a grid of two dimensions) that only
+                          // clear the rows that no slot names
+    uint32_t clear_rows;  // rows that each of them takes at a time, at most kClearRows
 };
+
+// Zeros in the rows_out that no slot names, used or dropped, by workgroup
+// `group` of `groups`: it marks the named ones of clear_rows rows in LDS, from
+// all places, and clears the others.  The rest of the launch writes named rows
+// only, so neither has to wait for the other.  Bound by the vector work on each
+// place, some 90 cycles for 64 of them: 11 us for 65536 slots, while the rows take
+// the memory's time (8192 x 8 x 2048 bfloat16 with dots: 91 us with and without).
+constexpr uint32_t kClearRows = 65536;
+
+template <class T>
+__device__ __forceinline__ void clear_unnamed_rows(const RowWork<T> &a, size_t group, size_t groups) {
+    constexpr int W = kVec<T>;
+    constexpr int kDeep = 8;  // accesses of a thread in flight
+    typedef int32_t Quad __attribute__((ext_vector_type(4), aligned(4)));
+    __shared__ uint32_t named[kClearRows / 32];
+    const uint32_t tid = threadIdx.x, lane = tid % 64;
+    const size_t slots = a.tokens * static_cast<size_t>(a.k), quads = slots / 4;
+    for (size_t lo = group * a.clear_rows; lo < a.num_rows; lo += groups * a.clear_rows) {
+        const uint32_t rows = a.num_rows - lo < a.clear_rows ? static_cast<uint32_t>(a.num_rows - lo) : a.clear_rows;
+        const uint32_t words = (rows + 31) / 32;
+        for (uint32_t i = tid; i < words; i += kRowBlock) named[i] = 0;
+        __syncthreads();
+        const auto mark = [&](int32_t position) {
+            const uint32_t r = static_cast<uint32_t>(position >= 0 ? position : ~position) - static_cast<uint32_t>(lo);
+            if (r < rows) atomicOr(&named[r / 32], 1u << r % 32);
+        };
+        for (size_t q0 = tid; q0 < quads; q0 += kRowBlock * kDeep) {
+            Quad v[kDeep];  // behind the end the last one again: a mark twice is a mark
+#pragma unroll
+            for (int i = 0; i < kDeep; ++i) {
+                const size_t q = q0 + static_cast<size_t>(i) * kRowBlock;
+                v[i] = reinterpret_cast<const Quad *>(a.position)[q < quads ? q : quads - 1];
+            }
+#pragma unroll
+            for (int i = 0; i < kDeep; ++i) mark(v[i].x), mark(v[i].y), mark(v[i].z), mark(v[i].w);
+        }
+        if (tid < slots % 4) mark(a.position[quads * 4 + tid]);
+        __syncthreads();
+        for (uint32_t w0 = tid - lane; w0 < words; w0 += kRowBlock) {
+            const uint32_t w = w0 + lane, have = rows - w * 32;  // rows of the lane's word, if it has any
+            uint32_t left = 0;
+            if (w < words) left = ~named[w] & (have < 32 ? (1u << have) - 1 : 0xFFFFFFFFu);
+            for (uint64_t some = __ballot(left != 0); some != 0; some &= some - 1) {
+                const int of = __builtin_ctzll(some);
+                for (uint32_t m = lane_value(left, of); m != 0; m &= m - 1) {
+                    const size_t row = lo + (w0 + static_cast<uint32_t>(of)) * 32 + static_cast<uint32_t>(__builtin_ctz(m));
+                    const float zeros[W] = {};
+                    for (int col = static_cast<int>(lane) * W; col < a.width; col += 64 * W) {
+                        store_some<T, W>(a.rows_out + row * a.rows_out_stride + col, a.width - col, zeros);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
 
 constexpr int kMaxBatch = 8;       // slots of a token whose rows are in flight together
 constexpr int kMaxJoinBatch = 16;  // in a join with dots, which holds all of them
+
+// Zeros in whole rows, `lanes` threads (a power of two) to a row: for the
+// spreads whose time would not hide the search above.
+template <class T>
+__global__ __launch_bounds__(kRowBlock) void clear_rows_kernel(T *rows, size_t num_rows, int width, size_t stride,
+                                                               int lanes) {
+    constexpr int W = kVec<T>;
+    const int per_block = kRowBlock / lanes;
+    const float zeros[W] = {};
+    for (size_t r = static_cast<size_t>(blockIdx.x) * per_block + threadIdx.x / lanes; r < num_rows;
+         r += static_cast<size_t>(gridDim.x) * per_block) {
+        for (int col = static_cast<int>(threadIdx.x) % lanes * W; col < width; col += lanes * W) {
+            store_some<T, W>(rows + r * stride + col, width - col, zeros);
+        }
+    }
+}
 
 // Rows of more than kNarrow 16-byte accesses.  LANES threads hold 16-byte
 // columns of a token's row: they read x once and write it k times, or read k
@@ -904,10 +979,18 @@ __global__ __launch_bounds__(kRowBlock) void wide_rows_kernel(const RowWork<T> a
     const int group = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / LANES);
     // Workgroup (x, y): without dots chunks x * 2^side ... and tokens y * (kPer /
     // 2^side) ..., 2^side waves side by side in a row; with dots tokens alone.
+    if constexpr (SPREAD) {
+        if ((DOTS ? blockIdx.x : blockIdx.y) < a.clearing) {
+            const size_t across = DOTS ? 1 : gridDim.x;
+            clear_unnamed_rows<T>(a, DOTS ? blockIdx.x : blockIdx.y * across + blockIdx.x, a.clearing * across);
+            return;
+        }
+    }
+    const unsigned ahead = SPREAD ? a.clearing : 0;
     const int side = DOTS ? 0 : a.side;
     const int first = DOTS ? 0 : static_cast<int>(blockIdx.x << side) + (group & ((1 << side) - 1));
     if (first >= a.chunks) return;
-    const size_t block = DOTS ? blockIdx.x : blockIdx.y, blocks = DOTS ? gridDim.x : gridDim.y;
+    const size_t block = (DOTS ? blockIdx.x : blockIdx.y) - ahead, blocks = (DOTS ? gridDim.x : gridDim.y) - ahead;
     for (size_t t = block * (kPer >> side) + (group >> side); t < a.tokens; t += blocks * (kPer >> side)) {
         float acc[W] = {};
         for (int j0 = 0; j0 < a.k; j0 += BATCH) {
@@ -1042,11 +1125,18 @@ __global__ __launch_bounds__(kRowBlock) void wide_rows_kernel(const RowWork<T> a
 template <class T, bool SPREAD, bool WEIGHTED, bool DOTS>
 __global__ __launch_bounds__(kRowBlock) void narrow_rows_kernel(const RowWork<T> a) {
     constexpr int W = kVec<T>;
+    if constexpr (SPREAD) {
+        if (blockIdx.x < a.clearing) {
+            clear_unnamed_rows<T>(a, blockIdx.x, a.clearing);
+            return;
+        }
+    }
+    const unsigned ahead = SPREAD ? a.clearing : 0;
     const int per_block = kRowBlock / a.lanes;
     const int lane = static_cast<int>(threadIdx.x) % a.lanes;
     const int col = lane * W, have = a.width - col;  // have <= 0: a lane beyond the row
-    for (size_t t = static_cast<size_t>(blockIdx.x) * per_block + threadIdx.x / a.lanes; t < a.tokens;
-         t += static_cast<size_t>(gridDim.x) * per_block) {
+    for (size_t t = static_cast<size_t>(blockIdx.x - ahead) * per_block + threadIdx.x / a.lanes; t < a.tokens;
+         t += static_cast<size_t>(gridDim.x - ahead) * per_block) {
         float x[W], acc[W] = {};
         if constexpr (SPREAD || DOTS) load_some<T, W>(a.x + t * a.x_stride + col, have, x);
         for (int j = 0; j < a.k; ++j) {

@@ -373,8 +373,8 @@ def combine_rows_backward(grad_out: torch.Tensor, position: torch.Tensor, rows: 
     """The gradients of combine_rows from that of its result: grad_rows, and
     with rows given also grad_weights (T, k) float32, as a pair.  weights are
     the forward call's.  grad_rows has the shape of rows, or (T * k, H) without
-    them; the rows of dropped slots are zeros, and as in dispatch_rows rows
-    that no slot names are left as they were."""
+    them.  The rows of dropped slots are zeros, and so are the rows that no slot
+    names; a given `out` keeps those as they were, as in dispatch_rows."""
     _rows(grad_out, "grad_out")
     device, width = grad_out.device, grad_out.shape[1]
     tokens, k = _places(position, weights, device)
@@ -397,10 +397,11 @@ def combine_rows_backward(grad_out: torch.Tensor, position: torch.Tensor, rows: 
     dots = grad_weights_out
     if rows is not None and dots is None:
         dots = torch.empty(tokens, k, dtype=torch.float32, device=device)
-    code = _lib.load().rs_combine_rows_backward(
+    name = "rs_combine_rows_backward_all" if out is None else "rs_combine_rows_backward"
+    code = getattr(_lib.load(), name)(
         grad_out.data_ptr(), _ROW_DTYPES[grad_out.dtype], tokens, width, grad_out.stride(0), position.data_ptr(),
         _ptr(weights), k, _ptr(rows), 0 if rows is None else rows.stride(0), grad.data_ptr(), grad.stride(0), count,
         _ptr(dots), _raw_stream(device.index))
     if code:
-        _fail(code, "rs_combine_rows_backward")
+        _fail(code, name)
     return grad if rows is None else (grad, dots)

@@ -169,3 +169,15 @@ def test_oracle_rows_are_each_other_transposed():
     there = (eo.spread(x, position, w, np.zeros((T * k, H))) * y).sum()
     assert abs(there - (x * eo.join(y, position, w)[0]).sum()) < 1e-12
     assert abs(there - (w * eo.dots(x, y, position)[0]).sum()) < 1e-12
+
+
+def test_row_checks_of_the_whole_gradient(lib):
+    """rs_combine_rows_backward_all refuses what rs_combine_rows_backward does."""
+    def call(rows=E, gr=D, gw=F, g=A, dtype=F16, num=N, position=B, weights=C, k=K, tokens=T, width=H, stride=H):
+        return lib.rs_combine_rows_backward_all(g, dtype, tokens, width, H, position, weights, k, rows, H, gr, stride,
+                                                num, gw, None)
+    for bad in (dict(rows=None), dict(rows=E + 1), dict(gw=F + 2), dict(gw=A), dict(gw=D), dict(gr=E), dict(gr=None),
+                dict(stride=H - 1), dict(g=None), dict(gw=B), dict(gr=C), dict(dtype=3), dict(width=0), dict(k=65),
+                dict(tokens=2**30), dict(num=2**31), dict(position=B + 2), dict(weights=C + 2)):
+        assert call(**bad) == INVALID, bad
+    assert call(tokens=0, num=0, g=None, gr=None, position=None, gw=None) == OK

@@ -1,0 +1,99 @@
+"""GPU tests of the mixture-of-experts calls at their edges: rows that no slot
+names, and values and tensors that the other tests do not pass."""
+import numpy as np
+import pytest
+
+import expert_oracle as eo
+from test_gpu_experts import DTYPES, close, host, note, rounded
+
+torch = pytest.importorskip("torch")
+rs = pytest.importorskip("lsd_radix_sort_pass_amd")
+
+pytestmark = pytest.mark.gpu
+
+
+def poison(*shapes_and_dtypes):
+    """Leaves NaN in the memory that the next allocations of these sizes get."""
+    held = [torch.full(shape, float("nan"), dtype=dtype, device="cuda") for shape, dtype in shapes_and_dtypes]
+    del held
+
+
+def places(rng, T, k, num_rows, kind):
+    """Places of T * k slots among num_rows rows, some rows without a slot."""
+    n = T * k
+    if kind == "fewer slots than rows":
+        p = rng.permutation(num_rows)[:n]
+    elif kind == "a part of a sort":                  # most places lie behind the rows
+        p = rng.permutation(4 * n)[:n]
+    else:                                             # "skipped": half of them do
+        p = rng.permutation(n)
+        p = np.where(rng.random(n) < 0.5, p, 2**31 - 1 - p)
+    p = np.where(rng.random(n) < 0.2, ~p, p)          # dropped ones among both
+    return p.astype(np.int32).reshape(T, k)
+
+
+# Narrow and wide rows, small and many slots, the 512-byte rule's two sides.
+UNNAMED = [(3, 2, 40), (7, 8, 1537), (1, 1, 1), (61, 3, 129), (5, 17, 2051), (2100, 8, 100), (2100, 8, 520),
+           (700, 30, 264), (9, 2, 5000)]
+
+
+@pytest.mark.parametrize("kind", ["fewer slots than rows", "a part of a sort", "skipped"])
+@pytest.mark.parametrize("T,k,width", UNNAMED)
+def test_gradient_of_unnamed_rows(T, k, width, kind):
+    """A row that combine_rows does not read has gradient zero."""
+    rng = np.random.default_rng(T + k + width)
+    for dtype in DTYPES if T < 100 else ["bfloat16"]:
+        note(f"combine_rows_backward {dtype} T={T} k={k} width={width} {kind}")
+        num_rows = T * k + (T * k + 5 if kind == "fewer slots than rows" else 0)
+        position = places(rng, T, k, num_rows, kind)
+        dp = torch.from_numpy(position).cuda()
+        g, _ = rounded(rng.normal(size=(T, width)), dtype)
+        rows, _ = rounded(rng.normal(size=(num_rows, width)), dtype)
+        weights = rng.normal(size=(T, k)).astype(np.float32)
+        dw = torch.from_numpy(weights).cuda()
+        exact = eo.spread(host(g), position, weights, np.zeros((num_rows, width)))
+        poison(((num_rows, width), DTYPES[dtype]))
+        grad, _ = rs.combine_rows_backward(g, dp, rows, dw)
+        close(grad, exact, eo.spread_bound(exact, dtype), "with the weights' gradient")
+        if num_rows == T * k:
+            poison(((num_rows, width), DTYPES[dtype]))
+            grad = rs.combine_rows_backward(g, dp, weights=dw)
+            close(grad, exact, eo.spread_bound(exact, dtype), "rows alone")
+        # A given buffer keeps what it has in such rows.
+        out = torch.full((num_rows, width), 5.0, dtype=DTYPES[dtype], device="cuda")
+        rs.combine_rows_backward(g, dp, rows, dw, out=out)
+        exact = eo.spread(host(g), position, weights, np.full((num_rows, width), 5.0))
+        close(out, exact, eo.spread_bound(exact, dtype), "given buffer")
+
+
+def test_gradient_of_rows_without_tokens():
+    note("combine_rows_backward T=0")
+    poison(((9, 16), torch.float32))
+    x = torch.empty(0, 16, device="cuda")
+    grad, dots = rs.combine_rows_backward(x, torch.empty(0, 2, dtype=torch.int32, device="cuda"),
+                                          torch.randn(9, 16, device="cuda"))
+    assert grad.shape == (9, 16) and (grad == 0).all() and dots.shape == (0, 2)
+
+
+@pytest.mark.parametrize("k,width", [(8, 100), (8, 264), (8, 600), (1, 2100)])
+def test_gradient_of_unnamed_rows_among_many(k, width):
+    """More slots than 2^16, where narrow rows are cleared otherwise than wide
+    ones.  A product of two float32 rounded once is the result to the bit."""
+    T = 72_000 // k
+    n = T * k
+    note(f"combine_rows_backward T={T} k={k} width={width}")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(width)
+    position = torch.randperm(n, generator=gen, device="cuda").to(torch.int32)
+    position[::3] += n                                            # behind the rows
+    position[1::7] = ~position[1::7]                              # dropped
+    g = torch.randn(T, width, generator=gen, device="cuda").bfloat16()
+    rows = torch.randn(n, width, generator=gen, device="cuda").bfloat16()
+    w = torch.rand(T, k, generator=gen, device="cuda")
+    want = torch.zeros_like(rows)
+    s = torch.nonzero((position >= 0) & (position < n))[:, 0]
+    want[position[s].long()] = (g[s // k].float() * w.reshape(-1)[s, None]).bfloat16()
+    for with_dots in (True, False):
+        poison(((n, width), torch.bfloat16))
+        grad = rs.combine_rows_backward(g, position.reshape(T, k), rows if with_dots else None, w)
+        assert torch.equal(grad[0] if with_dots else grad, want)
