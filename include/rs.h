@@ -360,7 +360,8 @@ rs_status rs_dispatch_rows(const void *x, int dtype, size_t tokens, int width, s
 /* Its gradients: grad_x[t] = sum over j of w[t][j] * grad_rows[place of (t, j)]
  * and, if grad_weights is given, grad_weights[t][j] = <x[t], grad_rows[place]>
  * (x may be NULL otherwise).  Dropped slots and skipped places add nothing and
- * have gradient 0; their rows are not read. */
+ * have gradient 0; their rows are not read.  For places that differ: of several
+ * slots that name a row rs_dispatch_rows writes one, here each has a gradient. */
 rs_status rs_dispatch_rows_backward(const void *grad_rows, int dtype, size_t num_rows, size_t grad_rows_stride,
                                     const int32_t *position, const float *weights, int k, const void *x,
                                     size_t x_stride, void *grad_x, size_t grad_x_stride, float *grad_weights,
@@ -378,7 +379,10 @@ rs_status rs_combine_rows(const void *rows, int dtype, size_t num_rows, size_t r
  * a dropped slot (every row of rs_sort_experts's places is written), and, if
  * grad_weights is given, grad_weights[t][j] = <grad_out[t], rows[place]>, 0 for
  * a dropped slot (rows may be NULL otherwise).  As in rs_dispatch_rows a row
- * that no slot names is left as it was. */
+ * that no slot names is left as it was.  The slots' places have to differ, as
+ * those of rs_sort_experts do: rs_combine_rows reads a row as often as it is
+ * named, but its gradient here is that of one of the slots that name it (each
+ * element from any of them), not their sum. */
 rs_status rs_combine_rows_backward(const void *grad_out, int dtype, size_t tokens, int width, size_t grad_out_stride,
                                    const int32_t *position, const float *weights, int k, const void *rows,
                                    size_t rows_stride, void *grad_rows, size_t grad_rows_stride, size_t num_rows,

@@ -278,9 +278,10 @@ def dispatch_rows(x: torch.Tensor, position: torch.Tensor, weights: Optional[tor
 
     x (T, H) float32, float16 or bfloat16; position (T, k) int32 as
     sort_experts gives it; weights (T, k) float32.  out (rows, H) defaults to
-    a new (T * k, H) tensor, which sort_experts's positions fill; rows of a
-    given `out` that no slot names are left as they were, and places beyond it
-    are skipped."""
+    a new (T * k, H) tensor, which sort_experts's positions fill: without `out`
+    the places have to be such, each row named by a slot.  Rows of a given `out`
+    that no slot names are left as they were, and places beyond it are skipped.
+    A row that several slots name gets each element from any of them."""
     _rows(x, "x")
     device = x.device
     tokens, k = _places(position, weights, device)
@@ -374,7 +375,9 @@ def combine_rows_backward(grad_out: torch.Tensor, position: torch.Tensor, rows: 
     with rows given also grad_weights (T, k) float32, as a pair.  weights are
     the forward call's.  grad_rows has the shape of rows, or (T * k, H) without
     them.  The rows of dropped slots are zeros, and so are the rows that no slot
-    names; a given `out` keeps those as they were, as in dispatch_rows."""
+    names; a given `out` keeps those as they were, as in dispatch_rows.  The
+    places have to differ, as sort_experts's do: a row that several slots name
+    gets the gradient of one of them, not their sum."""
     _rows(grad_out, "grad_out")
     device, width = grad_out.device, grad_out.shape[1]
     tokens, k = _places(position, weights, device)

@@ -97,3 +97,23 @@ def test_gradient_of_unnamed_rows_among_many(k, width):
         poison(((n, width), torch.bfloat16))
         grad = rs.combine_rows_backward(g, position.reshape(T, k), rows if with_dots else None, w)
         assert torch.equal(grad[0] if with_dots else grad, want)
+
+
+@pytest.mark.parametrize("width", [40, 600])
+def test_rows_named_twice(width):
+    """A row that two slots name: combine_rows reads it for both, and of the
+    gradients the row gets one, the weights each their own."""
+    note(f"rows named twice, width {width}")
+    rng = np.random.default_rng(width)
+    position = torch.tensor([[0, 4], [4, 1], [2, 7]], dtype=torch.int32, device="cuda")
+    x, _ = rounded(rng.normal(size=(3, width)), "float32")
+    rows, v = rounded(rng.normal(size=(6, width)), "float32")
+    w = torch.tensor([[1.0, 2.0], [4.0, 0.5], [1.0, 8.0]], device="cuda")       # products are exact
+    exact, size = eo.join(v, host(position), host(w))
+    close(rs.combine_rows(rows, position, w), exact, eo.join_bound(exact, size, 2, "float32"), "combine_rows")
+    poison(((6, width), torch.float32))
+    grad, grad_w = rs.combine_rows_backward(x, position, rows, w)
+    sums, sizes = eo.dots(host(x), v, host(position))
+    close(grad_w, sums, eo.dots_bound(sizes, width), "weights")
+    assert torch.equal(grad[[0, 1, 2, 3, 5]], torch.stack([x[0], x[1] * 0.5, x[2], x[0] * 0, x[0] * 0]))
+    assert ((grad[4] == x[0] * 2) | (grad[4] == x[1] * 4)).all()
