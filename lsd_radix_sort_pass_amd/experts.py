@@ -383,14 +383,18 @@ def combine_rows_backward(grad_out: torch.Tensor, position: torch.Tensor, rows: 
     tokens, k = _places(position, weights, device)
     if grad_out.shape[0] != tokens:
         raise ValueError("position must have a row for each row of grad_out")
-    count = tokens * k if out is None else out.shape[0]
     if rows is not None:
-        count = rows.shape[0]
-        _rows(rows, "rows", device, (grad_out.dtype,), (count, width))
+        _rows(rows, "rows", device, (grad_out.dtype,))
+        if rows.shape[1] != width:
+            raise ValueError("rows must have the width of grad_out")
     elif grad_weights_out is not None:
         raise ValueError("grad_weights_out needs rows")
     if out is not None:
-        _rows(out, "out", device, (grad_out.dtype,), (count, width))
+        _rows(out, "out", device, (grad_out.dtype,), None if rows is None else rows.shape)
+        if out.shape[1] != width:
+            raise ValueError("out must have the width of grad_out")
+    like = out if rows is None else rows
+    count = tokens * k if like is None else like.shape[0]
     if grad_weights_out is not None:
         _flat(grad_weights_out, "grad_weights_out", _F32, device, (tokens, k))
     if stream is not None or device.index != _current():

@@ -117,3 +117,26 @@ def test_rows_named_twice(width):
     close(grad_w, sums, eo.dots_bound(sizes, width), "weights")
     assert torch.equal(grad[[0, 1, 2, 3, 5]], torch.stack([x[0], x[1] * 0.5, x[2], x[0] * 0, x[0] * 0]))
     assert ((grad[4] == x[0] * 2) | (grad[4] == x[1] * 4)).all()
+
+
+def test_refusals_of_the_rows_gradient():
+    """What is no tensor is a TypeError, a wrong shape a ValueError, whichever
+    argument it is."""
+    note("refusals of combine_rows_backward")
+    g = torch.randn(6, 32, device="cuda")
+    pos = torch.arange(12, dtype=torch.int32, device="cuda").reshape(6, 2)
+    rows = torch.randn(12, 32, device="cuda")
+    for bad in ([1.0], 3, "rows"):
+        for kw in (dict(rows=bad), dict(out=bad), dict(rows=rows, out=bad), dict(rows=bad, out=rows),
+                   dict(weights=bad), dict(rows=rows, grad_weights_out=bad)):
+            with pytest.raises(TypeError):
+                rs.combine_rows_backward(g, pos, **kw)
+    scalar, empty = torch.zeros((), device="cuda"), torch.empty(0, device="cuda")
+    for bad in (scalar, empty, rows[0], rows[None], rows[:, :31], rows.cpu()):
+        for kw in (dict(rows=bad), dict(out=bad), dict(rows=rows, out=bad)):
+            with pytest.raises(ValueError):
+                rs.combine_rows_backward(g, pos, **kw)
+    with pytest.raises(ValueError):
+        rs.combine_rows_backward(g, pos, rows, out=torch.empty(13, 32, device="cuda"))
+    with pytest.raises(TypeError):
+        rs.combine_rows_backward(g, pos, rows.half())
