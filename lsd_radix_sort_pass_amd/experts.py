@@ -13,8 +13,9 @@ Each call only marshals arguments to the C ABI (include/rs.h, which states the
 results in full).  Gradients are calls of their own (`*_backward`), as every
 call here is one or two kernel launches on the caller's stream: all of them
 can be captured into a graph.  They do not record for autograd, and refuse
-tensors that require a gradient while gradients are enabled: call them inside
-a torch.autograd.Function, or under torch.no_grad().
+tensors that require a gradient while gradients are enabled (call them inside
+a torch.autograd.Function, or under torch.no_grad()) or that carry a
+forward-mode tangent (inside a torch.autograd.Function).
 
 `stream` works as if the call were made under torch.cuda.stream(stream):
 outputs and temp storage that a call allocates belong to that stream, and
@@ -28,6 +29,7 @@ import ctypes
 from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
+import torch.autograd.forward_ad as _forward
 
 from . import _lib
 
@@ -108,6 +110,15 @@ def _places(position, weights, device, name="position") -> Tuple[int, int]:
     return shape
 
 
+def _refuse_tangents(**tensors) -> None:
+    """Refuses tensors that carry a forward-mode tangent; called while such a
+    level is entered.  (None does where forward gradients are off.)"""
+    for name, t in tensors.items():
+        if t is not None and _forward.unpack_dual(t).tangent is not None:
+            raise ValueError(f"{name} carries a tangent, which this call does not record: use it in a "
+                             "torch.autograd.Function")
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -174,6 +185,8 @@ def route_topk(logits: torch.Tensor, k: int, mode: str = "softmax", renormalize:
         _flat(weights_out, "weights_out", _F32, device, (tokens, k))
     if experts_out is not None:
         _flat(experts_out, "experts_out", _I32, device, (tokens, k))
+    if _forward._current_level >= 0:
+        _refuse_tangents(logits=logits, weights_out=weights_out)
     if stream is not None or device.index != _current():
         with _on(device, stream, logits, weights_out, experts_out):
             return route_topk(logits, k, mode, renormalize, scale, weights_out, experts_out)
@@ -207,6 +220,8 @@ def route_topk_backward(logits: torch.Tensor, experts: torch.Tensor, grad_weight
     _flat(grad_weights, "grad_weights", _F32, device, (tokens, k))
     if out is not None:
         _rows(out, "out", device, (logits.dtype,), (tokens, count))
+    if _forward._current_level >= 0:
+        _refuse_tangents(logits=logits, grad_weights=grad_weights, out=out)
     if stream is not None or device.index != _current():
         with _on(device, stream, logits, experts, grad_weights, out):
             return route_topk_backward(logits, experts, grad_weights, mode, renormalize, scale, out)
@@ -292,6 +307,8 @@ def dispatch_rows(x: torch.Tensor, position: torch.Tensor, weights: Optional[tor
         _rows(out, "out", device, (x.dtype,))
         if out.shape[1] != width:
             raise ValueError("out must have the width of x")
+    if _forward._current_level >= 0:
+        _refuse_tangents(x=x, weights=weights, out=out)
     if stream is not None or device.index != _current():
         with _on(device, stream, x, position, weights, out):
             return dispatch_rows(x, position, weights, out)
@@ -324,6 +341,8 @@ def dispatch_rows_backward(grad_rows: torch.Tensor, position: torch.Tensor, x: O
         _rows(out, "out", device, (grad_rows.dtype,), (tokens, width))
     if grad_weights_out is not None:
         _flat(grad_weights_out, "grad_weights_out", _F32, device, (tokens, k))
+    if _forward._current_level >= 0:
+        _refuse_tangents(grad_rows=grad_rows, x=x, weights=weights, out=out, grad_weights_out=grad_weights_out)
     if stream is not None or device.index != _current():
         with _on(device, stream, grad_rows, position, x, weights, out, grad_weights_out):
             return dispatch_rows_backward(grad_rows, position, x, weights, out, grad_weights_out)
@@ -354,6 +373,8 @@ def combine_rows(rows: torch.Tensor, position: torch.Tensor, weights: Optional[t
     tokens, k = _places(position, weights, device)
     if out is not None:
         _rows(out, "out", device, (rows.dtype,), (tokens, width))
+    if _forward._current_level >= 0:
+        _refuse_tangents(rows=rows, weights=weights, out=out)
     if stream is not None or device.index != _current():
         with _on(device, stream, rows, position, weights, out):
             return combine_rows(rows, position, weights, out)
@@ -397,6 +418,8 @@ def combine_rows_backward(grad_out: torch.Tensor, position: torch.Tensor, rows: 
     count = tokens * k if like is None else like.shape[0]
     if grad_weights_out is not None:
         _flat(grad_weights_out, "grad_weights_out", _F32, device, (tokens, k))
+    if _forward._current_level >= 0:
+        _refuse_tangents(grad_out=grad_out, rows=rows, weights=weights, out=out, grad_weights_out=grad_weights_out)
     if stream is not None or device.index != _current():
         with _on(device, stream, grad_out, position, rows, weights, out, grad_weights_out):
             return combine_rows_backward(grad_out, position, rows, weights, out, grad_weights_out)

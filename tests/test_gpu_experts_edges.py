@@ -140,3 +140,65 @@ def test_refusals_of_the_rows_gradient():
         rs.combine_rows_backward(g, pos, rows, out=torch.empty(13, 32, device="cuda"))
     with pytest.raises(TypeError):
         rs.combine_rows_backward(g, pos, rows.half())
+
+
+def test_refusal_of_tangents():
+    """A tensor that carries a forward-mode tangent is refused rather than its
+    tangent lost, unless forward gradients are off, as they are inside a
+    torch.autograd.Function."""
+    note("tangents")
+    import torch.autograd.forward_ad as fwad
+    x, w = torch.randn(6, 32, device="cuda"), torch.rand(6, 2, device="cuda")
+    pos = torch.arange(12, dtype=torch.int32, device="cuda").reshape(6, 2)
+    rows = torch.randn(12, 32, device="cuda")
+    ids = torch.zeros(6, 2, dtype=torch.int32, device="cuda")
+    with fwad.dual_level():
+        def dual(t):
+            return fwad.make_dual(t, torch.ones_like(t))
+        calls = [lambda: rs.route_topk(dual(x), 2), lambda: rs.route_topk_backward(dual(x), ids, w),
+                 lambda: rs.route_topk_backward(x, ids, dual(w)), lambda: rs.dispatch_rows(dual(x), pos),
+                 lambda: rs.dispatch_rows(x, pos, dual(w)), lambda: rs.combine_rows(dual(rows), pos),
+                 lambda: rs.combine_rows(rows, pos, dual(w)), lambda: rs.dispatch_rows_backward(dual(rows), pos),
+                 lambda: rs.dispatch_rows_backward(rows, pos, dual(x)), lambda: rs.combine_rows_backward(dual(x), pos),
+                 lambda: rs.combine_rows_backward(x, pos, dual(rows), w),
+                 lambda: rs.dispatch_rows(x, pos, out=dual(rows))]
+        for i, call in enumerate(calls):
+            with pytest.raises(ValueError, match="tangent"):
+                print(i, call())
+        with torch.no_grad(), pytest.raises(ValueError, match="tangent"):
+            rs.combine_rows(dual(rows), pos)
+        # Tensors without one are as ever, and so is every tensor where none is recorded.
+        want = rs.combine_rows(rows, pos, w)
+        off = dual(rows)
+        with fwad._set_fwd_grad_enabled(False):
+            assert torch.equal(rs.combine_rows(off, pos, w), want)
+    assert torch.equal(rs.combine_rows(rows, pos, w), want)
+
+
+class JvpCombine(torch.autograd.Function):
+    @staticmethod
+    def forward(rows, position, w):
+        return rs.combine_rows(rows, position, w)
+
+    @staticmethod
+    def setup_context(ctx, inputs, output):
+        ctx.save_for_forward(*inputs)
+
+    @staticmethod
+    def jvp(ctx, rows_t, _, w_t):
+        rows, position, w = ctx.saved_tensors
+        return rs.combine_rows(rows_t, position, w) + rs.combine_rows(rows, position, w_t)
+
+
+def test_tangents_through_a_function():
+    """combine_rows is linear in its rows and in its weights."""
+    note("tangents through a function")
+    import torch.autograd.forward_ad as fwad
+    pos = torch.randperm(12, device="cuda").to(torch.int32).reshape(6, 2)
+    rows, rows_t = torch.randn(2, 12, 32, device="cuda")
+    w, w_t = torch.rand(2, 6, 2, device="cuda")
+    with fwad.dual_level():
+        out = JvpCombine.apply(fwad.make_dual(rows, rows_t), pos, fwad.make_dual(w, w_t))
+        value, tangent = fwad.unpack_dual(out)
+    assert torch.equal(value, rs.combine_rows(rows, pos, w))
+    assert torch.equal(tangent, rs.combine_rows(rows_t, pos, w) + rs.combine_rows(rows, pos, w_t))
