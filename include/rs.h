@@ -316,15 +316,20 @@ typedef enum rs_gate { RS_GATE_SOFTMAX = 0, RS_GATE_SIGMOID = 1 } rs_gate;
  * as weights_out[t][j] = scale * p, or scale * p / (sum of the chosen p) if
  * renormalize != 0.  -0 equals +0; a NaN ranks above every number.  A logit of
  * -inf marks an expert that the row may not use: it is never chosen, and slots
- * left over get expert -1 and weight 0 (a row of -inf: all of them).  NaN and
- * +inf give what the formulas give.  1 <= k <= min(experts, RS_MAX_CHOICES). */
+ * left over get expert -1 and weight 0 (a row of -inf: all of them).  A
+ * sigmoid of NaN is NaN and of +inf 1.  A softmax takes the exponentials of the
+ * differences from the largest logit, so a NaN or +inf makes all weights of its
+ * row NaN.  1 <= k <= min(experts, RS_MAX_CHOICES). */
 rs_status rs_route_topk(const void *logits, int dtype, size_t tokens, int experts, size_t stride, int k, int gate,
                         int renormalize, float scale, float *weights_out, int32_t *experts_out, hipStream_t stream);
 
 /* The gradient of the logits from that of the weights, for the experts that
  * rs_route_topk chose; every element of the rows is written.  Slots whose
  * expert is outside [0, experts) or has a logit of -inf add nothing, whatever
- * their gradient holds; an expert named by several slots gets the sum. */
+ * their gradient holds; an expert named by several slots gets the sum.  A logit
+ * of -inf has gradient 0; elsewhere NaN and infinities give what the formulas
+ * give: with a softmax over the row one NaN among its logits or the gradients
+ * of its weights, or a logit of +inf, makes NaN of all of it. */
 rs_status rs_route_topk_backward(const void *logits, int dtype, size_t tokens, int experts, size_t stride,
                                  const int32_t *chosen, const float *grad_weights, int k, int gate, int renormalize,
                                  float scale, void *grad_logits, size_t grad_stride, hipStream_t stream);

@@ -427,7 +427,10 @@ __global__ __launch_bounds__(kRouteBlock) void route_topk_kernel(const T *__rest
 //   softmax, renormalized  dl_i = scale * u_i * (a_i - sum_j h_j u_j), chosen i only
 //   sigmoid                dl_i = scale * a_i * p_i * (1 - p_i), chosen i only
 //   sigmoid, renormalized  dl_i = scale * u_i * (a_i - sum_j h_j u_j) * (1 - p_i)
-// Only the first needs the whole row; the others read the k chosen logits.
+// Only the first needs the whole row; the others read the k chosen logits.  Its
+// -0 marks a barred expert, whose gradient is 0 whatever the row holds; an
+// exponential that underflows is +0 and follows the formula (a row with a NaN or
+// +inf, or a NaN gradient of a weight, has no finite gradient anywhere else).
 // Lane j < k of the group holds slot j; the slots' terms reach the lanes that
 // hold their elements through LDS.  Bound by memory: 32768 x 256 float32,
 // softmax, k = 8, 18.2 us (69 MB, 3.8 TB/s).
@@ -459,7 +462,7 @@ __global__ __launch_bounds__(kRouteBlock) void route_topk_backward_kernel(
         total = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            p[v] = p[v] == -__builtin_inff() ? 0.0f : exp_in_sum(p[v] - top);
+            p[v] = p[v] == -__builtin_inff() ? -0.0f : exp_in_sum(p[v] - top);
             total += p[v];
         }
         total = group_sum<G>(total);
@@ -522,7 +525,7 @@ __global__ __launch_bounds__(kRouteBlock) void route_topk_backward_kernel(
             const float a = terms[sub][i0 + w];
             if (whole) {
                 const float q = p[c * W + w] / total;
-                f[w] = p[c * W + w] == 0.0f ? 0.0f : scale * (q * (a - mean));
+                f[w] = __float_as_uint(p[c * W + w]) == 0x80000000u ? 0.0f : scale * (q * (a - mean));
             } else {
                 f[w] = scale * a;
             }

@@ -202,3 +202,39 @@ def test_tangents_through_a_function():
         value, tangent = fwad.unpack_dual(out)
     assert torch.equal(value, rs.combine_rows(rows, pos, w))
     assert torch.equal(tangent, rs.combine_rows(rows_t, pos, w) + rs.combine_rows(rows, pos, w_t))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("E", [5, 64, 300])
+def test_route_not_finite(dtype, E):
+    """A +inf or a NaN in a row: every weight of a softmax is NaN, and every
+    element of its gradient but those of barred experts, also those so far
+    below the largest that their exponentials are 0."""
+    note(f"route_topk {dtype} E={E} with +inf and NaN")
+    inf, nan = float("inf"), float("nan")
+    l = torch.full((4, E), -300.0)                      # exp(-300 - 0) is 0 in float32
+    l[:, 0], l[:, 1], l[:, 2], l[:, 4] = 0.0, 1.0, -inf, -200.0
+    l[1, 3], l[2, 3] = inf, nan
+    logits = l.to(DTYPES[dtype]).cuda()
+    barred = torch.zeros(E, dtype=torch.bool)
+    barred[2] = True
+    k = 3
+    for renorm in (False, True):
+        w, e = rs.route_topk(logits, k, "softmax", renorm)
+        assert e[[0, 3]].tolist() == [[1, 0, 4]] * 2
+        assert e[1:3].tolist() == [[3, 1, 0]] * 2
+        assert torch.isfinite(w[[0, 3]]).all() and torch.isnan(w[1:3]).all()
+        g = torch.ones(4, k, device="cuda")
+        g[3, 1] = nan                                   # a gradient that is not finite, finite logits
+        grad = rs.route_topk_backward(logits, e, g, "softmax", renorm).float().cpu()
+        assert torch.isfinite(grad[0]).all()
+        chosen = torch.zeros(4, E, dtype=torch.bool).scatter_(1, e.cpu().long(), True)
+        for t in (1, 2, 3):
+            bad = chosen[t] if renorm else ~barred          # renormalized: the others have no part in it
+            assert torch.isnan(grad[t][bad]).all() and (grad[t][~bad] == 0).all(), t
+    for renorm in (False, True):                        # the sigmoid of +inf is 1, that of NaN a NaN
+        w, e = rs.route_topk(logits, k, "sigmoid", renorm)
+        assert torch.isfinite(w[[0, 1, 3]]).all()
+        assert torch.isnan(w[2] if renorm else w[2, :1]).all() and torch.isfinite(w[2, 1:]).all() != renorm
+        if not renorm:
+            assert w[1, 0] == 1.0
