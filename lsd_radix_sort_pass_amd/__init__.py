@@ -355,7 +355,7 @@ def prof_samples(kind: int, sub: int = -1) -> list:
 
 def prof_ranker(mode: int) -> int:
     """Local ranker (test and measurement hook): 0 LDS-atomic (default), 1
-    ballot match ranker (32-bit keys; see rs_prof_ranker).  Returns the
+    ballot match ranker (32-bit keys, experts; see rs_prof_ranker).  Returns the
     previous mode."""
     return int(_lib.load().rs_prof_ranker(int(mode)))
 

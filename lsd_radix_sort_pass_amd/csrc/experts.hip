@@ -165,8 +165,8 @@ rs_status sort_experts(const ID *ids, size_t n, int first, int experts, int32_t 
     uint32_t *totals = table + size_t{p.chunks} * rs::table_stride(e);
     const auto place = [&](auto kernel, unsigned grid, size_t chunk) {
         return launch_kernel(RS_KERNEL_EXPERT, stream, [&] {
-            run_kernel(kernel, grid, rs::kPlaceBlock, stream, ids, n, f, e, chunk, table, totals, order, position,
-                       offsets);
+            run_kernel(kernel, grid, rs::kPlaceBlock, stream, ids, n, f, e, chunk, table, totals, g_ranker == 1, order,
+                       position, offsets);
         });
     };
     const auto run = [&](auto keys) {

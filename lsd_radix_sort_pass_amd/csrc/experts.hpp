@@ -631,8 +631,11 @@ __global__ __launch_bounds__(kPlaceBlock) void expert_scan_kernel(uint32_t *__re
 // so equal keys keep slot order whatever the waves' timing.  The last two terms
 // are what an LDS add to the wave's counter of the key returns: like the pass
 // kernel's local rank, this takes the lanes' same-address adds to be served
-// in lane order, which the lane order test pins.  Dropped slots, often a long
-// run of padding, are ranked by a ballot instead of 64 adds to one address.
+// in lane order, a measured property, here among up to 1025 counters and with
+// lanes masked out, which the tests of this sort pin on the lane order test's
+// patterns.  match: ranked by ballots instead (match_rank), whatever that order;
+// 2^20 slots of 256 experts take 2.5 us more so, 8192 slots 4.3.  Dropped slots, often a long run of
+// padding, are ranked by a ballot instead of 64 adds to one address.
 // A tile's slots are put in key order in LDS, so that order is written in
 // runs (the sort of 2^20 slots of 256 experts takes 13.4 us so, 16.1 without).
 // KEYS >= experts sizes the LDS.  Bound by the chain of round trips: ids and
@@ -647,12 +650,13 @@ template <class ID, int ITEMS, int KEYS, int TABLE>
 __global__ __launch_bounds__(kPlaceBlock) void expert_place_kernel(const ID *__restrict__ ids, size_t n, ID first,
                                                                    uint32_t experts, size_t chunk,
                                                                    const uint32_t *__restrict__ table,
-                                                                   const uint32_t *__restrict__ totals,
+                                                                   const uint32_t *__restrict__ totals, bool match,
                                                                    int32_t *__restrict__ order,
                                                                    int32_t *__restrict__ position,
                                                                    int32_t *__restrict__ offsets) {
     constexpr uint32_t kTile = kPlaceBlock * ITEMS;
-    static_assert(kTile <= 0x10000 && KEYS <= kPlaceBlock);
+    constexpr int kKeyBits = KEYS == 256 ? 9 : 11;  // of keys up to KEYS
+    static_assert(kTile <= 0x10000 && KEYS <= kPlaceBlock && KEYS < 1 << kKeyBits);
     __shared__ uint32_t count[kPlaceWaves * (KEYS + 1)];  // [wave][key]
     __shared__ uint32_t base[KEYS + 1];                   // place of the next slot of a key
     __shared__ uint32_t delta[KEYS + 1];                  // a slot's place less its place in the tile
@@ -742,6 +746,10 @@ __global__ __launch_bounds__(kPlaceBlock) void expert_place_kernel(const ID *__r
         uint32_t *const own = count + wave * keys;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
+            if (match) {
+                rank[i] = match_rank<kKeyBits>(key[i], key[i] <= experts, own, 1u);
+                continue;
+            }
             if (key[i] < experts) rank[i] = atomicAdd(&own[key[i]], 1u);
             const uint64_t dropped = __ballot(key[i] == experts);
             if (dropped != 0) {

@@ -238,3 +238,46 @@ def test_route_not_finite(dtype, E):
         assert torch.isnan(w[2] if renorm else w[2, :1]).all() and torch.isfinite(w[2, 1:]).all() != renorm
         if not renorm:
             assert w[1, 0] == 1.0
+
+
+def expert_patterns(rng, n, experts):
+    """Expert numbers whose equal ones stand in every relation to the lanes, the
+    half of the patterns with dropped slots between them."""
+    lane = np.arange(n) % 64
+    some = rng.integers(0, experts, n)
+    base = {"uniform": some, "all equal": np.full(n, experts - 1), "two": some % 2, "four": some % 4 * (experts // 4),
+            "sixteen": some % 16, "skewed": some & rng.integers(0, experts, n) & rng.integers(0, experts, n),
+            "lane mod 4": lane % 4, "lane div 16": lane // 16, "one bank": lane % 8 * 32 % experts,
+            "half waves": (lane >= 32) * 3, "reversed lanes": 63 - lane}
+    for name, ids in base.items():
+        yield name, ids
+        yield name + ", dropped between", np.where(rng.random(n) < 0.4, -1, ids)
+        yield name + ", odd lanes dropped", np.where(lane % 2 == 1, experts + 7, ids)
+
+
+@pytest.mark.parametrize("ranker", [0, 1])
+@pytest.mark.parametrize("experts", [100, 256, 1024])
+def test_sort_experts_lane_order(ranker, experts):
+    """The sort is stable whatever the lanes of equal experts, in every form of
+    its kernel: 1, 4 and 8 slots a thread of one workgroup, and 256 workgroups
+    under contention, with counts summed and scanned.  Ranker 0 takes this from
+    the order in which the LDS serves a wave's same-address adds, ranker 1 from
+    ballots."""
+    rng = np.random.default_rng(experts)
+    prev = rs.prof_ranker(ranker)
+    try:
+        for n in (1000, 4096, 8192, 1_050_000):
+            for name, ids in expert_patterns(rng, n, experts):
+                note(f"sort_experts ranker={ranker} n={n} experts={experts} {name}")
+                key = np.where((ids < 0) | (ids >= experts), experts, ids)
+                order = torch.from_numpy(np.argsort(key, kind="stable")).cuda()
+                place = torch.empty_like(order)
+                place[order] = torch.arange(n, device="cuda")
+                place = torch.where(torch.from_numpy(key == experts).cuda(), ~place, place)
+                res = rs.sort_experts(torch.from_numpy(ids.astype(np.int32)).cuda(), experts)
+                assert torch.equal(res.order.long(), order), name
+                assert torch.equal(res.position.long(), place), name
+                counts = np.concatenate([[0], np.cumsum(np.bincount(key, minlength=experts + 1)[:experts])])
+                assert np.array_equal(host(res.offsets), counts), name
+    finally:
+        rs.prof_ranker(prev)
