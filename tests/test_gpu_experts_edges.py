@@ -281,3 +281,135 @@ def test_sort_experts_lane_order(ranker, experts):
                 assert np.array_equal(host(res.offsets), counts), name
     finally:
         rs.prof_ranker(prev)
+
+
+# With dots, rows of more than 64 accesses take 1 to 4 chunks in flight together
+# for up to two slots a token, 1 or 2 for up to four: widths for each count of
+# either element size, most with a last access that is moved back.
+FEW_SLOTS = [(9, 1, 1537), (9, 2, 4099), (5, 2, 2500), (5, 1, 4000), (7, 2, 8191), (6, 1, 9001), (40, 2, 700),
+             (40, 1, 521), (30, 2, 300), (30, 1, 290), (5, 3, 2500), (6, 4, 4099), (7, 2, 4096), (4, 1, 8192)]
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("T,k,width", FEW_SLOTS)
+def test_rows_of_few_slots(dtype, T, k, width):
+    rng = np.random.default_rng(T * 100 + k * 10 + width)
+    for dropped, weighted, pad in ((0.0, True, 0), (0.4, False, 3), (0.4, True, 1)):
+        note(f"rows {dtype} T={T} k={k} width={width} dropped={dropped} weighted={weighted} pad={pad}")
+        position = rng.permutation(T * k).astype(np.int32).reshape(T, k)
+        mask = rng.random((T, k)) < dropped
+        if dropped:
+            mask[T // 2] = True                       # a token without any slot
+        position = np.where(mask, ~position, position).astype(np.int32)
+        dp = torch.from_numpy(position).cuda()
+        weights = rng.normal(size=(T, k)).astype(np.float32) if weighted else None
+        dw = torch.from_numpy(weights).cuda() if weighted else None
+        x, xv = rounded(rng.normal(size=(T, width + pad)), dtype)
+        rows, rv = rounded(rng.normal(size=(T * k, width + pad)), dtype)
+        x, xv, rows, rv = x[:, pad:], xv[:, pad:], rows[:, pad:], rv[:, pad:]
+        for p in position[position < 0]:
+            rows[~p] = float("nan")
+
+        def target(n):
+            store = torch.full((n, width + pad + 2), 5.0, dtype=DTYPES[dtype], device="cuda")
+            return store, store[:, 1:width + 1]
+        sums, sizes = eo.dots(xv, rv, position)
+        there = eo.spread(xv, position, weights, np.zeros((T * k, width)))
+        back, size = eo.join(rv, position, weights)
+        for given in (False, True):
+            store, out = target(T)
+            gw = torch.full((T, k), 7.0, device="cuda") if given else None
+            got, dots = rs.dispatch_rows_backward(rows, dp, x, dw, out=out if given else None, grad_weights_out=gw)
+            close(got, back, eo.join_bound(back, size, k, dtype), "dispatch_rows_backward")
+            close(dots, sums, eo.dots_bound(sizes, width), "dispatch_rows_backward weights")
+            assert (store[:, :1] == 5).all() and (store[:, width + 1:] == 5).all()
+            store, out = target(T * k)
+            got, dots = rs.combine_rows_backward(x, dp, rows, dw, out=out if given else None, grad_weights_out=gw)
+            close(got, there, eo.spread_bound(there, dtype), "combine_rows_backward")
+            close(dots, sums, eo.dots_bound(sizes, width), "combine_rows_backward weights")
+            assert (store[:, :1] == 5).all() and (store[:, width + 1:] == 5).all()
+        close(rs.combine_rows(rows, dp, dw), back, eo.join_bound(back, size, k, dtype), "combine_rows")
+        close(rs.dispatch_rows(x, dp, dw), there, eo.spread_bound(there, dtype), "dispatch_rows")
+
+
+def many_rows(T, k, width, dtype, dropped, seed):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    position = torch.randperm(T * k, generator=gen, device="cuda").to(torch.int32).reshape(T, k)
+    if dropped:
+        position = torch.where(torch.rand(T, k, generator=gen, device="cuda") < dropped, ~position, position)
+    x = torch.randn(T, width, generator=gen, device="cuda", dtype=dtype)
+    rows = torch.randn(T * k, width, generator=gen, device="cuda", dtype=dtype)
+    return position, x, rows, torch.rand(T, k, generator=gen, device="cuda") - 0.5
+
+
+def check_many_rows(position, x, rows, w, dtype):
+    """All four row calls on many tokens against float64 sums on the device,
+    block by block; bounds as in expert_oracle."""
+    T, k = position.shape
+    width = x.shape[1]
+    half, tiny = eo.HALF_STEP[dtype], eo.TINY[dtype]
+    joined, dots = rs.dispatch_rows_backward(rows, position, x, w)
+    plain = rs.combine_rows(rows, position, w)
+    spread, dots2 = rs.combine_rows_backward(x, position, rows, w)
+    sent = rs.dispatch_rows(x, position, w)
+    assert torch.equal(joined, plain) and torch.equal(spread, sent)
+    step = max(1, (1 << 26) // (width * k))
+    for a in range(0, T, step):
+        p, wt = position[a:a + step], w[a:a + step].double()
+        used = (p >= 0).double()
+        place = torch.where(p >= 0, p, ~p).long()
+        xd = x[a:a + step].double()
+        r = rows[place].double()                                            # (step, k, width)
+        term = r * (wt * used)[:, :, None]
+        exact, size = term.sum(1), term.abs().sum(1)
+        bound = (2 * k * eo.U32 * size + exact.abs() * half) * 1.01 + tiny
+        assert ((joined[a:a + step].double() - exact).abs() <= bound).all(), f"join, tokens from {a}"
+        pr = r * xd[:, None, :] * used[:, :, None]
+        bound = 2 * (width / 64 + 24) * eo.U32 * pr.abs().sum(2) + eo.TINY["float32"]
+        for d in (dots, dots2):
+            assert ((d[a:a + step].double() - pr.sum(2)).abs() <= bound).all(), f"dots, tokens from {a}"
+        exact = xd[:, None, :] * (wt * used)[:, :, None]
+        bound = exact.abs() * (half + eo.U32) * 1.01 + tiny
+        assert ((spread[place].double() - exact).abs() <= bound).all(), f"spread, tokens from {a}"
+
+
+@pytest.mark.parametrize("T,k,width,dtype", [(12_000, 2, 4099, "bfloat16"), (30_000, 1, 2501, "float32"),
+                                             (9_000, 3, 5003, "float16"), (4_000, 17, 2051, "bfloat16")])
+def test_rows_beyond_the_last_level_cache(T, k, width, dtype):
+    """More than 256 MiB of rows, which are read with non-temporal loads: odd
+    widths, few slots, some of them dropped."""
+    note(f"rows T={T} k={k} width={width} {dtype}")
+    check_many_rows(*many_rows(T, k, width, DTYPES[dtype], 0.3, T), dtype)
+
+
+@pytest.mark.parametrize("T,k,width", [((1 << 20) + 7, 1, 521), ((1 << 22) + 5, 1, 264), ((1 << 23) + 9, 1, 129),
+                                       ((1 << 22) // 17 + 999, 17, 257)])
+def test_rows_beyond_one_grid(T, k, width):
+    """More tokens (or slots) than the 2^20 workgroups of a launch take at once:
+    a workgroup and a wave a token, eight tokens a workgroup, a wave a slot."""
+    note(f"rows T={T} k={k} width={width}")
+    check_many_rows(*many_rows(T, k, width, torch.bfloat16, 0.1, T), "bfloat16")
+
+
+def test_route_beyond_one_launch():
+    """More rows than the 2^20 workgroups of a launch take: two experts, whose
+    softmax is a sigmoid of their difference (12 half steps: the difference,
+    which is below 16 and errs by half a step of that, two exponentials, sum,
+    quotient; the gradient as many again)."""
+    T = (1 << 24) + 21
+    note(f"route_topk T={T}")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    logits = torch.randn(T, 2, generator=gen, device="cuda")
+    w, e = rs.route_topk(logits, 1)
+    d = logits[:, 1].double() - logits[:, 0].double()
+    assert torch.equal(e[:, 0].bool(), d > 0)
+    p = torch.sigmoid(d.abs())
+    assert ((w[:, 0].double() - p).abs() <= 32 * eo.U32 * p).all()
+    g = torch.randn(T, 1, generator=gen, device="cuda")
+    grad = rs.route_topk_backward(logits, e, g)
+    want = torch.where(e[:, 0] == 1, 1.0, -1.0).double() * g[:, 0].double() * p * (1 - p)
+    # The chosen one's a - mean = g (1 - p) loses what cancels in 1 - p.
+    bound = 64 * eo.U32 * g[:, 0].double().abs()
+    assert ((grad[:, 1].double() - want).abs() <= bound).all() and ((grad[:, 0].double() + want).abs() <= bound).all()
