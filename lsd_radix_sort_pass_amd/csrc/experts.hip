@@ -319,12 +319,14 @@ bool launch_rows(rs::RowWork<T> w, hipStream_t stream) {
 // bfloat16, k = 8, with dots: 2048 x 128 9.1 / 9.1 / 11.3, 8192 x 128 12.7 / 14.0 /
 // 17.6, 32768 x 128 32 / 51 / 44, 32768 x 256 59 / 65 / 78, 8192 x 2048 91 / 91 / 126;
 // without: 3000 x 128 6.5 / 6.5 / 8.8, 8192 x 128 7 / 13 / 11, 32768 x 256 25 / 49 /
-// 44, 32768 x 512 51 / 69 / 87, 32768 x 1024 106 / 108 / 181.  More slots than 2^22
-// would not fit the groups' bits.
+// 44, 32768 x 512 51 / 69 / 87, 32768 x 1024 106 / 108 / 181; with dots for 1000 rows
+// of 512 among 500000 x 8 slots 349 / 614 / 369.  More slots than 2^22 would not fit
+// the groups' bits.
 constexpr size_t kClearGroups = 64;
 bool clear_beside(size_t slots, size_t num_rows, size_t row_bytes, bool dots) {
     if (num_rows > slots || slots > kClearGroups * rs::kClearRows) return false;
-    return slots <= (size_t{1} << 16) || row_bytes >= (dots ? 512 : 1024);
+    const size_t hides = (dots ? 512 : 1024) / (slots <= (size_t{1} << 16) ? 4 : 1);  // bytes of rows a slot
+    return slots <= (size_t{1} << 14) || num_rows * row_bytes >= slots * hides;
 }
 
 // Enqueues zeros in whole rows.

@@ -634,10 +634,10 @@ __global__ __launch_bounds__(kPlaceBlock) void expert_scan_kernel(uint32_t *__re
 // in lane order, a measured property, here among up to 1025 counters and with
 // lanes masked out, which the tests of this sort pin on the lane order test's
 // patterns.  match: ranked by ballots instead (match_rank), whatever that order;
-// 2^20 slots of 256 experts take 2.5 us more so, 8192 slots 4.3.  Dropped slots, often a long run of
-// padding, are ranked by a ballot instead of 64 adds to one address.
-// A tile's slots are put in key order in LDS, so that order is written in
-// runs (the sort of 2^20 slots of 256 experts takes 13.4 us so, 16.1 without).
+// 2^20 slots of 256 experts take 2.5 us more so, 8192 slots 4.3.  Dropped slots,
+// often a long run of padding, are ranked by a ballot instead of 64 adds to one
+// address.  A tile's slots are put in key order in LDS, so that order is written in runs
+// (the sort of 2^20 slots of 256 experts takes 13.4 us so, 16.1 without).
 // KEYS >= experts sizes the LDS.  Bound by the chain of round trips: ids and
 // table, LDS counts, scans, writes: 8.9 us for 2^20 slots of 128 experts (12 MiB).
 enum : int {

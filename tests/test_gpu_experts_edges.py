@@ -413,3 +413,40 @@ def test_route_beyond_one_launch():
     # The chosen one's a - mean = g (1 - p) loses what cancels in 1 - p.
     bound = 64 * eo.U32 * g[:, 0].double().abs()
     assert ((grad[:, 1].double() - want).abs() <= bound).all() and ((grad[:, 0].double() + want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("T,k,width,num_rows", [(50, 4, 600, 200), (9000, 8, 80, 72_000), (50, 4, 600, 333)])
+def test_gradient_of_unnamed_rows_in_a_graph(T, k, width, num_rows):
+    """Captured, replayed with other places and on another stream: the rows that
+    were named before and are not now get zeros again."""
+    note(f"combine_rows_backward in a graph T={T} k={k} width={width} rows={num_rows}")
+    g = torch.randn(T, width, device="cuda").bfloat16()
+    rows = torch.randn(num_rows, width, device="cuda").bfloat16()
+    w = torch.rand(T, k, device="cuda")
+    position = torch.empty(T, k, dtype=torch.int32, device="cuda")
+
+    def fill(seed):
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(seed)
+        p = torch.randperm(2 * num_rows, generator=gen, device="cuda")[:T * k].to(torch.int32)
+        position.copy_(torch.where(p % 5 == 0, ~p, p).reshape(T, k))
+    fill(0)
+    rs.combine_rows_backward(g, position, rows, w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        grad, grad_w = rs.combine_rows_backward(g, position, rows, w)
+    side = torch.cuda.Stream()
+    for seed in range(1, 5):
+        fill(seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = torch.zeros_like(rows)
+        s = torch.nonzero((position.reshape(-1) >= 0) & (position.reshape(-1) < num_rows))[:, 0]
+        want[position.reshape(-1)[s].long()] = (g[s // k].float() * w.reshape(-1)[s, None]).bfloat16()
+        eager = rs.combine_rows_backward(g, position, rows, w)
+        side.wait_stream(torch.cuda.current_stream())
+        beside = rs.combine_rows_backward(g, position, rows, w, stream=side)
+        torch.cuda.synchronize()
+        for a, b in ((grad, grad_w), eager, beside):
+            assert torch.equal(a, want) and torch.equal(b, eager[1])
