@@ -297,8 +297,9 @@ rs_status rs_sort_keys_u32_noalloc(const uint32_t *keys_in, uint32_t *keys_out, 
  * are computed in float32 and rounded once, to nearest even, where the result
  * is 16 bits wide; every sum has a fixed order, so results repeat bit for bit.
  * An output's address range, from its first row to its last, may not overlap
- * that of an input or another output.  The calls allocate nothing, only enqueue on `stream` (of the current device), keep no state
- * and can be captured into a graph.  Argument errors are reported before any
+ * that of an input or another output.  The calls allocate nothing, only
+ * enqueue on `stream` (of the current device), keep no state and can be
+ * captured into a graph.  Argument errors are reported before any
  * HIP call, as for the sorts: RS_ERROR_INVALID_VALUE for a NULL or misaligned
  * pointer, a size outside the stated limits, an unknown type or gate, or an
  * overlap. */

@@ -362,7 +362,8 @@ __device__ __forceinline__ bool choose_by_counts(const float (&x)[V], const T *r
 // in lane j.  counts: choose_by_counts is tried first (k <= G / 2).
 // Each logit is read once; a wave then spends some 390 vector instructions on
 // its 64 / G rows, which bounds it together with the one wait for the row.
-// 16384 x 256 float32, k = 8: 5.8 us (17.8 MB, 3.1 TB/s); in rounds alone 10.1.
+// 16384 x 256 float32, k = 8: 5.8 us (17.8 MB, 3.1 TB/s) with the rows in the
+// last-level cache, 7.3 from memory; in rounds alone 10.1.
 template <class T, int G, int V>
 __global__ __launch_bounds__(kRouteBlock) void route_topk_kernel(const T *__restrict__ logits, size_t tokens,
                                                                  int experts, size_t stride, int k, int gate,
@@ -432,8 +433,9 @@ __global__ __launch_bounds__(kRouteBlock) void route_topk_kernel(const T *__rest
 // exponential that underflows is +0 and follows the formula (a row with a NaN or
 // +inf, or a NaN gradient of a weight, has no finite gradient anywhere else).
 // Lane j < k of the group holds slot j; the slots' terms reach the lanes that
-// hold their elements through LDS.  Bound by memory: 32768 x 256 float32,
-// softmax, k = 8, 18.2 us (69 MB, 3.8 TB/s).
+// hold their elements through LDS.  32768 x 256 float32, softmax, k = 8: 16.1 us
+// (69 MB, 4.3 TB/s), not the memory's rate: the choices are loaded after the row
+// is summed, then the chosen logits, and two barriers tie four waves together.
 template <class T, int G, int V>
 __global__ __launch_bounds__(kRouteBlock) void route_topk_backward_kernel(
     const T *__restrict__ logits, size_t tokens, int experts, size_t stride, const int32_t *__restrict__ chosen,
@@ -965,8 +967,9 @@ __global__ __launch_bounds__(kRowBlock) void clear_rows_kernel(T *rows, size_t n
 // The last access of a row is moved back to end with it where the width is no
 // multiple of the access: its first elements are computed twice, to the same
 // result, and counted once in the products.
-// Bound by memory, which a plain copy moves at 4.9 - 5.4 TB/s: bfloat16 spread
-// 16384 x 8 x 4096 217 us (5.6 TB/s), join 206 us (5.9), spread with dots
+// Bound by memory, which a plain copy moves at 4.9 - 5.7 TB/s: bfloat16 spread
+// 16384 x 8 x 4096 217 us (5.6 TB/s), join 206 us (5.9, its output partly taken by
+// the last-level cache; 224 us, 5.4, where that holds none of it), spread with dots
 // 8192 x 8 x 2048 117 us (4.9), join with dots 60 us (5.6).  Row by row instead of
 // in batches the join took 262 us, dots in a pass of their own 144 in all.
 // a.once (ONCE without dots, where the branch would cost a small join 0.3 us of

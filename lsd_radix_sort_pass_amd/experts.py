@@ -25,7 +25,6 @@ caller's.
 from __future__ import annotations
 
 import contextlib
-import ctypes
 from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
