@@ -401,6 +401,87 @@ rs_status rs_combine_rows_backward_all(const void *grad_out, int dtype, size_t t
                                        const void *rows, size_t rows_stride, void *grad_rows, size_t grad_rows_stride,
                                        size_t num_rows, float *grad_weights, hipStream_t stream);
 
+/* The experts' own work: matrix products of rows that stand sorted by expert
+ * (rs_sort_experts, rs_dispatch_rows), in 16 and 32 bits or with 8-bit operands,
+ * their gradients, and the gated activation between two products.
+ *
+ * Expert e has the rows [offsets[e], offsets[e + 1]), e = 0 .. experts - 1 (offsets as
+ * rs_sort_experts writes them: ascending; values outside [0, num_rows] are
+ * taken as its ends).  offsets NULL: the one expert has all rows (experts = 1), a
+ * plain product.  Rows before offsets[0] and from offsets[experts] on belong to no
+ * expert: they are never read, and results for them are left as they were, or
+ * zeros if all != 0.
+ *
+ * Types, strides, rounding, overlap, streams and errors are as for the
+ * calls above; matrices are [experts][out_width][in_width] with consecutive
+ * elements in a row and strides between rows and between experts, in
+ * elements.  Products are summed in float32 in a fixed order (in blocks, by matrix
+ * instructions, which add the products of a block in an order of their own)
+ * and rounded once.  1 <= widths <= RS_MAX_ROW_WIDTH, experts <=
+ * RS_MAX_EXPERTS, num_rows <= RS_MAX_SLOTS. */
+
+/* out[r][n] = sum over k of weights[e][n][k] * rows[r][k], e the expert of row r. */
+rs_status rs_expert_products(const void *rows, int dtype, size_t num_rows, int in_width, size_t rows_stride,
+                             const int32_t *offsets, int experts, const void *weights, int out_width,
+                             size_t weights_stride, size_t weights_expert, void *out, size_t out_stride, int all,
+                             hipStream_t stream);
+
+/* Its gradients from that of out, each if its pointer is given (then what it reads
+ * is needed: weights for the one, rows for the other):
+ *   grad_rows[r][k]       = sum over n of grad[r][n] * weights[e][n][k]
+ *   grad_weights[e][n][k] = sum over the rows r of e of grad[r][n] * rows[r][k],
+ * the latter contiguous, zeros for an expert without rows. */
+rs_status rs_expert_products_backward(const void *grad, int dtype, size_t num_rows, int out_width, size_t grad_stride,
+                                      const int32_t *offsets, int experts, const void *weights, size_t weights_stride,
+                                      size_t weights_expert, const void *rows, size_t rows_stride, int in_width,
+                                      void *grad_rows, size_t grad_rows_stride, void *grad_weights, int all,
+                                      hipStream_t stream);
+
+/* The product of operands in 8 bits (e4m3: 4 exponent bits, 3 of the mantissa,
+ * largest value 448, no infinities), with a float32 scale for each block of
+ * RS_SCALE_BLOCK elements of a row and for each RS_SCALE_BLOCK x RS_SCALE_BLOCK of a
+ * matrix; with B = ceil(in_width / RS_SCALE_BLOCK):
+ *   out[r][n] = sum over b < B of row_scales[b][r] * weight_scales[e][n / RS_SCALE_BLOCK][b]
+ *               * sum over k of block b of rows[r][k] * weights[e][n][k],
+ * out in dtype.  row_scales [B][num_rows] and weight_scales
+ * [experts][ceil(out_width / RS_SCALE_BLOCK)][B] are contiguous. */
+#define RS_SCALE_BLOCK 128
+rs_status rs_expert_products_fp8(const uint8_t *rows, const float *row_scales, size_t num_rows, int in_width,
+                                 size_t rows_stride, const int32_t *offsets, int experts, const uint8_t *weights,
+                                 const float *weight_scales, int out_width, size_t weights_stride,
+                                 size_t weights_expert, void *out, int dtype, size_t out_stride, int all,
+                                 hipStream_t stream);
+
+/* Such operands: with m the largest size of the finite elements of a block, but at
+ * least 2^-100, its scale is m / 448 and its elements are e4m3(x * (448 / m)),
+ * to nearest even; NaN and infinities become NaN.  all: rows of no expert
+ * become zeros with the scale of such a block.  out of rs_quantize_weights is
+ * contiguous. */
+rs_status rs_quantize_rows(const void *rows, int dtype, size_t num_rows, int width, size_t rows_stride,
+                           const int32_t *offsets, int experts, uint8_t *out, size_t out_stride, float *scales, int all,
+                           hipStream_t stream);
+rs_status rs_quantize_weights(const void *weights, int dtype, int experts, int out_width, int in_width,
+                              size_t weights_stride, size_t weights_expert, uint8_t *out, float *scales,
+                              hipStream_t stream);
+
+/* Gated rows: a row holds a (width elements), then b, and out[r] = act(a) * b with
+ *   silu: act(x) = x / (1 + exp(-x)),   gelu: act(x) = x * (1 + erf(x / sqrt 2)) / 2.
+ * width <= RS_MAX_ROW_WIDTH / 2.  NaN and infinities give what the formulas
+ * give, or NaN.  The gradient is that of the whole row, from grad [num_rows][width]:
+ * da = grad * b * act'(a), then db = grad * act(a).  rs_gate_quantize_rows gives
+ * the gated rows as rs_quantize_rows does, from their values before they are
+ * rounded to dtype. */
+typedef enum rs_act { RS_ACT_SILU = 0, RS_ACT_GELU = 1 } rs_act;
+rs_status rs_gate_rows(const void *rows, int dtype, size_t num_rows, int width, size_t rows_stride,
+                       const int32_t *offsets, int experts, int act, void *out, size_t out_stride, int all,
+                       hipStream_t stream);
+rs_status rs_gate_rows_backward(const void *grad, size_t grad_stride, const void *rows, int dtype, size_t num_rows,
+                                int width, size_t rows_stride, const int32_t *offsets, int experts, int act,
+                                void *grad_rows, size_t grad_rows_stride, int all, hipStream_t stream);
+rs_status rs_gate_quantize_rows(const void *rows, int dtype, size_t num_rows, int width, size_t rows_stride,
+                                const int32_t *offsets, int experts, int act, uint8_t *out, size_t out_stride,
+                                float *scales, int all, hipStream_t stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char *rs_status_string(rs_status status);
 

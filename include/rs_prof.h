@@ -33,7 +33,10 @@ typedef enum rs_kernel_kind {
     RS_KERNEL_ROUTE = 6,  /* top-k routing and its gradient */
     RS_KERNEL_EXPERT = 7, /* slots sorted by expert (counting and placing launches) */
     RS_KERNEL_ROWS = 8,   /* rows dispatched or combined, and their gradients */
-    RS_KERNEL_KINDS = 9
+    RS_KERNEL_PRODUCT = 9,   /* products of sorted rows and experts' weights, and their gradients */
+    RS_KERNEL_GATE = 10,     /* gated rows and their gradient */
+    RS_KERNEL_QUANTIZE = 11, /* rows and weights to 8 bits */
+    RS_KERNEL_KINDS = 12
 } rs_kernel_kind;
 
 /* Turn per-kernel event timing on (non-zero) or off: while on, every kernel

@@ -26,6 +26,8 @@ import torch
 from . import _lib
 from .experts import (MAX_CHOICES, MAX_EXPERTS, ExpertOrder, combine_rows, combine_rows_backward, dispatch_rows,
                       dispatch_rows_backward, route_topk, route_topk_backward, sort_experts, temp_bytes_experts)
+from .products import (SCALE_BLOCK, Quantized, expert_products, expert_products_backward, expert_products_fp8,
+                       gate_quantize_rows, gate_rows, gate_rows_backward, quantize_rows, quantize_weights)
 
 __all__ = [
     "RadixSortError", "key_bits", "temp_bytes", "temp_bytes_morton30", "sort_morton30", "alloc_temp", "sort_keys", "sort_pairs",
@@ -34,6 +36,8 @@ __all__ = [
     "NOALLOC_MAX_KEYS", "DeviceGuardError", "prof_samples", "prof_force_giveup", "lds_rank_probe", "prof_ranker",
     "MAX_CHOICES", "MAX_EXPERTS", "ExpertOrder", "route_topk", "route_topk_backward", "temp_bytes_experts",
     "sort_experts", "dispatch_rows", "dispatch_rows_backward", "combine_rows", "combine_rows_backward",
+    "SCALE_BLOCK", "Quantized", "expert_products", "expert_products_backward", "expert_products_fp8", "gate_quantize_rows",
+    "gate_rows", "gate_rows_backward", "quantize_rows", "quantize_weights",
 ]
 
 TEMP_ALIGN = 256

@@ -23,7 +23,10 @@ RS_KERNEL_SMALL = 5
 RS_KERNEL_ROUTE = 6
 RS_KERNEL_EXPERT = 7
 RS_KERNEL_ROWS = 8
-RS_KERNEL_KINDS = 9
+RS_KERNEL_PRODUCT = 9
+RS_KERNEL_GATE = 10
+RS_KERNEL_QUANTIZE = 11
+RS_KERNEL_KINDS = 12
 
 # Every function the two public headers declare, with its ctypes signature.
 _VP = ctypes.c_void_p
@@ -75,6 +78,15 @@ SIGNATURES = {
     "rs_combine_rows": (_I, [_VP, _I, _SZ, _SZ, _VP, _VP, _I, _VP, _SZ, _I, _SZ, _VP]),
     "rs_combine_rows_backward": (_I, [_VP, _I, _SZ, _I, _SZ, _VP, _VP, _I, _VP, _SZ, _VP, _SZ, _SZ, _VP, _VP]),
     "rs_combine_rows_backward_all": (_I, [_VP, _I, _SZ, _I, _SZ, _VP, _VP, _I, _VP, _SZ, _VP, _SZ, _SZ, _VP, _VP]),
+    "rs_expert_products": (_I, [_VP, _I, _SZ, _I, _SZ, _VP, _I, _VP, _I, _SZ, _SZ, _VP, _SZ, _I, _VP]),
+    "rs_expert_products_backward": (_I, [_VP, _I, _SZ, _I, _SZ, _VP, _I, _VP, _SZ, _SZ, _VP, _SZ, _I, _VP, _SZ, _VP, _I,
+                                         _VP]),
+    "rs_expert_products_fp8": (_I, [_VP, _VP, _SZ, _I, _SZ, _VP, _I, _VP, _VP, _I, _SZ, _SZ, _VP, _I, _SZ, _I, _VP]),
+    "rs_quantize_rows": (_I, [_VP, _I, _SZ, _I, _SZ, _VP, _I, _VP, _SZ, _VP, _I, _VP]),
+    "rs_quantize_weights": (_I, [_VP, _I, _I, _I, _I, _SZ, _SZ, _VP, _VP, _VP]),
+    "rs_gate_rows": (_I, [_VP, _I, _SZ, _I, _SZ, _VP, _I, _I, _VP, _SZ, _I, _VP]),
+    "rs_gate_rows_backward": (_I, [_VP, _SZ, _VP, _I, _SZ, _I, _SZ, _VP, _I, _I, _VP, _SZ, _I, _VP]),
+    "rs_gate_quantize_rows": (_I, [_VP, _I, _SZ, _I, _SZ, _VP, _I, _I, _VP, _SZ, _VP, _I, _VP]),
     "rs_status_string": (ctypes.c_char_p, [_I]),
     "rs_prof_enable": (_I, [_I]),
     "rs_prof_reset": (None, []),

@@ -10,13 +10,14 @@ import argparse
 import os
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "librs.so")
-SOURCES = [os.path.join(CSRC, "librs.hip")]
+SOURCES = [os.path.join(CSRC, "librs.hip"), os.path.join(CSRC, "products.hip")]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -24,7 +25,6 @@ HIPCC_FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-Wall",
     # Packed FP32 instructions are kept out of every code object.
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -39,17 +39,30 @@ def hipcc() -> str:
 
 
 def build(save_temps: str | None = None, verbose: bool = False) -> str:
-    out_tmp = LIB + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-o", out_tmp, *SOURCES]
-    cwd = PKG
-    if save_temps:
-        os.makedirs(save_temps, exist_ok=True)
-        cmd.insert(1, "-save-temps")
-        cwd = save_temps
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True, cwd=cwd)
-    os.replace(out_tmp, LIB)
+    """Compiles the sources side by side, each to an object, and links them."""
+    with tempfile.TemporaryDirectory() as objects:
+        cwd = PKG
+        if save_temps:
+            os.makedirs(save_temps, exist_ok=True)
+            cwd = save_temps
+        running, outputs = [], []
+        for source in SOURCES:
+            out = os.path.join(objects, os.path.basename(source) + ".o")
+            cmd = [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", source, "-o", out]
+            if save_temps:
+                cmd.insert(1, "-save-temps")
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            running.append((cmd, subprocess.Popen(cmd, cwd=cwd)))
+            outputs.append(out)
+        failed = [(cmd, p.returncode) for cmd, p in running if p.wait() != 0]
+        if failed:
+            raise subprocess.CalledProcessError(failed[0][1], failed[0][0])
+        link = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", LIB + ".tmp", *outputs]
+        if verbose:
+            print(" ".join(link), flush=True)
+        subprocess.run(link, check=True, cwd=cwd)
+    os.replace(LIB + ".tmp", LIB)
     return LIB
 
 

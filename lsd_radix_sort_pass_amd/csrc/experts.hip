@@ -4,55 +4,13 @@
 #include <algorithm>
 
 #include "experts.hpp"
+#include "launch.hpp"
 
 namespace {
-
-constexpr unsigned kMaxGrid = 1u << 20;  // workgroups; the kernels stride over the rest
-
-int dtype_bytes(int dtype) {
-    switch (dtype) {
-        case RS_F32: return 4;
-        case RS_F16:
-        case RS_BF16: return 2;
-        default: return 0;
-    }
-}
-
-bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-// Bytes that `count` rows of `width` elements span.
-size_t span_bytes(size_t count, size_t width, size_t stride, size_t elem) {
-    return count == 0 ? 0 : ((count - 1) * stride + width) * elem;
-}
-
-// A present, aligned array; or any pointer for an empty one.
-bool good(const void *p, size_t count, size_t align) { return count == 0 || (p != nullptr && aligned(p, align)); }
-
-constexpr size_t kMaxStride = size_t{1} << 40;
-
-// Whether the rows of an array are addressable and, for an output, disjoint.
-bool good_rows(const void *p, size_t count, int width, size_t stride, size_t elem, bool output) {
-    if (!good(p, count, elem)) return false;
-    if (count <= 1) return true;
-    if (stride > kMaxStride || (count - 1) > (size_t{1} << 62) / ((stride + 1) * elem)) return false;
-    return !output || stride >= static_cast<size_t>(width);
-}
-
-bool disjoint(const Span *spans, int outputs, int all) {
-    for (int o = 0; o < outputs; ++o) {
-        for (int i = o + 1; i < all; ++i) {
-            if (spans[o].lo != spans[o].hi && spans[i].lo != spans[i].hi && overlap(spans[o], spans[i])) return false;
-        }
-    }
-    return true;
-}
 
 // ---------------------------------------------------------------------------
 // Routing
 // ---------------------------------------------------------------------------
-template <int N>
-using IntC = std::integral_constant<int, N>;
-
 // Calls f(first row, rows, workgroups) for launches that cover `tokens` rows
 // of `lanes` threads each: one, until the threads of a launch reach 2^28.
 template <class F>
@@ -75,15 +33,6 @@ bool with_values(int per_lane, F &&f) {
     if (per_lane <= 4) return f(IntC<4>{});
     if (per_lane <= 8) return f(IntC<8>{});
     return f(IntC<16>{});
-}
-
-template <class F>
-bool with_dtype(int dtype, F &&f) {
-    switch (dtype) {
-        case RS_F32: return f(float{});
-        case RS_F16: return f(rs::f16{});
-        default: return f(rs::bf16{});
-    }
 }
 
 // Whether k choices among rows of `values` logits in each of `lanes` lanes are

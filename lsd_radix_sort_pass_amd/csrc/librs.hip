@@ -1,6 +1,5 @@
-// librs.hip -- the library's translation unit: the sorts, and the
-// mixture-of-experts calls, which use the sorts' launch, timing and argument
-// helpers.
+// librs.hip -- the sorts, and the mixture-of-experts calls around them, which use
+// the sorts' launch and argument helpers.
 #include "rs.hip"
 
 #include "experts.hip"

@@ -1,0 +1,330 @@
+// products.hip -- C ABI of the experts' own work (matrix products of sorted
+// rows, rows in 8 bits, gated rows): argument checks and launches.
+#include <algorithm>
+
+#include "gates.hpp"
+#include "launch.hpp"
+#include "products.hpp"
+
+namespace {
+
+constexpr int kMaxWidth = RS_MAX_ROW_WIDTH;
+constexpr size_t kMaxExpertStride = size_t{1} << 50;
+
+bool good_groups(const int32_t *offsets, int experts, size_t num_rows) {
+    if (experts < 1 || experts > RS_MAX_EXPERTS || num_rows > RS_MAX_SLOTS) return false;
+    return offsets == nullptr ? experts == 1 : aligned(offsets, 4);
+}
+
+Span span_offsets(const int32_t *offsets, int experts) {
+    return span_of(offsets, offsets ? 4 * (static_cast<size_t>(experts) + 1) : 0);
+}
+
+// Matrices [experts][rows][width], read.
+struct Matrices {
+    const void *p;
+    int experts, rows, width;
+    size_t stride, expert, elem;
+
+    bool good() const {
+        return ::good(p, 1, elem) && rows >= 1 && rows <= kMaxWidth && width >= 1 && width <= kMaxWidth &&
+               stride <= kMaxStride && expert <= kMaxExpertStride;
+    }
+    Span span() const {
+        const size_t last = static_cast<size_t>(experts - 1) * expert + static_cast<size_t>(rows - 1) * stride;
+        return span_of(p, (last + static_cast<size_t>(width)) * elem);
+    }
+};
+
+size_t scale_blocks(int width) { return (static_cast<size_t>(width) + rs::kScaleBlock - 1) / rs::kScaleBlock; }
+
+bool addressable(Span s) { return s.lo <= s.hi && s.hi - s.lo < (size_t{1} << 62); }
+
+// Enqueues the product of w, whose results are q by p (RAGGED_C: of each expert).
+template <class T, class OUT, bool RAGGED_C, bool Q_ACROSS, bool P_ACROSS>
+bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
+    const size_t p_tiles = (static_cast<size_t>(w.pn) + 127) / 128;
+    size_t q_tiles;
+    if (RAGGED_C) {
+        q_tiles = (static_cast<size_t>(w.qn) + 127) / 128 * static_cast<size_t>(w.experts);
+    } else {
+        // Each expert's last tile may be a part, and so may that of the rows of none.
+        q_tiles = w.num_rows / 128 + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1;
+    }
+    const size_t jobs = q_tiles * p_tiles;
+    const unsigned grid = static_cast<unsigned>(std::min<size_t>(jobs, size_t{1} << 24));
+    return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] {
+        run_kernel(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS>, grid, 256, stream, w);
+    });
+}
+
+rs::Divider divider(size_t by) {
+    unsigned up = 0;
+    while ((size_t{1} << up) < by) ++up;
+    return {static_cast<uint32_t>(((uint64_t{1} << (31 + up)) + by - 1) / by), 31 + up};
+}
+
+template <class F>
+bool with_act(int act, F &&f) {
+    return act == RS_ACT_GELU ? f(IntC<rs::kActGelu>{}) : f(IntC<rs::kActSilu>{});
+}
+
+bool good_gate(int dtype, int act, int width) {
+    return dtype_bytes(dtype) != 0 && (act == RS_ACT_SILU || act == RS_ACT_GELU) && width >= 1 && width <= kMaxWidth / 2;
+}
+
+// Enqueues h = act(a) b of rows, or its gradient if grad is given.
+rs_status gate_rows(const void *grad, size_t grad_stride, const void *rows, int dtype, size_t num_rows, int width,
+                    size_t rows_stride, const int32_t *offsets, int experts, int act, void *out, size_t out_stride,
+                    int all, bool backward, hipStream_t stream) {
+    if (!good_gate(dtype, act, width) || !good_groups(offsets, experts, num_rows)) return RS_ERROR_INVALID_VALUE;
+    const size_t elem = static_cast<size_t>(dtype_bytes(dtype));
+    const int out_width = backward ? 2 * width : width;
+    if (!good_rows(rows, num_rows, 2 * width, rows_stride, elem, false) ||
+        !good_rows(out, num_rows, out_width, out_stride, elem, true) ||
+        (backward && !good_rows(grad, num_rows, width, grad_stride, elem, false))) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    const auto wide = static_cast<size_t>(width);
+    const Span spans[] = {span_of(out, span_bytes(num_rows, static_cast<size_t>(out_width), out_stride, elem)),
+                          span_of(rows, span_bytes(num_rows, 2 * wide, rows_stride, elem)),
+                          span_of(grad, backward ? span_bytes(num_rows, wide, grad_stride, elem) : 0),
+                          span_offsets(offsets, experts)};
+    if (!disjoint(spans, 1, 4)) return RS_ERROR_INVALID_VALUE;
+    if (num_rows == 0) return RS_SUCCESS;
+    rs::GateWork w{};
+    w.rows = rows, w.grad = grad, w.out = out;
+    w.rows_stride = rows_stride, w.grad_stride = grad_stride, w.out_stride = out_stride;
+    w.offsets = offsets, w.experts = experts, w.num_rows = num_rows, w.width = width, w.clear = all != 0;
+    const bool ok = with_dtype(dtype, [&](auto zero) {
+        using T = decltype(zero);
+        return with_act(act, [&](auto a) {
+            constexpr int kAct = decltype(a)::value;
+            const auto go = [&](auto kernel, int v) {
+                w.chunks = (width + v - 1) / v;
+                const size_t units = num_rows * static_cast<size_t>(w.chunks);
+                const unsigned grid = grid_for(units, rs::kGateBlock, kMaxGrid);
+                return launch_kernel(RS_KERNEL_GATE, stream, [&] {
+                    run_kernel(kernel, grid, rs::kGateBlock, stream, w, divider(static_cast<size_t>(w.chunks)));
+                });
+            };
+            constexpr int V = rs::kVec<T>;
+            if (width < V) {
+                return backward ? go(rs::gate_kernel<T, 1, kAct, true>, 1) : go(rs::gate_kernel<T, 1, kAct, false>, 1);
+            }
+            return backward ? go(rs::gate_kernel<T, V, kAct, true>, V) : go(rs::gate_kernel<T, V, kAct, false>, V);
+        });
+    });
+    return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
+}
+
+// Enqueues rows (gate: act(a) b of them) in 8 bits with their scales.
+rs_status quantize_rows(const void *rows, int dtype, size_t num_rows, int width, size_t rows_stride,
+                        const int32_t *offsets, int experts, bool gate, int act, uint8_t *out, size_t out_stride,
+                        float *scales, int all, hipStream_t stream) {
+    if (gate ? !good_gate(dtype, act, width) : dtype_bytes(dtype) == 0 || width < 1 || width > kMaxWidth) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    if (!good_groups(offsets, experts, num_rows)) return RS_ERROR_INVALID_VALUE;
+    const size_t elem = static_cast<size_t>(dtype_bytes(dtype)), blocks = scale_blocks(width);
+    const int in_width = gate ? 2 * width : width;
+    if (!good_rows(rows, num_rows, in_width, rows_stride, elem, false) ||
+        !good_rows(out, num_rows, width, out_stride, 1, true) || !good(scales, num_rows, 4)) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    const Span spans[] = {span_of(out, span_bytes(num_rows, static_cast<size_t>(width), out_stride, 1)),
+                          span_of(scales, num_rows * blocks * 4),
+                          span_of(rows, span_bytes(num_rows, static_cast<size_t>(in_width), rows_stride, elem)),
+                          span_offsets(offsets, experts)};
+    if (!disjoint(spans, 2, 4)) return RS_ERROR_INVALID_VALUE;
+    if (num_rows == 0) return RS_SUCCESS;
+    rs::GateWork w{};
+    w.rows = rows, w.out = out, w.scales = scales, w.rows_stride = rows_stride, w.out_stride = out_stride;
+    w.offsets = offsets, w.experts = experts, w.num_rows = num_rows, w.width = width, w.clear = all != 0;
+    const auto across = static_cast<unsigned>((blocks + rs::kQuantizeBlocks - 1) / rs::kQuantizeBlocks);
+    const dim3 grid(across, static_cast<unsigned>(std::min<size_t>((num_rows + 15) / 16, 65535)));
+    const bool ok = with_dtype(dtype, [&](auto zero) {
+        using T = decltype(zero);
+        const auto go = [&](auto kernel) {
+            return launch_kernel(RS_KERNEL_QUANTIZE, stream,
+                                 [&] { run_kernel(kernel, grid, rs::kGateBlock, stream, w); });
+        };
+        const bool whole = width % 8 == 0;
+        if (!gate) {
+            return whole ? go(rs::quantize_rows_kernel<T, 0, false, true>) : go(rs::quantize_rows_kernel<T, 0, false, false>);
+        }
+        return with_act(act, [&](auto a) {
+            constexpr int kAct = decltype(a)::value;
+            return whole ? go(rs::quantize_rows_kernel<T, kAct, true, true>)
+                         : go(rs::quantize_rows_kernel<T, kAct, true, false>);
+        });
+    });
+    return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
+}
+
+}  // namespace
+
+extern "C" {
+
+rs_status rs_expert_products(const void *rows, int dtype, size_t num_rows, int in_width, size_t rows_stride,
+                             const int32_t *offsets, int experts, const void *weights, int out_width,
+                             size_t weights_stride, size_t weights_expert, void *out, size_t out_stride, int all,
+                             hipStream_t stream) {
+    const size_t elem = static_cast<size_t>(dtype_bytes(dtype));
+    if (elem == 0 || !good_groups(offsets, experts, num_rows)) return RS_ERROR_INVALID_VALUE;
+    const Matrices m{weights, experts, out_width, in_width, weights_stride, weights_expert, elem};
+    if (!m.good() || !good_rows(rows, num_rows, in_width, rows_stride, elem, false) ||
+        !good_rows(out, num_rows, out_width, out_stride, elem, true)) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    const Span spans[] = {span_of(out, span_bytes(num_rows, static_cast<size_t>(out_width), out_stride, elem)),
+                          span_of(rows, span_bytes(num_rows, static_cast<size_t>(in_width), rows_stride, elem)), m.span(),
+                          span_offsets(offsets, experts)};
+    if (!addressable(spans[2]) || !disjoint(spans, 1, 4)) return RS_ERROR_INVALID_VALUE;
+    if (num_rows == 0) return RS_SUCCESS;
+    const bool ok = with_dtype(dtype, [&](auto zero) {
+        using T = decltype(zero);
+        rs::ProductWork<T, T> w{};
+        w.q = static_cast<const T *>(rows), w.q_stride = rows_stride;
+        w.p = static_cast<const T *>(weights), w.p_stride = weights_stride, w.p_expert = weights_expert;
+        w.out = static_cast<T *>(out), w.out_stride = out_stride;
+        w.offsets = offsets, w.experts = experts, w.num_rows = num_rows;
+        w.pn = out_width, w.cn = in_width, w.clear = all != 0;
+        return launch_product<T, T, false, false, false>(w, stream);
+    });
+    return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
+}
+
+rs_status rs_expert_products_backward(const void *grad, int dtype, size_t num_rows, int out_width, size_t grad_stride,
+                                      const int32_t *offsets, int experts, const void *weights, size_t weights_stride,
+                                      size_t weights_expert, const void *rows, size_t rows_stride, int in_width,
+                                      void *grad_rows, size_t grad_rows_stride, void *grad_weights, int all,
+                                      hipStream_t stream) {
+    const size_t elem = static_cast<size_t>(dtype_bytes(dtype));
+    if (elem == 0 || !good_groups(offsets, experts, num_rows)) return RS_ERROR_INVALID_VALUE;
+    const auto wide_in = static_cast<size_t>(in_width), wide_out = static_cast<size_t>(out_width);
+    if (in_width < 1 || in_width > kMaxWidth || out_width < 1 || out_width > kMaxWidth ||
+        !good_rows(grad, num_rows, out_width, grad_stride, elem, false)) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    const bool to_rows = grad_rows != nullptr, to_weights = grad_weights != nullptr;
+    const Matrices m{weights, experts, out_width, in_width, weights_stride, weights_expert, elem};
+    if (to_rows && (!m.good() || !good_rows(grad_rows, num_rows, in_width, grad_rows_stride, elem, true))) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    if (to_weights && (!aligned(grad_weights, elem) || !good_rows(rows, num_rows, in_width, rows_stride, elem, false))) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    const size_t matrix = wide_in * wide_out;
+    const Span spans[] = {span_of(grad_rows, to_rows ? span_bytes(num_rows, wide_in, grad_rows_stride, elem) : 0),
+                          span_of(grad_weights, to_weights ? static_cast<size_t>(experts) * matrix * elem : 0),
+                          span_of(grad, span_bytes(num_rows, wide_out, grad_stride, elem)),
+                          to_rows ? m.span() : span_of(weights, 0),
+                          span_of(rows, to_weights ? span_bytes(num_rows, wide_in, rows_stride, elem) : 0),
+                          span_offsets(offsets, experts)};
+    if (!addressable(spans[1]) || !addressable(spans[3]) || !disjoint(spans, 2, 6)) return RS_ERROR_INVALID_VALUE;
+    const bool ok = with_dtype(dtype, [&](auto zero) {
+        using T = decltype(zero);
+        rs::ProductWork<T, T> w{};
+        w.q = static_cast<const T *>(grad), w.q_stride = grad_stride;
+        w.offsets = offsets, w.experts = experts, w.num_rows = num_rows, w.pn = in_width;
+        if (to_rows && num_rows != 0) {
+            w.p = static_cast<const T *>(weights), w.p_stride = weights_stride, w.p_expert = weights_expert;
+            w.out = static_cast<T *>(grad_rows), w.out_stride = grad_rows_stride;
+            w.cn = out_width, w.clear = all != 0;
+            if (!launch_product<T, T, false, false, true>(w, stream)) return false;
+        }
+        if (!to_weights) return true;
+        w.p = static_cast<const T *>(rows), w.p_stride = rows_stride, w.p_expert = 0;
+        w.out = static_cast<T *>(grad_weights), w.out_stride = wide_in, w.out_expert = matrix;
+        w.qn = out_width, w.cn = 0;
+        return launch_product<T, T, true, true, true>(w, stream);
+    });
+    return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
+}
+
+rs_status rs_expert_products_fp8(const uint8_t *rows, const float *row_scales, size_t num_rows, int in_width,
+                                 size_t rows_stride, const int32_t *offsets, int experts, const uint8_t *weights,
+                                 const float *weight_scales, int out_width, size_t weights_stride,
+                                 size_t weights_expert, void *out, int dtype, size_t out_stride, int all,
+                                 hipStream_t stream) {
+    const size_t elem = static_cast<size_t>(dtype_bytes(dtype));
+    if (elem == 0 || !good_groups(offsets, experts, num_rows)) return RS_ERROR_INVALID_VALUE;
+    const Matrices m{weights, experts, out_width, in_width, weights_stride, weights_expert, 1};
+    if (!m.good() || !good_rows(rows, num_rows, in_width, rows_stride, 1, false) || !good(row_scales, num_rows, 4) ||
+        !good(weight_scales, 1, 4) || !good_rows(out, num_rows, out_width, out_stride, elem, true)) {
+        return RS_ERROR_INVALID_VALUE;
+    }
+    const size_t blocks = scale_blocks(in_width), out_blocks = scale_blocks(out_width);
+    const Span spans[] = {span_of(out, span_bytes(num_rows, static_cast<size_t>(out_width), out_stride, elem)),
+                          span_of(rows, span_bytes(num_rows, static_cast<size_t>(in_width), rows_stride, 1)), m.span(),
+                          span_of(row_scales, num_rows * blocks * 4),
+                          span_of(weight_scales, static_cast<size_t>(experts) * blocks * out_blocks * 4),
+                          span_offsets(offsets, experts)};
+    if (!addressable(spans[2]) || !disjoint(spans, 1, 6)) return RS_ERROR_INVALID_VALUE;
+    if (num_rows == 0) return RS_SUCCESS;
+    const bool ok = with_dtype(dtype, [&](auto zero) {
+        using OUT = decltype(zero);
+        rs::ProductWork<rs::fp8, OUT> w{};
+        w.q = reinterpret_cast<const rs::fp8 *>(rows), w.q_stride = rows_stride, w.q_scales = row_scales;
+        w.p = reinterpret_cast<const rs::fp8 *>(weights), w.p_stride = weights_stride, w.p_expert = weights_expert;
+        w.p_scales = weight_scales;
+        w.out = static_cast<OUT *>(out), w.out_stride = out_stride;
+        w.offsets = offsets, w.experts = experts, w.num_rows = num_rows;
+        w.pn = out_width, w.cn = in_width, w.clear = all != 0;
+        return launch_product<rs::fp8, OUT, false, false, false>(w, stream);
+    });
+    return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
+}
+
+rs_status rs_quantize_rows(const void *rows, int dtype, size_t num_rows, int width, size_t rows_stride,
+                           const int32_t *offsets, int experts, uint8_t *out, size_t out_stride, float *scales, int all,
+                           hipStream_t stream) {
+    return quantize_rows(rows, dtype, num_rows, width, rows_stride, offsets, experts, false, RS_ACT_SILU, out, out_stride,
+                         scales, all, stream);
+}
+
+rs_status rs_quantize_weights(const void *weights, int dtype, int experts, int out_width, int in_width,
+                              size_t weights_stride, size_t weights_expert, uint8_t *out, float *scales,
+                              hipStream_t stream) {
+    const size_t elem = static_cast<size_t>(dtype_bytes(dtype));
+    if (elem == 0 || experts < 1 || experts > RS_MAX_EXPERTS) return RS_ERROR_INVALID_VALUE;
+    const Matrices m{weights, experts, out_width, in_width, weights_stride, weights_expert, elem};
+    if (!m.good() || !good(out, 1, 1) || !good(scales, 1, 4)) return RS_ERROR_INVALID_VALUE;
+    const size_t e = static_cast<size_t>(experts);
+    const size_t blocks = e * scale_blocks(out_width) * scale_blocks(in_width);
+    const Span spans[] = {span_of(out, e * static_cast<size_t>(out_width) * static_cast<size_t>(in_width)),
+                          span_of(scales, blocks * 4), m.span()};
+    if (!addressable(spans[0]) || !addressable(spans[2]) || !disjoint(spans, 2, 3)) return RS_ERROR_INVALID_VALUE;
+    const rs::QuantizeWeightsWork w{weights, out, scales, weights_stride, weights_expert, experts, out_width, in_width};
+    const unsigned grid = static_cast<unsigned>(std::min<size_t>(blocks, kMaxGrid));
+    const bool ok = with_dtype(dtype, [&](auto zero) {
+        return launch_kernel(RS_KERNEL_QUANTIZE, stream, [&] {
+            run_kernel(rs::quantize_weights_kernel<decltype(zero)>, grid, rs::kGateBlock, stream, w);
+        });
+    });
+    return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
+}
+
+rs_status rs_gate_rows(const void *rows, int dtype, size_t num_rows, int width, size_t rows_stride,
+                       const int32_t *offsets, int experts, int act, void *out, size_t out_stride, int all,
+                       hipStream_t stream) {
+    return gate_rows(nullptr, 0, rows, dtype, num_rows, width, rows_stride, offsets, experts, act, out, out_stride, all,
+                     false, stream);
+}
+
+rs_status rs_gate_rows_backward(const void *grad, size_t grad_stride, const void *rows, int dtype, size_t num_rows,
+                                int width, size_t rows_stride, const int32_t *offsets, int experts, int act,
+                                void *grad_rows, size_t grad_rows_stride, int all, hipStream_t stream) {
+    return gate_rows(grad, grad_stride, rows, dtype, num_rows, width, rows_stride, offsets, experts, act, grad_rows,
+                     grad_rows_stride, all, true, stream);
+}
+
+rs_status rs_gate_quantize_rows(const void *rows, int dtype, size_t num_rows, int width, size_t rows_stride,
+                                const int32_t *offsets, int experts, int act, uint8_t *out, size_t out_stride,
+                                float *scales, int all, hipStream_t stream) {
+    return quantize_rows(rows, dtype, num_rows, width, rows_stride, offsets, experts, true, act, out, out_stride, scales,
+                         all, stream);
+}
+
+}  // extern "C"
