@@ -5,6 +5,17 @@
 #include "gates.hpp"
 #include "launch.hpp"
 #include "products.hpp"
+#include "products_wide.hpp"
+
+// Named here, as the host's pass does not emit all of those that only calls within
+// generic lambdas name.
+#define RS_WIDE(T)                                                                                          \
+    template __global__ void rs::wide_product_kernel<T, false, false, false>(const rs::ProductWork<T, T>); \
+    template __global__ void rs::wide_product_kernel<T, false, false, true>(const rs::ProductWork<T, T>);  \
+    template __global__ void rs::wide_product_kernel<T, true, true, true>(const rs::ProductWork<T, T>);
+RS_WIDE(rs::f16)
+RS_WIDE(rs::bf16)
+#undef RS_WIDE
 
 namespace {
 
@@ -40,9 +51,38 @@ size_t scale_blocks(int width) { return (static_cast<size_t>(width) + rs::kScale
 
 bool addressable(Span s) { return s.lo <= s.hi && s.hi - s.lo < (size_t{1} << 62); }
 
+size_t align_to(size_t x, size_t by) { return (x + by - 1) / by * by; }
+
+template <class T, class OUT>
+bool wide_pays(const rs::ProductWork<T, OUT> &w, bool ragged_c) {
+    const size_t rows = w.num_rows / static_cast<size_t>(w.experts);
+    return rows >= 96 && w.pn > 128 && (!ragged_c || w.qn > 128);
+}
+
+// Whether the wide kernel can take an operand: its 16-byte chunks are aligned, a
+// tile spans less than 2^31 bytes, and a row has a chunk (across: whole ones).
+bool feeds(const void *p, size_t stride, size_t expert, int width, bool across, size_t elem) {
+    const size_t chunk = 16 / elem;
+    return aligned(p, 16) && stride % chunk == 0 && expert % chunk == 0 && stride <= (size_t{1} << 22) &&
+           width >= static_cast<int>(chunk) && (!across || static_cast<size_t>(width) % chunk == 0);
+}
+
 // Enqueues the product of w, whose results are q by p (RAGGED_C: of each expert).
 template <class T, class OUT, bool RAGGED_C, bool Q_ACROSS, bool P_ACROSS>
 bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
+    if constexpr (sizeof(T) == 2) {
+        const size_t p_tiles = (static_cast<size_t>(w.pn) + rs::kWide - 1) / rs::kWide;
+        const size_t tiles = RAGGED_C
+            ? align_to((static_cast<size_t>(w.qn) + rs::kWide - 1) / rs::kWide * p_tiles, rs::kXcds) * static_cast<size_t>(w.experts)
+            : align_to((w.num_rows / rs::kWide + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1) * p_tiles, rs::kXcds);
+        if (tiles <= (size_t{1} << 30) && feeds(w.q, w.q_stride, 0, Q_ACROSS ? w.qn : w.cn, Q_ACROSS, 2) &&
+            feeds(w.p, w.p_stride, w.p_expert, P_ACROSS ? w.pn : w.cn, P_ACROSS, 2) && wide_pays(w, RAGGED_C)) {
+            return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] {
+                run_kernel(rs::wide_product_kernel<T, RAGGED_C, Q_ACROSS, P_ACROSS>, static_cast<unsigned>(tiles),
+                           rs::kWideThreads, stream, w);
+            });
+        }
+    }
     const size_t p_tiles = (static_cast<size_t>(w.pn) + 127) / 128;
     size_t q_tiles;
     if (RAGGED_C) {

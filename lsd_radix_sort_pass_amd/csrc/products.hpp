@@ -108,10 +108,11 @@ __device__ inline RowTile find_tile(const int32_t *offsets, int experts, int num
         const RowSpan r = rows_of(offsets, e, num_rows);
         const int tiles = base + lane < experts ? tiles_of(r.hi - r.lo, height) : 0;
         const int upto = wave_prefix(tiles, lane);
-        const int all = __shfl(upto, 63);
+        const int all = __builtin_amdgcn_readlane(upto, 63);
         if (t < all) {
             const int at = __ffsll(static_cast<unsigned long long>(__ballot(upto > t))) - 1;
-            return {base + at, t - (__shfl(upto, at) - __shfl(tiles, at)), {__shfl(r.lo, at), __shfl(r.hi, at)}};
+            return {base + at, t - __builtin_amdgcn_readlane(upto - tiles, at),
+                    {__builtin_amdgcn_readlane(r.lo, at), __builtin_amdgcn_readlane(r.hi, at)}};
         }
         t -= all;
     }
@@ -157,8 +158,8 @@ __device__ __forceinline__ f32x4 mma16_fp8(i32x4 p0, i32x4 p1, i32x4 q0, i32x4 q
 // ---------------------------------------------------------------------------
 // A tile holds 128 bytes of c for each of 128 rows (along), or the elements of
 // 128 columns for as many steps of c as fill 16 KiB (across).  Its 16-byte
-// chunks (along) and 32-byte units (across) are exchanged so that the lanes of a
-// read spread over all banks.
+// chunks (along) and 32-byte units (across) are exchanged so that the 16 or 32 lanes
+// that LDS serves at once (256 bytes, all 64 banks) meet every bank once.
 constexpr int kTileBytes = 16384;
 
 template <class T>
@@ -168,7 +169,7 @@ constexpr int kStep = 128 / static_cast<int>(sizeof(T));  // elements of c in a 
 template <class T, bool ACROSS>
 __device__ __forceinline__ int tile_at(int row, int chunk) {
     if constexpr (!ACROSS) {
-        return row * 128 + ((chunk ^ (row & 7)) << 4);
+        return row * 128 + ((chunk ^ (row >> 1 & 7)) << 4);
     } else if constexpr (sizeof(T) == 2) {
         const int turn = (row & 3) | ((row >> 1) & 4);
         return row * 256 + ((chunk ^ (turn << 1)) << 4);

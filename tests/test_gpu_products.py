@@ -60,6 +60,9 @@ def offsets_of(n, E, kind):
 # several tiles each way, whole tiles, rows whose starts are aligned and not.
 SHAPES = [(1, 1, 1, 1), (3, 2, 5, 7), (17, 4, 33, 64), (40, 5, 3, 2), (130, 3, 129, 65), (300, 5, 136, 200),
           (64, 8, 256, 520), (1000, 6, 304, 1032), (513, 2, 640, 96), (700, 3, 257, 259), (8, 64, 192, 256)]
+# Many rows an expert and rows that begin at 16 bytes: contractions of one and several
+# stages with and without a rest, tiles of more and fewer than 128 rows.
+SHAPES += [(300, 1, 136, 8), (1500, 4, 264, 200), (900, 2, 512, 1032), (520, 3, 1000, 40), (2100, 5, 152, 352)]
 KINDS = ["all", "holes", "one", "none"]
 
 
@@ -87,18 +90,18 @@ def test_products(n, E, N, K, kind, dtype):
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
-@pytest.mark.parametrize("N,K", [(40, 72), (130, 264), (33, 65)])
+@pytest.mark.parametrize("N,K", [(40, 72), (130, 264), (33, 65), (256, 328)])
 def test_products_strided(N, K, dtype):
     """Rows and matrices that are views: wider rows, every other row, experts in
     another order of strides, outputs among other columns; what lies beside them
     stays, NaN there does no harm."""
     note(f"strided {dtype} N={N} K={K}")
     gen = generator(N)
-    n, E = 150, 4
-    o = offsets_of(n, E, "holes")
-    s = po.spans(o, E, n)
-    for extra in (8, 3):
-        x = torch.full((2 * n, K + extra), float("nan"), dtype=DTYPES[dtype], device="cuda")[::2, 1:K + 1]
+    E = 4
+    for extra, n, begin in ((8, 150, 1), (3, 150, 1), (8, 1200, 0), (16, 700, 8)):
+        o = offsets_of(n, E, "holes")
+        s = po.spans(o, E, n)
+        x = torch.full((2 * n, K + extra), float("nan"), dtype=DTYPES[dtype], device="cuda")[::2, begin:K + begin]
         w = torch.full((N, E, K + extra), float("nan"), dtype=DTYPES[dtype], device="cuda")[:, :, :K].transpose(0, 1)
         g = torch.full((n, N + extra), float("nan"), dtype=DTYPES[dtype], device="cuda")[:, :N]
         x.copy_(normal(gen, (n, K), dtype)), w.copy_(normal(gen, (E, N, K), dtype)), g.copy_(normal(gen, (n, N), dtype))
