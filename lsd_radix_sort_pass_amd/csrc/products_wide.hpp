@@ -4,11 +4,12 @@
 //
 // The waves form two groups of four, one wave of each group on every SIMD.  Group
 // g has the rows q = 128 g .. 128 g + 127, each of its waves 64 columns p, so a
-// wave holds 128 x 64 results.  The contraction goes in stages of 64 bytes of c.
-// In a slot, one group reads the operands of its next stage from LDS while the
-// other multiplies; a barrier ends the slot and they change places.  A SIMD
-// thus multiplies in every slot, and no wave has to hold two stages' operands.
-// LDS is a ring of four stages, three of them on their way.
+// wave holds 128 x 64 results.  The contraction goes in stages of 128 bytes of c (whole
+// cache lines), two slots each: the first 64 rows of a group, then the other 64.  In a
+// slot, one group reads what it needs from LDS while the other multiplies; a barrier
+// ends the slot and they change places, so a SIMD multiplies in every slot.
+// LDS holds two stages.  What a slot has read, p and the first rows or the
+// others, is loaded again at once, and has five slots to arrive.
 //
 // A tile of at most 128 rows leaves group 1 without work, and the multiplying
 // slots of group 0 then follow each other at once: it takes little over half the time.
@@ -22,10 +23,10 @@ typedef int i32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWideThreads = 512;
 constexpr int kWide = 256;              // results of a tile each way
-constexpr int kStageBytes = 64;         // of c in a stage
+constexpr int kStageBytes = 128;        // of c in a stage
 constexpr int kWideOperand = kWide * kStageBytes;
-constexpr int kRing = 4;
-constexpr int kWideLds = kRing * 2 * kWideOperand;
+constexpr int kWideStage = 2 * kWideOperand;  // p, the first 64 rows q of both groups, their others
+constexpr int kWideLds = 2 * kWideStage;
 
 typedef __attribute__((address_space(3))) void *lds_ptr;
 
@@ -33,40 +34,36 @@ __device__ __forceinline__ unsigned lds_address(const void *p) {
     return static_cast<unsigned>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)p));
 }
 
-// Byte of a stage of an operand where 16-byte chunk `chunk` of its row `row`
-// stands.  Along c a row is one of 256 and has 4 chunks; across it is one of 32
-// steps of c and has 32 chunks, exchanged in fours of pairs, as the transposing read
-// takes 32 bytes of a row.  The lanes that LDS serves at once (256 bytes: 16 of the
-// wide reads, 32 of the transposing ones) meet every bank once: 246 bytes a clock and
-// CU, 126 where two meet.
-template <bool ACROSS>
+// Byte of a block of LDS where 16-byte chunk `chunk` of its row `row` stands.  Along
+// c a row has 8 chunks; across it is a step of c with 32 chunks (p) or 16 (half of
+// q), exchanged in fours, as the transposing read takes 32 bytes of a row.  The lanes that
+// LDS serves at once (256 bytes: 16 of the wide reads, 32 of the transposing ones)
+// meet every bank once: 246 bytes a clock and CU, 126 where two meet.
+template <bool ACROSS, int CHUNKS>
 __device__ __forceinline__ int stage_at(int row, int chunk) {
-    if constexpr (!ACROSS) {
-        return row * 64 + ((chunk ^ (row >> 2 & 3)) << 4);
-    } else {
-        return row * 512 + ((chunk ^ ((row & 3) << 2)) << 4);
-    }
+    static_assert(ACROSS || CHUNKS == 8);
+    const int turn = ACROSS ? (row & 3) << 2 : row >> 1 & 7;
+    return row * (CHUNKS * 16) + ((chunk ^ turn) << 4);
 }
 
-// Where a lane's reads of 32 rows or columns from mn on begin.  Along: at[k] for
-// step k, rows 32 j further on are 2048 j bytes further.  Across: at[j] for the columns
-// 32 j further on; 8192 bytes a step.
-template <bool ACROSS>
+// Where a lane's reads of 2 x 32 rows or columns from mn on begin.  Along: at[k] for
+// step k of 16 elements of c, and 4096 bytes further for the second 32 rows.
+// Across: at[j] for the j-th 32 columns, a step is 16 rows further.
+template <bool ACROSS, int CHUNKS>
 struct Reader {
-    unsigned at[ACROSS ? 4 : 2];
+    unsigned at[ACROSS ? 2 : 4];
 
     __device__ __forceinline__ void set(int mn, int lane) {
         if constexpr (!ACROSS) {
-            const int row = mn + (lane & 31), odd = lane >> 5;
-            at[0] = stage_at<false>(row, odd);
-            at[1] = stage_at<false>(row, 2 + odd);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) at[k] = stage_at<false, CHUNKS>(mn + (lane & 31), 2 * k + (lane >> 5));
         } else {
             const int i = lane & 15, g = lane >> 4;
             const int row = 8 * (g >> 1) + (i >> 2);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2; ++j) {
                 const int col = mn + 32 * j + 16 * (g & 1);
-                at[j] = stage_at<true>(row, (col >> 3) + (i >> 1 & 1)) + (i & 1) * 8;
+                at[j] = stage_at<true, CHUNKS>(row, (col >> 3) + (i >> 1 & 1)) + (i & 1) * 8;
             }
         }
     }
@@ -74,84 +71,99 @@ struct Reader {
 
 __device__ __forceinline__ i32x4 joined(i32x2 a, i32x2 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3); }
 
-// The operands of a stage of a wave: p of 2 x 32 and q of 4 x 32 rows, 2 steps of 16
-// elements of c.  The reads and the wait for them are one block, so that the compiler
-// neither waits for the loads into LDS before it nor uses a register too early.
-struct StageOperands {
-    i32x4 p[2][2], q[4][2];
+// Operands of 2 x 32 rows, 4 steps of 16 elements of c.
+struct Operands {
+    i32x4 f[2][4];
 };
 
-template <bool Q_ACROSS, bool P_ACROSS>
-__device__ __forceinline__ void read_stage(const Reader<Q_ACROSS> &rq, const Reader<P_ACROSS> &rp, unsigned q_base,
-                                           unsigned p_base, StageOperands &s) {
+// Reads of an operand's block and the wait for them, one block of instructions, so
+// that the compiler neither waits for the loads into LDS before it nor uses a register
+// too early.
 #if defined(__HIP_DEVICE_COMPILE__)  // (the host's pass knows no such registers)
-    if constexpr (!Q_ACROSS && !P_ACROSS) {
-        asm volatile(
-            "ds_read_b128 %0, %12\n ds_read_b128 %4, %14\n ds_read_b128 %5, %14 offset:2048\n"
-            "ds_read_b128 %6, %14 offset:4096\n ds_read_b128 %7, %14 offset:6144\n ds_read_b128 %1, %12 offset:2048\n"
-            "ds_read_b128 %2, %13\n ds_read_b128 %3, %13 offset:2048\n ds_read_b128 %8, %15\n"
-            "ds_read_b128 %9, %15 offset:2048\n ds_read_b128 %10, %15 offset:4096\n ds_read_b128 %11, %15 offset:6144\n"
-            "s_waitcnt lgkmcnt(0)"
-            : "=&v"(s.p[0][0]), "=&v"(s.p[1][0]), "=&v"(s.p[0][1]), "=&v"(s.p[1][1]), "=&v"(s.q[0][0]),
-              "=&v"(s.q[1][0]), "=&v"(s.q[2][0]), "=&v"(s.q[3][0]), "=&v"(s.q[0][1]), "=&v"(s.q[1][1]),
-              "=&v"(s.q[2][1]), "=&v"(s.q[3][1])
-            : "v"(p_base + rp.at[0]), "v"(p_base + rp.at[1]), "v"(q_base + rq.at[0]), "v"(q_base + rq.at[1])
-            : "memory");
-    } else if constexpr (!Q_ACROSS) {
-        i32x2 p[2][2][2];
-        asm volatile(
-            "ds_read_b64_tr_b16 %0, %16\n ds_read_b64_tr_b16 %1, %16 offset:2048\n"
-            "ds_read_b128 %8, %18\n ds_read_b128 %9, %18 offset:2048\n ds_read_b128 %10, %18 offset:4096\n"
-            "ds_read_b128 %11, %18 offset:6144\n"
-            "ds_read_b64_tr_b16 %4, %17\n ds_read_b64_tr_b16 %5, %17 offset:2048\n"
-            "ds_read_b64_tr_b16 %2, %16 offset:8192\n ds_read_b64_tr_b16 %3, %16 offset:10240\n"
-            "ds_read_b64_tr_b16 %6, %17 offset:8192\n ds_read_b64_tr_b16 %7, %17 offset:10240\n"
-            "ds_read_b128 %12, %19\n ds_read_b128 %13, %19 offset:2048\n ds_read_b128 %14, %19 offset:4096\n"
-            "ds_read_b128 %15, %19 offset:6144\n"
-            "s_waitcnt lgkmcnt(0)"
-            : "=&v"(p[0][0][0]), "=&v"(p[0][0][1]), "=&v"(p[0][1][0]), "=&v"(p[0][1][1]), "=&v"(p[1][0][0]),
-              "=&v"(p[1][0][1]), "=&v"(p[1][1][0]), "=&v"(p[1][1][1]), "=&v"(s.q[0][0]), "=&v"(s.q[1][0]),
-              "=&v"(s.q[2][0]), "=&v"(s.q[3][0]), "=&v"(s.q[0][1]), "=&v"(s.q[1][1]), "=&v"(s.q[2][1]),
-              "=&v"(s.q[3][1])
-            : "v"(p_base + rp.at[0]), "v"(p_base + rp.at[1]), "v"(q_base + rq.at[0]), "v"(q_base + rq.at[1])
-            : "memory");
+#define RS_READ_ALONG(n0, n1, n2, n3, n4, n5, n6, n7, a0, a1, a2, a3)                                    \
+    "ds_read_b128 %" #n0 ", %" #a0 "\n ds_read_b128 %" #n4 ", %" #a0 " offset:4096\n"                    \
+    "ds_read_b128 %" #n1 ", %" #a1 "\n ds_read_b128 %" #n5 ", %" #a1 " offset:4096\n"                    \
+    "ds_read_b128 %" #n2 ", %" #a2 "\n ds_read_b128 %" #n6 ", %" #a2 " offset:4096\n"                    \
+    "ds_read_b128 %" #n3 ", %" #a3 "\n ds_read_b128 %" #n7 ", %" #a3 " offset:4096\n"
+#define RS_ALONG_OUT(o)                                                                                   \
+    "=&v"(o.f[0][0]), "=&v"(o.f[0][1]), "=&v"(o.f[0][2]), "=&v"(o.f[0][3]), "=&v"(o.f[1][0]), "=&v"(o.f[1][1]), \
+        "=&v"(o.f[1][2]), "=&v"(o.f[1][3])
+#define RS_READ_TURNED(n, a, o) "ds_read_b64_tr_b16 %" #n ", %" #a " offset:" #o "\n"
+#define RS_TURNED_OUT(v)                                                                                  \
+    "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7]), \
+        "=&v"(v[8]), "=&v"(v[9]), "=&v"(v[10]), "=&v"(v[11]), "=&v"(v[12]), "=&v"(v[13]), "=&v"(v[14]), "=&v"(v[15])
+#endif
+
+__device__ __forceinline__ void from_turned(const i32x2 (&v)[16], Operands &o) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < 2; ++j) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) s.p[j][k] = joined(p[j][k][0], p[j][k][1]);
-        }
+        for (int k = 0; k < 4; ++k) o.f[j][k] = joined(v[8 * j + 2 * k], v[8 * j + 2 * k + 1]);
+    }
+}
+
+// q alone.
+template <bool Q_ACROSS>
+__device__ __forceinline__ void read_q(const Reader<Q_ACROSS, Q_ACROSS ? 16 : 8> &r, unsigned base, Operands &o) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    if constexpr (!Q_ACROSS) {
+        asm volatile(RS_READ_ALONG(0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11) "s_waitcnt lgkmcnt(0)"
+                     : RS_ALONG_OUT(o)
+                     : "v"(base + r.at[0]), "v"(base + r.at[1]), "v"(base + r.at[2]), "v"(base + r.at[3])
+                     : "memory");
     } else {
-        static_assert(Q_ACROSS && P_ACROSS);
-        i32x2 p[2][2][2], q[4][2][2];
-        asm volatile(
-            "ds_read_b64_tr_b16 %0, %24\n ds_read_b64_tr_b16 %1, %24 offset:2048\n"
-            "ds_read_b64_tr_b16 %8, %26\n ds_read_b64_tr_b16 %9, %26 offset:2048\n"
-            "ds_read_b64_tr_b16 %12, %27\n ds_read_b64_tr_b16 %13, %27 offset:2048\n"
-            "ds_read_b64_tr_b16 %16, %28\n ds_read_b64_tr_b16 %17, %28 offset:2048\n"
-            "ds_read_b64_tr_b16 %20, %29\n ds_read_b64_tr_b16 %21, %29 offset:2048\n"
-            "ds_read_b64_tr_b16 %4, %25\n ds_read_b64_tr_b16 %5, %25 offset:2048\n"
-            "ds_read_b64_tr_b16 %2, %24 offset:8192\n ds_read_b64_tr_b16 %3, %24 offset:10240\n"
-            "ds_read_b64_tr_b16 %10, %26 offset:8192\n ds_read_b64_tr_b16 %11, %26 offset:10240\n"
-            "ds_read_b64_tr_b16 %14, %27 offset:8192\n ds_read_b64_tr_b16 %15, %27 offset:10240\n"
-            "ds_read_b64_tr_b16 %18, %28 offset:8192\n ds_read_b64_tr_b16 %19, %28 offset:10240\n"
-            "ds_read_b64_tr_b16 %22, %29 offset:8192\n ds_read_b64_tr_b16 %23, %29 offset:10240\n"
-            "ds_read_b64_tr_b16 %6, %25 offset:8192\n ds_read_b64_tr_b16 %7, %25 offset:10240\n"
-            "s_waitcnt lgkmcnt(0)"
-            : "=&v"(p[0][0][0]), "=&v"(p[0][0][1]), "=&v"(p[0][1][0]), "=&v"(p[0][1][1]), "=&v"(p[1][0][0]),
-              "=&v"(p[1][0][1]), "=&v"(p[1][1][0]), "=&v"(p[1][1][1]), "=&v"(q[0][0][0]), "=&v"(q[0][0][1]),
-              "=&v"(q[0][1][0]), "=&v"(q[0][1][1]), "=&v"(q[1][0][0]), "=&v"(q[1][0][1]), "=&v"(q[1][1][0]),
-              "=&v"(q[1][1][1]), "=&v"(q[2][0][0]), "=&v"(q[2][0][1]), "=&v"(q[2][1][0]), "=&v"(q[2][1][1]),
-              "=&v"(q[3][0][0]), "=&v"(q[3][0][1]), "=&v"(q[3][1][0]), "=&v"(q[3][1][1])
-            : "v"(p_base + rp.at[0]), "v"(p_base + rp.at[1]), "v"(q_base + rq.at[0]), "v"(q_base + rq.at[1]),
-              "v"(q_base + rq.at[2]), "v"(q_base + rq.at[3])
-            : "memory");
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) s.p[j][k] = joined(p[j][k][0], p[j][k][1]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s.q[j][k] = joined(q[j][k][0], q[j][k][1]);
+        i32x2 v[16];
+        asm volatile(RS_READ_TURNED(0, 16, 0) RS_READ_TURNED(1, 16, 1024) RS_READ_TURNED(8, 17, 0)
+                     RS_READ_TURNED(9, 17, 1024) RS_READ_TURNED(2, 16, 4096) RS_READ_TURNED(3, 16, 5120)
+                     RS_READ_TURNED(10, 17, 4096) RS_READ_TURNED(11, 17, 5120) RS_READ_TURNED(4, 16, 8192)
+                     RS_READ_TURNED(5, 16, 9216) RS_READ_TURNED(12, 17, 8192) RS_READ_TURNED(13, 17, 9216)
+                     RS_READ_TURNED(6, 16, 12288) RS_READ_TURNED(7, 16, 13312) RS_READ_TURNED(14, 17, 12288)
+                     RS_READ_TURNED(15, 17, 13312) "s_waitcnt lgkmcnt(0)"
+                     : RS_TURNED_OUT(v)
+                     : "v"(base + r.at[0]), "v"(base + r.at[1])
+                     : "memory");
+        from_turned(v, o);
+    }
+#endif
+}
+
+// p and q.
+template <bool Q_ACROSS, bool P_ACROSS>
+__device__ __forceinline__ void read_pq(const Reader<Q_ACROSS, Q_ACROSS ? 16 : 8> &rq,
+                                        const Reader<P_ACROSS, P_ACROSS ? 32 : 8> &rp, unsigned q_base,
+                                        unsigned p_base, Operands &q, Operands &p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    if constexpr (!P_ACROSS) {
+        static_assert(!Q_ACROSS);
+        asm volatile(RS_READ_ALONG(0, 1, 2, 3, 4, 5, 6, 7, 16, 17, 18, 19)
+                     RS_READ_ALONG(8, 9, 10, 11, 12, 13, 14, 15, 20, 21, 22, 23) "s_waitcnt lgkmcnt(0)"
+                     : RS_ALONG_OUT(p), RS_ALONG_OUT(q)
+                     : "v"(p_base + rp.at[0]), "v"(p_base + rp.at[1]), "v"(p_base + rp.at[2]), "v"(p_base + rp.at[3]),
+                       "v"(q_base + rq.at[0]), "v"(q_base + rq.at[1]), "v"(q_base + rq.at[2]), "v"(q_base + rq.at[3])
+                     : "memory");
+    } else {
+#define RS_READ_TURNED_P(a, b)                                                                                     \
+    RS_READ_TURNED(0, a, 0) RS_READ_TURNED(1, a, 2048) RS_READ_TURNED(8, b, 0) RS_READ_TURNED(9, b, 2048)             \
+    RS_READ_TURNED(2, a, 8192) RS_READ_TURNED(3, a, 10240) RS_READ_TURNED(10, b, 8192)                              \
+    RS_READ_TURNED(11, b, 10240) RS_READ_TURNED(4, a, 16384) RS_READ_TURNED(5, a, 18432)                            \
+    RS_READ_TURNED(12, b, 16384) RS_READ_TURNED(13, b, 18432) RS_READ_TURNED(6, a, 24576)                           \
+    RS_READ_TURNED(7, a, 26624) RS_READ_TURNED(14, b, 24576) RS_READ_TURNED(15, b, 26624)
+        i32x2 v[16];
+        if constexpr (!Q_ACROSS) {
+            asm volatile(RS_READ_TURNED_P(24, 25) RS_READ_ALONG(16, 17, 18, 19, 20, 21, 22, 23, 26, 27, 28, 29)
+                         "s_waitcnt lgkmcnt(0)"
+                         : RS_TURNED_OUT(v), RS_ALONG_OUT(q)
+                         : "v"(p_base + rp.at[0]), "v"(p_base + rp.at[1]), "v"(q_base + rq.at[0]),
+                           "v"(q_base + rq.at[1]), "v"(q_base + rq.at[2]), "v"(q_base + rq.at[3])
+                         : "memory");
+        } else {
+            asm volatile(RS_READ_TURNED_P(16, 17) "s_waitcnt lgkmcnt(0)"
+                         : RS_TURNED_OUT(v)
+                         : "v"(p_base + rp.at[0]), "v"(p_base + rp.at[1])
+                         : "memory");
+            read_q<true>(rq, q_base, q);
         }
+        from_turned(v, p);
     }
 #endif
 }
@@ -179,60 +191,66 @@ __device__ __forceinline__ const T *uniform(const T *p) {
     return reinterpret_cast<const T *>(static_cast<uintptr_t>(hi) << 32 | lo);
 }
 
-// An operand on its way into LDS: a wave brings 2 x 1 KiB of a stage.
-template <class T, bool ACROSS>
+// A block of an operand on its way into LDS, a KiB a wave and load: p, 4 loads, or half
+// (0, 1) of q, 2 loads: 64 rows of each group.
+template <class T, bool ACROSS, bool IS_P>
 struct Feeder {
+    static constexpr int kLoads = IS_P ? 4 : 2;
+    static constexpr int kChunks = ACROSS ? (IS_P ? 32 : 16) : 8;
+    static constexpr int kRows = 64 / kChunks;  // of LDS in a load
     static constexpr int kStep = kStageBytes / static_cast<int>(sizeof(T));
-    unsigned offset[2];  // bytes from the tile's first element of a stage
-    const T *base;       // of the next stage
+    unsigned offset[kLoads];  // bytes from the tile's first element of a stage
+    const T *base;            // of the next stage
     size_t stride;
-    int rows, width, row0, col0;
+    int rows, width, first, half;
+
+    // Row or column of the tile that row or column i of the block is.
+    __device__ __forceinline__ int of_tile(int i) const { return IS_P ? i : (i >> 6) * 128 + half * 64 + (i & 63); }
 
     // Row and column in the tile of the 16 bytes that a lane brings in load i.
     // Rows and columns of results that do not exist are others' again.
     __device__ __forceinline__ void place(int i, int wave, int lane, int &row, int &col) const {
+        const int r = (kLoads * wave + i) * kRows + lane / kChunks, c = lane % kChunks;
         if constexpr (!ACROSS) {
-            const int r = (2 * wave + i) * 16 + (lane >> 2);
-            row = r < rows - row0 ? r : rows - row0 - 1;
-            col = ((lane & 3) ^ (r >> 2 & 3)) * 8;
+            const int t = of_tile(r), last = rows - first - 1;
+            row = t < last ? t : last;
+            col = (c ^ (r >> 1 & 7)) * 8;
         } else {
-            row = (2 * wave + i) * 2 + (lane >> 5);
-            const int c = ((lane & 31) ^ ((row & 3) << 2)) * 8;
-            col = c < width - col0 - 8 ? c : width - col0 - 8;
+            const int t = of_tile((c ^ ((r & 3) << 2)) * 8), last = width - first - 8;
+            row = r;
+            col = t < last ? t : last;
         }
     }
 
     // The operand's matrix has `rows` rows of `width` elements, the tile begins at
     // `first`, a row (along) or a column (across).
-    __device__ __forceinline__ void set(const T *matrix, size_t stride_, int rows_, int width_, int first, int wave,
-                                        int lane) {
-        stride = stride_, rows = rows_, width = width_;
-        row0 = ACROSS ? 0 : first, col0 = ACROSS ? first : 0;
-        base = uniform(matrix + static_cast<size_t>(row0) * stride + col0);
+    __device__ __forceinline__ void set(const T *matrix, size_t stride_, int rows_, int width_, int first_, int half_,
+                                        int wave, int lane) {
+        stride = stride_, rows = rows_, width = width_, first = first_, half = half_;
+        base = uniform(matrix + (ACROSS ? static_cast<size_t>(first) : static_cast<size_t>(first) * stride));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kLoads; ++i) {
             int row, col;
             place(i, wave, lane, row, col);
             offset[i] = static_cast<unsigned>((static_cast<size_t>(row) * stride + col) * sizeof(T));
         }
     }
 
-    // Enqueues the loads of the next stage to `to`.
-    __device__ __forceinline__ void load(char *to, int wave) {
-        const auto from = __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(base), 0, 0x7FFFFFFF, 0x00020000);
+    // Enqueues the loads of the next stage, of which `have` elements of c exist, to
+    // `to`.  The last ones go through registers, with zeros behind them.
+    __device__ __forceinline__ void load(char *to, int wave, int lane, int have) {
+        if (have >= kStep) {
+            const auto from = __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(base), 0, 0x7FFFFFFF, 0x00020000);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr)(to + (2 * wave + i) * 1024), 16,
-                                                     static_cast<int>(offset[i]), 0, 0, 0);
+            for (int i = 0; i < kLoads; ++i) {
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr)(to + (kLoads * wave + i) * 1024), 16,
+                                                         static_cast<int>(offset[i]), 0, 0, 0);
+            }
+            base += ACROSS ? kStep * stride : kStep;
+            return;
         }
-        base += ACROSS ? kStep * stride : kStep;
-    }
-
-    // The last stage, of which `have` elements of c exist: through registers, zeros
-    // behind them.
-    __device__ __forceinline__ void load_part(char *to, int wave, int lane, int have) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kLoads; ++i) {
             int row, col;
             place(i, wave, lane, row, col);
             i32x4 v;
@@ -246,8 +264,9 @@ struct Feeder {
                 v = load16(reinterpret_cast<const char *>(base + static_cast<size_t>(r) * stride + col));
                 if (row >= have) v = i32x4{0, 0, 0, 0};
             }
-            *reinterpret_cast<i32x4 *>(to + (2 * wave + i) * 1024 + lane * 16) = v;
+            *reinterpret_cast<i32x4 *>(to + (kLoads * wave + i) * 1024 + lane * 16) = v;
         }
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     }
 };
 
@@ -387,37 +406,41 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
         }
     }
     if (stages > 0) {
-        Feeder<T, Q_ACROSS> fq;
-        Feeder<T, P_ACROSS> fp;
-        fq.set(q, w.q_stride, Q_ACROSS ? c_n : q_rows, Q_ACROSS ? w.qn : c_n, q0, wave, lane);
-        fp.set(p, w.p_stride, P_ACROSS ? c_n : w.pn, P_ACROSS ? w.pn : c_n, p0, wave, lane);
-        Reader<Q_ACROSS> rq;
-        Reader<P_ACROSS> rp;
-        rq.set(q_wave, lane);
+        Feeder<T, Q_ACROSS, false> f0, f1;
+        Feeder<T, P_ACROSS, true> fp;
+        f0.set(q, w.q_stride, Q_ACROSS ? c_n : q_rows, Q_ACROSS ? w.qn : c_n, q0, 0, wave, lane);
+        f1.set(q, w.q_stride, Q_ACROSS ? c_n : q_rows, Q_ACROSS ? w.qn : c_n, q0, 1, wave, lane);
+        fp.set(p, w.p_stride, P_ACROSS ? c_n : w.pn, P_ACROSS ? w.pn : c_n, p0, 0, wave, lane);
+        Reader<Q_ACROSS, Q_ACROSS ? 16 : 8> rq;
+        Reader<P_ACROSS, P_ACROSS ? 32 : 8> rp;
+        rq.set(group * 64, lane);
         rp.set(p_wave, lane);
         const unsigned lds = lds_address(ring);
-        // Whether this wave has results at all.
-        const bool works = q0 + q_wave < q_rows && p0 + p_wave < w.pn;
+        // Whether this wave has results at all, and in its second 64 rows.
+        const bool works = q0 + q_wave < q_rows && p0 + p_wave < w.pn, works1 = works && q0 + q_wave + 64 < q_rows;
 
-        const auto issue = [&](int s) {
-            char *to = ring + s % kRing * (2 * kWideOperand);
-            const int have = c_n - s * kStep;
-            if (have >= kStep) {
-                fq.load(to, wave);
-                fp.load(to + kWideOperand, wave);
-            } else {
-                fq.load_part(to, wave, lane, have);
-                fp.load_part(to + kWideOperand, wave, lane, have);
-                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        // Six loads a wave: p and the first rows of stage s; two: the others.
+        const auto issue0 = [&](int s) {
+            if (s >= stages) return;
+            char *to = ring + s % 2 * kWideStage;
+            fp.load(to, wave, lane, c_n - s * kStep);
+            f0.load(to + kWideOperand, wave, lane, c_n - s * kStep);
+        };
+        const auto issue1 = [&](int s) {
+            if (s < stages) f1.load(ring + s % 2 * kWideStage + kWideOperand * 3 / 2, wave, lane, c_n - s * kStep);
+        };
+        // Waits for the first part of stage s (behind it its second and the first of the
+        // next may be on their way), or for its second (behind it the whole next one).
+        const auto arrived0 = [&](int s) {
+            if (s + 1 < stages) {
+                asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+            } else if (s < stages) {
+                asm volatile("s_waitcnt vmcnt(2)" ::: "memory");
             }
         };
-        // Waits until of the stages enqueued last only `late` are on their way: four
-        // loads each.
-        const auto wait = [&](int late) {
-            if (late >= 2) {
+        const auto arrived1 = [&](int s) {
+            if (s + 1 < stages) {
                 asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
-            } else if (late == 1) {
-                asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
             } else {
                 asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             }
@@ -427,31 +450,54 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
         };
-        const int first = stages < 3 ? stages : 3;
-        for (int s = 0; s < first; ++s) issue(s);
-        wait(first - 1);
-        barrier();
-        if (group == 1) barrier();  // half a turn behind
-        for (int s = 0; s < stages; ++s) {
-            // The place of stage s + 3 was read last, by group 1, in the slot before this one.
-            if (s + 3 < stages) issue(s + 3);
-            StageOperands o;
-            const unsigned at = lds + static_cast<unsigned>(s % kRing) * (2 * kWideOperand);
-            if (works) read_stage<Q_ACROSS, P_ACROSS>(rq, rp, at, at + kWideOperand, o);
-            wait(stages - 2 - s);
-            barrier();
-            if (works) {
-                __builtin_amdgcn_s_setprio(1);
+        Operands op, oq;
+        const auto multiply = [&](int s, auto half) {
+            constexpr int kHalf = decltype(half)::value;
+            __builtin_amdgcn_s_setprio(1);
+            const auto step = [&](int k) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[i][j] = mma32<T>(o.p[i][k], o.q[j][k], acc[i][j]);
+                    for (int j = 0; j < 2; ++j) {
+                        acc[i][2 * kHalf + j] = mma32<T>(op.f[i][k], oq.f[j][k], acc[i][2 * kHalf + j]);
                     }
                 }
-                __builtin_amdgcn_s_setprio(0);
+            };
+            step(0);
+            step(1);
+            if (c_n - s * kStep > kStep / 2) {
+                step(2);
+                step(3);
             }
+            __builtin_amdgcn_s_setprio(0);
+        };
+        issue0(0);
+        issue1(0);
+        issue0(1);
+        issue1(1);
+        arrived1(0);
+        barrier();
+        // Slots: group 0 reads in the even ones and multiplies in the odd ones, group 1
+        // the other way round, a slot later.  What group 0 reads of stage s in slot 4 s
+        // and 4 s + 2, group 1 has read at the end of slot 4 s + 1 and 4 s + 3: from then on
+        // stage s + 2 takes its place.  Both groups have waited for it before group 0's slot
+        // 4 s + 8 or 4 s + 10.
+        if (group == 1) barrier();
+        for (int s = 0; s < stages; ++s) {
+            const unsigned at = lds + static_cast<unsigned>(s % 2) * kWideStage;
+            if (works) read_pq<Q_ACROSS, P_ACROSS>(rq, rp, at + kWideOperand, at, oq, op);
+            if (s > 0) issue1(s + 1);
+            if (group == 1) arrived1(s);
+            barrier();
+            if (works) multiply(s, std::integral_constant<int, 0>{});
+            if (group == 0) arrived1(s);
+            barrier();
+            if (works1) read_q<Q_ACROSS>(rq, at + kWideOperand * 3 / 2, oq);
+            issue0(s + 2);
+            if (group == 1) arrived0(s + 1);
+            barrier();
+            if (works1) multiply(s, std::integral_constant<int, 1>{});
+            if (group == 0) arrived0(s + 1);
             barrier();
         }
         if (group == 0) barrier();
