@@ -2,17 +2,18 @@
 // 256 x 256 results a workgroup of eight waves, operands brought to LDS by the
 // memory system itself, without passing through registers.
 //
-// The waves form two groups of four, one wave of each group on every SIMD.  Group
-// g has the rows q = 128 g .. 128 g + 127, each of its waves 64 columns p, so a
-// wave holds 128 x 64 results.  The contraction goes in stages of 128 bytes of c (whole
+// The waves form two groups of four, one wave of each group on every SIMD.  Each group
+// has half of the rows q, each of its waves 64 columns p, so a wave holds 128 x 64
+// results.  The contraction goes in stages of 128 bytes of c (whole
 // cache lines), two slots each: the first 64 rows of a group, then the other 64.  In a
 // slot, one group reads what it needs from LDS while the other multiplies; a barrier
 // ends the slot and they change places, so a SIMD multiplies in every slot.
 // LDS holds two stages.  What a slot has read, p and the first rows or the
 // others, is loaded again at once, and has five slots to arrive.
 //
-// A tile of at most 128 rows leaves group 1 without work, and the multiplying
-// slots of group 0 then follow each other at once: it takes little over half the time.
+// A tile with fewer rows is shared evenly, in 32s: its time goes with its rows in steps
+// of 64.  One of at most 128 has no second rows: a stage is then one slot, and three
+// fit into LDS.
 #pragma once
 
 #include "products.hpp"
@@ -26,7 +27,8 @@ constexpr int kWide = 256;              // results of a tile each way
 constexpr int kStageBytes = 128;        // of c in a stage
 constexpr int kWideOperand = kWide * kStageBytes;
 constexpr int kWideStage = 2 * kWideOperand;  // p, the first 64 rows q of both groups, their others
-constexpr int kWideLds = 2 * kWideStage;
+constexpr int kFlatStage = kWideStage * 3 / 4;  // without the others
+constexpr int kWideLds = 3 * kFlatStage;      // three of the latter, two of the former
 
 typedef __attribute__((address_space(3))) void *lds_ptr;
 
@@ -202,10 +204,10 @@ struct Feeder {
     unsigned offset[kLoads];  // bytes from the tile's first element of a stage
     const T *base;            // of the next stage
     size_t stride;
-    int rows, width, first, half;
+    int rows, width, first, half, height;
 
     // Row or column of the tile that row or column i of the block is.
-    __device__ __forceinline__ int of_tile(int i) const { return IS_P ? i : (i >> 6) * 128 + half * 64 + (i & 63); }
+    __device__ __forceinline__ int of_tile(int i) const { return IS_P ? i : (i >> 6) * height + half * 64 + (i & 63); }
 
     // Row and column in the tile of the 16 bytes that a lane brings in load i.
     // Rows and columns of results that do not exist are others' again.
@@ -223,10 +225,10 @@ struct Feeder {
     }
 
     // The operand's matrix has `rows` rows of `width` elements, the tile begins at
-    // `first`, a row (along) or a column (across).
+    // `first`, a row (along) or a column (across), and a group has `height` rows q.
     __device__ __forceinline__ void set(const T *matrix, size_t stride_, int rows_, int width_, int first_, int half_,
-                                        int wave, int lane) {
-        stride = stride_, rows = rows_, width = width_, first = first_, half = half_;
+                                        int height_, int wave, int lane) {
+        stride = stride_, rows = rows_, width = width_, first = first_, half = half_, height = height_;
         base = uniform(matrix + (ACROSS ? static_cast<size_t>(first) : static_cast<size_t>(first) * stride));
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
@@ -249,10 +251,14 @@ struct Feeder {
             base += ACROSS ? kStep * stride : kStep;
             return;
         }
+        int own = lane;
+#if defined(__HIP_DEVICE_COMPILE__)
+        asm volatile("" : "+v"(own));  // keeps what follows from being worked out, and held, before the loop
+#endif
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             int row, col;
-            place(i, wave, lane, row, col);
+            place(i, wave, own, row, col);
             i32x4 v;
             if constexpr (!ACROSS) {
                 // From the row's last whole chunk at most (the row has one).
@@ -362,7 +368,7 @@ template <class T, bool RAGGED_C, bool Q_ACROSS, bool P_ACROSS>
 __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const ProductWork<T, T> w) {
     __shared__ __align__(1024) char ring[kWideLds];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int group = wave >> 2, q_wave = group * 128, p_wave = (wave & 3) * 64;
+    const int group = wave >> 2, p_wave = (wave & 3) * 64;
     const int num_rows = static_cast<int>(w.num_rows), p_tiles = (w.pn + kWide - 1) / kWide;
 
     const T *q = w.q, *p = w.p;
@@ -393,6 +399,9 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
     }
 
     if (q0 >= q_rows || p0 >= w.pn) return;
+    // Rows of a group: half of the tile's, in 32s.
+    const int left = q_rows - q0 < kWide ? q_rows - q0 : kWide;
+    const int height = (left + 63) / 64 * 32, q_wave = group * height;
 
     constexpr int kStep = kStageBytes / static_cast<int>(sizeof(T));
     const int stages = (c_n + kStep - 1) / kStep;
@@ -408,23 +417,24 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
     if (stages > 0) {
         Feeder<T, Q_ACROSS, false> f0, f1;
         Feeder<T, P_ACROSS, true> fp;
-        f0.set(q, w.q_stride, Q_ACROSS ? c_n : q_rows, Q_ACROSS ? w.qn : c_n, q0, 0, wave, lane);
-        f1.set(q, w.q_stride, Q_ACROSS ? c_n : q_rows, Q_ACROSS ? w.qn : c_n, q0, 1, wave, lane);
-        fp.set(p, w.p_stride, P_ACROSS ? c_n : w.pn, P_ACROSS ? w.pn : c_n, p0, 0, wave, lane);
+        f0.set(q, w.q_stride, Q_ACROSS ? c_n : q_rows, Q_ACROSS ? w.qn : c_n, q0, 0, height, wave, lane);
+        f1.set(q, w.q_stride, Q_ACROSS ? c_n : q_rows, Q_ACROSS ? w.qn : c_n, q0, 1, height, wave, lane);
+        fp.set(p, w.p_stride, P_ACROSS ? c_n : w.pn, P_ACROSS ? w.pn : c_n, p0, 0, 0, wave, lane);
         Reader<Q_ACROSS, Q_ACROSS ? 16 : 8> rq;
         Reader<P_ACROSS, P_ACROSS ? 32 : 8> rp;
         rq.set(group * 64, lane);
         rp.set(p_wave, lane);
         const unsigned lds = lds_address(ring);
-        // Whether this wave has results at all, and in its second 64 rows.
-        const bool works = q0 + q_wave < q_rows && p0 + p_wave < w.pn, works1 = works && q0 + q_wave + 64 < q_rows;
+        // Whether this wave has results at all.
+        const bool works = q0 + q_wave < q_rows && p0 + p_wave < w.pn;
 
-        // Six loads a wave: p and the first rows of stage s; two: the others.
-        const auto issue0 = [&](int s) {
-            if (s >= stages) return;
-            char *to = ring + s % 2 * kWideStage;
+        // Six loads a wave: p and the first rows of stage s, to `to`; two: the others.
+        const auto load0 = [&](int s, char *to) {
             fp.load(to, wave, lane, c_n - s * kStep);
             f0.load(to + kWideOperand, wave, lane, c_n - s * kStep);
+        };
+        const auto issue0 = [&](int s) {
+            if (s < stages) load0(s, ring + s % 2 * kWideStage);
         };
         const auto issue1 = [&](int s) {
             if (s < stages) f1.load(ring + s % 2 * kWideStage + kWideOperand * 3 / 2, wave, lane, c_n - s * kStep);
@@ -451,61 +461,104 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
             __builtin_amdgcn_sched_barrier(0);
         };
         Operands op, oq;
+        // Multiplies rows 64 HALF .. of the group with the operands read last.
         const auto multiply = [&](int s, auto half) {
             constexpr int kHalf = decltype(half)::value;
-            __builtin_amdgcn_s_setprio(1);
-            const auto step = [&](int k) {
+            const auto steps = [&](auto from, auto blocks) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int k = from; k < from + 2; ++k) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        acc[i][2 * kHalf + j] = mma32<T>(op.f[i][k], oq.f[j][k], acc[i][2 * kHalf + j]);
+                    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                        for (int j = 0; j < blocks; ++j) {
+                            acc[i][2 * kHalf + j] = mma32<T>(op.f[i][k], oq.f[j][k], acc[i][2 * kHalf + j]);
+                        }
                     }
                 }
             };
-            step(0);
-            step(1);
-            if (c_n - s * kStep > kStep / 2) {
-                step(2);
-                step(3);
+            const bool second = c_n - s * kStep > kStep / 2;  // (zeros otherwise)
+            __builtin_amdgcn_s_setprio(1);
+            if (height >= 64 * kHalf + 64) {
+                steps(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{});
+                if (second) steps(std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{});
+            } else {
+                steps(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{});
+                if (second) steps(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});
             }
             __builtin_amdgcn_s_setprio(0);
         };
-        issue0(0);
-        issue1(0);
-        issue0(1);
-        issue1(1);
-        arrived1(0);
-        barrier();
         // Slots: group 0 reads in the even ones and multiplies in the odd ones, group 1
-        // the other way round, a slot later.  What group 0 reads of stage s in slot 4 s
-        // and 4 s + 2, group 1 has read at the end of slot 4 s + 1 and 4 s + 3: from then on
-        // stage s + 2 takes its place.  Both groups have waited for it before group 0's slot
-        // 4 s + 8 or 4 s + 10.
-        if (group == 1) barrier();
-        for (int s = 0; s < stages; ++s) {
-            const unsigned at = lds + static_cast<unsigned>(s % 2) * kWideStage;
-            if (works) read_pq<Q_ACROSS, P_ACROSS>(rq, rp, at + kWideOperand, at, oq, op);
-            if (s > 0) issue1(s + 1);
-            if (group == 1) arrived1(s);
+        // the other way round, a slot later.  Group 1 is the last to multiply, and nobody
+        // waits for that.
+        if (height > 64) {
+            // What group 0 reads of stage s in slots 4 s and 4 s + 2, group 1 has read at the
+            // end of slots 4 s + 1 and 4 s + 3: from then on stage s + 2 takes its place.
+            // Both groups have waited for it before group 0's slots 4 s + 8 and 4 s + 10.
+            issue0(0);
+            issue1(0);
+            issue0(1);
+            issue1(1);
+            arrived1(0);
             barrier();
-            if (works) multiply(s, std::integral_constant<int, 0>{});
-            if (group == 0) arrived1(s);
+            if (group == 1) barrier();
+            for (int s = 0; s < stages; ++s) {
+                const unsigned at = lds + static_cast<unsigned>(s % 2) * kWideStage;
+                if (works) read_pq<Q_ACROSS, P_ACROSS>(rq, rp, at + kWideOperand, at, oq, op);
+                if (s > 0) issue1(s + 1);
+                if (group == 1) arrived1(s);
+                barrier();
+                if (works) multiply(s, std::integral_constant<int, 0>{});
+                if (group == 0) arrived1(s);
+                barrier();
+                if (works) read_q<Q_ACROSS>(rq, at + kWideOperand * 3 / 2, oq);
+                issue0(s + 2);
+                if (group == 1) arrived0(s + 1);
+                barrier();
+                if (works) multiply(s, std::integral_constant<int, 1>{});
+                if (group == 0) arrived0(s + 1);
+                if (s + 1 < stages || group == 0) barrier();
+            }
+        } else {
+            // Group 0 reads stage s in slot 2 s, group 1 in the next; from slot 2 s + 2 on
+            // stage s + 3 takes its place.  It is read first in slot 2 s + 6.
+            const auto issue = [&](int s, unsigned place) {
+                if (s < stages) load0(s, ring + place * kFlatStage);
+            };
+            const auto arrived = [&](int s) {  // behind stage s the next may be on its way
+                if (s + 1 < stages) {
+                    asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+                } else {
+                    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                }
+            };
+            issue(0, 0);
+            issue(1, 1);
+            arrived(0);
+            if (group == 1) issue(2, 2);
             barrier();
-            if (works1) read_q<Q_ACROSS>(rq, at + kWideOperand * 3 / 2, oq);
-            issue0(s + 2);
-            if (group == 1) arrived0(s + 1);
-            barrier();
-            if (works1) multiply(s, std::integral_constant<int, 1>{});
-            if (group == 0) arrived0(s + 1);
-            barrier();
+            if (group == 1) barrier();
+            unsigned place = 0;
+            for (int s = 0; s < stages; ++s) {
+                const unsigned at = lds + place * kFlatStage, before = place == 0 ? 2 : place - 1;
+                if (works) read_pq<Q_ACROSS, P_ACROSS>(rq, rp, at + kWideOperand, at, oq, op);
+                if (group == 0) {
+                    issue(s + 2, before);
+                } else {
+                    arrived(s + 1);
+                }
+                barrier();
+                if (group == 1) issue(s + 3, place);
+                if (works) multiply(s, std::integral_constant<int, 0>{});
+                if (group == 0) arrived(s + 1);
+                if (s + 1 < stages || group == 0) barrier();
+                place = place == 2 ? 0 : place + 1;
+            }
         }
-        if (group == 0) barrier();
     }
 
-    // Results to rows: through the wave's 16 KiB of the ring, 128 rows of 64
-    // elements, so that 8 lanes write 128 bytes of a row.
-    __syncthreads();
+    // Results to rows: through the wave's own 16 KiB of LDS, 128 rows of 64
+    // elements, so that 8 lanes write 128 bytes of a row.  (All operands have been
+    // read: group 0 passed the barrier behind the slot in which group 1 read the last.)
     char *mine = ring + wave * 16384;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -523,9 +576,8 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
             }
         }
     }
-    __syncthreads();
 #pragma unroll 4
-    for (int k = 0; k < 16; ++k) {
+    for (int k = 0; k < height / 8; ++k) {
         const int row = 8 * k + (lane >> 3), chunk = lane & 7;
         const i32x4 v = *reinterpret_cast<const i32x4 *>(mine + row * 128 + ((chunk ^ (row & 7)) << 4));
         const int qi = q0 + q_wave + row, pi = p0 + p_wave + 8 * chunk, have = w.pn - pi;

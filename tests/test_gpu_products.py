@@ -655,3 +655,22 @@ def test_kernel_timing():
     counts = [rs.prof_summary(kind)[0] for kind in (_lib.RS_KERNEL_PRODUCT, _lib.RS_KERNEL_GATE, _lib.RS_KERNEL_QUANTIZE)]
     assert counts[0] >= 4 and counts[1:] == [2, 2]
     rs.prof_reset()
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("N,K", [(264, 200), (520, 8), (136, 1000)])
+def test_products_tiles_of_every_height(N, K, dtype):
+    """Experts whose last tile has any number of rows, among many stages and one."""
+    note(f"heights {dtype} N={N} K={K}")
+    counts = [1, 31, 32, 33, 63, 64, 65, 96, 100, 127, 128, 129, 160, 191, 192, 193, 224, 255, 256, 300, 0, 513]
+    E, n, gen = len(counts), sum(counts) + 70, generator(N)
+    o = torch.tensor([40] + counts, device="cuda").cumsum(0).to(torch.int32)
+    s = po.spans(o, E, n)
+    x, w, g = normal(gen, (n, K), dtype), normal(gen, (E, N, K), dtype, K ** -0.5), normal(gen, (n, N), dtype)
+    exact, size = po.product(x, s, w, torch.zeros(n, N, device="cuda"))
+    close(rs.expert_products(x, o, w), exact, po.product_bound(exact, size, K, dtype), "product")
+    grad_rows, grad_w = rs.expert_products_backward(g, o, w, x)
+    exact, size = po.product_rows_backward(g, s, w, torch.zeros(n, K, device="cuda"))
+    close(grad_rows, exact, po.product_bound(exact, size, N, dtype), "gradient of rows")
+    exact, size = po.product_weights_backward(g, s, x)
+    close(grad_w, exact, po.product_bound(exact, size, n, dtype), "gradient of weights")
