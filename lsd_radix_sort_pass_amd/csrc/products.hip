@@ -16,6 +16,9 @@
 RS_WIDE(rs::f16)
 RS_WIDE(rs::bf16)
 #undef RS_WIDE
+template __global__ void rs::wide_fp8_kernel<float>(const rs::ProductWork<rs::fp8, float>);
+template __global__ void rs::wide_fp8_kernel<rs::f16>(const rs::ProductWork<rs::fp8, rs::f16>);
+template __global__ void rs::wide_fp8_kernel<rs::bf16>(const rs::ProductWork<rs::fp8, rs::bf16>);
 
 namespace {
 
@@ -70,17 +73,23 @@ bool feeds(const void *p, size_t stride, size_t expert, int width, bool across, 
 // Enqueues the product of w, whose results are q by p (RAGGED_C: of each expert).
 template <class T, class OUT, bool RAGGED_C, bool Q_ACROSS, bool P_ACROSS>
 bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
-    if constexpr (sizeof(T) == 2) {
+    if constexpr (sizeof(T) <= 2) {
         const size_t p_tiles = (static_cast<size_t>(w.pn) + rs::kWide - 1) / rs::kWide;
         const size_t tiles = RAGGED_C
             ? align_to((static_cast<size_t>(w.qn) + rs::kWide - 1) / rs::kWide * p_tiles, rs::kXcds) * static_cast<size_t>(w.experts)
             : align_to((w.num_rows / rs::kWide + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1) * p_tiles, rs::kXcds);
-        if (tiles <= (size_t{1} << 30) && feeds(w.q, w.q_stride, 0, Q_ACROSS ? w.qn : w.cn, Q_ACROSS, 2) &&
-            feeds(w.p, w.p_stride, w.p_expert, P_ACROSS ? w.pn : w.cn, P_ACROSS, 2) && wide_pays(w, RAGGED_C)) {
-            return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] {
-                run_kernel(rs::wide_product_kernel<T, RAGGED_C, Q_ACROSS, P_ACROSS>, static_cast<unsigned>(tiles),
-                           rs::kWideThreads, stream, w);
-            });
+        if (tiles <= (size_t{1} << 30) && feeds(w.q, w.q_stride, 0, Q_ACROSS ? w.qn : w.cn, Q_ACROSS, sizeof(T)) &&
+            feeds(w.p, w.p_stride, w.p_expert, P_ACROSS ? w.pn : w.cn, P_ACROSS, sizeof(T)) && wide_pays(w, RAGGED_C)) {
+            const auto go = [&](auto kernel) {
+                return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] {
+                    run_kernel(kernel, static_cast<unsigned>(tiles), rs::kWideThreads, stream, w);
+                });
+            };
+            if constexpr (sizeof(T) == 1) {
+                return go(rs::wide_fp8_kernel<OUT>);
+            } else {
+                return go(rs::wide_product_kernel<T, RAGGED_C, Q_ACROSS, P_ACROSS>);
+            }
         }
     }
     const size_t p_tiles = (static_cast<size_t>(w.pn) + 127) / 128;

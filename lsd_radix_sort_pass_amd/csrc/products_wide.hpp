@@ -201,6 +201,7 @@ struct Feeder {
     static constexpr int kChunks = ACROSS ? (IS_P ? 32 : 16) : 8;
     static constexpr int kRows = 64 / kChunks;  // of LDS in a load
     static constexpr int kStep = kStageBytes / static_cast<int>(sizeof(T));
+    static constexpr int V = 16 / static_cast<int>(sizeof(T));
     unsigned offset[kLoads];  // bytes from the tile's first element of a stage
     const T *base;            // of the next stage
     size_t stride;
@@ -216,9 +217,9 @@ struct Feeder {
         if constexpr (!ACROSS) {
             const int t = of_tile(r), last = rows - first - 1;
             row = t < last ? t : last;
-            col = (c ^ (r >> 1 & 7)) * 8;
+            col = (c ^ (r >> 1 & 7)) * V;
         } else {
-            const int t = of_tile((c ^ ((r & 3) << 2)) * 8), last = width - first - 8;
+            const int t = of_tile((c ^ ((r & 3) << 2)) * V), last = width - first - V;
             row = r;
             col = t < last ? t : last;
         }
@@ -262,7 +263,7 @@ struct Feeder {
             i32x4 v;
             if constexpr (!ACROSS) {
                 // From the row's last whole chunk at most (the row has one).
-                const int back = have - 8 < col ? have - 8 : col;
+                const int back = have - V < col ? have - V : col;
                 v = load16(reinterpret_cast<const char *>(base + static_cast<size_t>(row) * stride + back));
                 v = cut<T>(v, col, have);
             } else {
@@ -364,6 +365,33 @@ __device__ inline WideTile wide_weights_tile(int experts, int q_tiles, int p_til
     return t;
 }
 
+// The results of a wave to rows: through its own 16 KiB of LDS, which hold 128 rows of
+// 64 results of 16 bits, so that 8 lanes write 128 bytes of a row.
+template <class OUT>
+__device__ __forceinline__ void rows_from_lds(const char *mine, OUT *out, size_t stride, int height, int q_first,
+                                              int q_rows, int p_first, int pn, int lane) {
+#pragma unroll 4
+    for (int k = 0; k < height / 8; ++k) {
+        const int row = 8 * k + (lane >> 3), chunk = lane & 7;
+        const i32x4 v = *reinterpret_cast<const i32x4 *>(mine + row * 128 + ((chunk ^ (row & 7)) << 4));
+        const int qi = q_first + row, pi = p_first + 8 * chunk, have = pn - pi;
+        if (qi >= q_rows || have <= 0) continue;
+        OUT *to = out + static_cast<size_t>(qi) * stride + pi;
+        if (have >= 8) {
+            *reinterpret_cast<i32x4_any *>(to) = v;
+        } else {
+            union {
+                i32x4 all;
+                OUT e[8];
+            } u{v};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (e < have) to[e] = u.e[e];
+            }
+        }
+    }
+}
+
 template <class T, bool RAGGED_C, bool Q_ACROSS, bool P_ACROSS>
 __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const ProductWork<T, T> w) {
     __shared__ __align__(1024) char ring[kWideLds];
@@ -429,42 +457,42 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
         const bool works = q0 + q_wave < q_rows && p0 + p_wave < w.pn;
 
         // Six loads a wave: p and the first rows of stage s, to `to`; two: the others.
-        const auto load0 = [&](int s, char *to) {
+        const auto load0 = [&](int s, char *to) __attribute__((always_inline)) {
             fp.load(to, wave, lane, c_n - s * kStep);
             f0.load(to + kWideOperand, wave, lane, c_n - s * kStep);
         };
-        const auto issue0 = [&](int s) {
+        const auto issue0 = [&](int s) __attribute__((always_inline)) {
             if (s < stages) load0(s, ring + s % 2 * kWideStage);
         };
-        const auto issue1 = [&](int s) {
+        const auto issue1 = [&](int s) __attribute__((always_inline)) {
             if (s < stages) f1.load(ring + s % 2 * kWideStage + kWideOperand * 3 / 2, wave, lane, c_n - s * kStep);
         };
         // Waits for the first part of stage s (behind it its second and the first of the
         // next may be on their way), or for its second (behind it the whole next one).
-        const auto arrived0 = [&](int s) {
+        const auto arrived0 = [&](int s) __attribute__((always_inline)) {
             if (s + 1 < stages) {
                 asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
             } else if (s < stages) {
                 asm volatile("s_waitcnt vmcnt(2)" ::: "memory");
             }
         };
-        const auto arrived1 = [&](int s) {
+        const auto arrived1 = [&](int s) __attribute__((always_inline)) {
             if (s + 1 < stages) {
                 asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
             } else {
                 asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             }
         };
-        const auto barrier = [] {
+        const auto barrier = []() __attribute__((always_inline)) {
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
         };
         Operands op, oq;
         // Multiplies rows 64 HALF .. of the group with the operands read last.
-        const auto multiply = [&](int s, auto half) {
+        const auto multiply = [&](int s, auto half) __attribute__((always_inline)) {
             constexpr int kHalf = decltype(half)::value;
-            const auto steps = [&](auto from, auto blocks) {
+            const auto steps = [&](auto from, auto blocks) __attribute__((always_inline)) {
 #pragma unroll
                 for (int k = from; k < from + 2; ++k) {
 #pragma unroll
@@ -521,10 +549,10 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
         } else {
             // Group 0 reads stage s in slot 2 s, group 1 in the next; from slot 2 s + 2 on
             // stage s + 3 takes its place.  It is read first in slot 2 s + 6.
-            const auto issue = [&](int s, unsigned place) {
+            const auto issue = [&](int s, unsigned place) __attribute__((always_inline)) {
                 if (s < stages) load0(s, ring + place * kFlatStage);
             };
-            const auto arrived = [&](int s) {  // behind stage s the next may be on its way
+            const auto arrived = [&](int s) __attribute__((always_inline)) {  // behind stage s the next may be on its way
                 if (s + 1 < stages) {
                     asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
                 } else {
@@ -576,23 +604,295 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
             }
         }
     }
-#pragma unroll 4
-    for (int k = 0; k < height / 8; ++k) {
-        const int row = 8 * k + (lane >> 3), chunk = lane & 7;
-        const i32x4 v = *reinterpret_cast<const i32x4 *>(mine + row * 128 + ((chunk ^ (row & 7)) << 4));
-        const int qi = q0 + q_wave + row, pi = p0 + p_wave + 8 * chunk, have = w.pn - pi;
-        if (qi >= q_rows || have <= 0) continue;
-        T *to = out + static_cast<size_t>(qi) * w.out_stride + pi;
-        if (have >= 8) {
-            *reinterpret_cast<i32x4_any *>(to) = v;
-        } else {
-            union {
-                i32x4 all;
-                T e[8];
-            } u{v};
+    rows_from_lds(mine, out, w.out_stride, height, q0 + q_wave, q_rows, p0 + p_wave, w.pn, lane);
+}
+
+// ---------------------------------------------------------------------------
+// The same of operands in 8 bits: a stage is a block of 128 elements that share a
+// scale.  Results of a block stand for themselves times the scales of row and
+// matrix, and are added to the sums in float32: 16 x 16 of them at a time, while the next
+// are multiplied.  The scales of the rows come with the stage.
+// ---------------------------------------------------------------------------
+constexpr int kScaleBytes = 2048;  // of a stage: 256 rows, and room for as many loads that nobody reads
+
+struct Reader8 {
+    unsigned at[2];
+
+    __device__ __forceinline__ void set(int mn, int lane) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (e < have) to[e] = u.e[e];
+        for (int k = 0; k < 2; ++k) at[k] = stage_at<false, 8>(mn + (lane & 15), 4 * k + (lane >> 4));
+    }
+};
+
+// Operands of 4 x 16 rows, 128 elements of c, and the scales of rows q.
+struct Operands8 {
+    i32x4 f[4][2];
+};
+
+#if defined(__HIP_DEVICE_COMPILE__)
+#define RS_READ_8(n0, n1, n2, n3, n4, n5, n6, n7, a0, a1)                                       \
+    "ds_read_b128 %" #n0 ", %" #a0 "\n ds_read_b128 %" #n1 ", %" #a1 "\n"                       \
+    "ds_read_b128 %" #n2 ", %" #a0 " offset:2048\n ds_read_b128 %" #n3 ", %" #a1 " offset:2048\n" \
+    "ds_read_b128 %" #n4 ", %" #a0 " offset:4096\n ds_read_b128 %" #n5 ", %" #a1 " offset:4096\n" \
+    "ds_read_b128 %" #n6 ", %" #a0 " offset:6144\n ds_read_b128 %" #n7 ", %" #a1 " offset:6144\n"
+#define RS_READ_SCALES(n0, n1, n2, n3, a)                                        \
+    "ds_read_b32 %" #n0 ", %" #a "\n ds_read_b32 %" #n1 ", %" #a " offset:64\n" \
+    "ds_read_b32 %" #n2 ", %" #a " offset:128\n ds_read_b32 %" #n3 ", %" #a " offset:192\n"
+#define RS_8_OUT(o)                                                                                               \
+    "=&v"(o.f[0][0]), "=&v"(o.f[0][1]), "=&v"(o.f[1][0]), "=&v"(o.f[1][1]), "=&v"(o.f[2][0]), "=&v"(o.f[2][1]), \
+        "=&v"(o.f[3][0]), "=&v"(o.f[3][1])
+#endif
+
+__device__ __forceinline__ void read_pq8(const Reader8 &rq, const Reader8 &rp, unsigned q_base, unsigned p_base,
+                                         unsigned scales, Operands8 &q, Operands8 &p, float (&scale)[4]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile(RS_READ_8(0, 1, 2, 3, 4, 5, 6, 7, 20, 21) RS_READ_8(8, 9, 10, 11, 12, 13, 14, 15, 22, 23)
+                 RS_READ_SCALES(16, 17, 18, 19, 24) "s_waitcnt lgkmcnt(0)"
+                 : RS_8_OUT(p), RS_8_OUT(q), "=&v"(scale[0]), "=&v"(scale[1]), "=&v"(scale[2]), "=&v"(scale[3])
+                 : "v"(p_base + rp.at[0]), "v"(p_base + rp.at[1]), "v"(q_base + rq.at[0]), "v"(q_base + rq.at[1]),
+                   "v"(scales)
+                 : "memory");
+#endif
+}
+
+__device__ __forceinline__ void read_q8(const Reader8 &r, unsigned base, Operands8 &q) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile(RS_READ_8(0, 1, 2, 3, 4, 5, 6, 7, 8, 9) "s_waitcnt lgkmcnt(0)"
+                 : RS_8_OUT(q)
+                 : "v"(base + r.at[0]), "v"(base + r.at[1])
+                 : "memory");
+#endif
+}
+
+__device__ __forceinline__ void read_scales(unsigned scales, float (&scale)[4]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile(RS_READ_SCALES(0, 1, 2, 3, 4) "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(scale[0]), "=&v"(scale[1]), "=&v"(scale[2]), "=&v"(scale[3])
+                 : "v"(scales)
+                 : "memory");
+#endif
+}
+
+template <class OUT>
+__global__ __launch_bounds__(kWideThreads) void wide_fp8_kernel(const ProductWork<fp8, OUT> w) {
+    __shared__ __align__(1024) char ring[kWideLds + 3 * kScaleBytes];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int group = wave >> 2, p_wave = (wave & 3) * 64;
+    const int num_rows = static_cast<int>(w.num_rows), p_tiles = (w.pn + kWide - 1) / kWide;
+    const WideTile t = wide_rows_tile(w.offsets, w.experts, num_rows, kWide, p_tiles, w.clear, blockIdx.x);
+    if (t.expert < 0) return;
+    const int q0 = t.q * kWide, p0 = t.p * kWide;
+    OUT *out = w.out;
+    if (t.expert == w.experts) {
+        clear_tile(out, w.out_stride, w.pn, RowTile{t.expert, t.q, t.rows}, kWide, num_rows, p0, kWide);
+        return;
+    }
+    const int q_rows = t.rows.hi - t.rows.lo, c_n = w.cn;
+    if (q0 >= q_rows || p0 >= w.pn) return;
+    const fp8 *q = w.q + static_cast<size_t>(t.rows.lo) * w.q_stride;
+    const fp8 *p = w.p + static_cast<size_t>(t.expert) * w.p_expert;
+    out += static_cast<size_t>(t.rows.lo) * w.out_stride;
+    const int left = q_rows - q0 < kWide ? q_rows - q0 : kWide;
+    const int height = (left + 63) / 64 * 32, q_wave = group * height;
+
+    constexpr int kStep = kStageBytes;
+    static_assert(kStep == kScaleBlock);
+    const int stages = (c_n + kStep - 1) / kStep;
+    f32x4 acc[4][8];
+#pragma unroll
+    for (auto &a : acc) {
+#pragma unroll
+        for (auto &b : a) b = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    Feeder<fp8, false, false> f0, f1;
+    Feeder<fp8, false, true> fp;
+    f0.set(q, w.q_stride, q_rows, c_n, q0, 0, height, wave, lane);
+    f1.set(q, w.q_stride, q_rows, c_n, q0, 1, height, wave, lane);
+    fp.set(p, w.p_stride, w.pn, c_n, p0, 0, 0, wave, lane);
+    Reader8 rq, rp;
+    rq.set(group * 64, lane);
+    rp.set(p_wave, lane);
+    const unsigned lds = lds_address(ring);
+    const bool works = q0 + q_wave < q_rows && p0 + p_wave < w.pn;
+
+    // Scales: wave k brings those of 64 rows, k of 4, a row a lane.
+    const float *scale_base = uniform(w.q_scales + t.rows.lo + q0);
+    const int scale_row = (wave & 3) * 64 + lane;
+    const unsigned scale_offset = 4u * static_cast<unsigned>(scale_row < left ? scale_row : left - 1);
+    const auto load_scales = [&](int place) __attribute__((always_inline)) {
+        const auto from = __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(scale_base), 0, 0x7FFFFFFF, 0x00020000);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr)(ring + kWideLds + place * kScaleBytes + wave * 256), 4,
+                                                 static_cast<int>(scale_offset), 0, 0, 0);
+        scale_base += w.num_rows;
+    };
+    // Of the matrix: one for the wave's 64 columns and a stage.
+    const int p_block = p0 + p_wave < w.pn ? (p0 + p_wave) / kScaleBlock : 0;
+    const size_t p_blocks = (static_cast<size_t>(w.pn) + kScaleBlock - 1) / kScaleBlock;
+    const auto *p_scales = (const __attribute__((address_space(4))) float *)uniform(
+        w.p_scales + (static_cast<size_t>(t.expert) * p_blocks + p_block) * stages);
+
+    // Seven loads a wave: p, the first rows and the scales of stage s; two: the others.
+    const auto load0 = [&](int s, char *to, int place) __attribute__((always_inline)) {
+        load_scales(place);
+        fp.load(to, wave, lane, c_n - s * kStep);
+        f0.load(to + kWideOperand, wave, lane, c_n - s * kStep);
+    };
+    const auto issue0 = [&](int s) __attribute__((always_inline)) {
+        if (s < stages) load0(s, ring + s % 2 * kWideStage, s % 2);
+    };
+    const auto issue1 = [&](int s) __attribute__((always_inline)) {
+        if (s < stages) f1.load(ring + s % 2 * kWideStage + kWideOperand * 3 / 2, wave, lane, c_n - s * kStep);
+    };
+    const auto arrived0 = [&](int s) __attribute__((always_inline)) {
+        if (s + 1 < stages) {
+            asm volatile("s_waitcnt vmcnt(9)" ::: "memory");
+        } else if (s < stages) {
+            asm volatile("s_waitcnt vmcnt(2)" ::: "memory");
+        }
+    };
+    const auto arrived1 = [&](int s) __attribute__((always_inline)) {
+        if (s + 1 < stages) {
+            asm volatile("s_waitcnt vmcnt(9)" ::: "memory");
+        } else {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+    };
+    const auto barrier = []() __attribute__((always_inline)) {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    Operands8 op, oq;
+    float scale[4], p_scale = p_scales[0];
+    const auto multiply = [&](auto half) __attribute__((always_inline)) {
+        constexpr int kHalf = decltype(half)::value;
+        f32x4 part[2][4];
+        const auto block = [&](auto j) __attribute__((always_inline)) {
+            constexpr int J = decltype(j)::value;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) part[J & 1][i] = mma16_fp8(op.f[i][0], op.f[i][1], oq.f[J][0], oq.f[J][1]);
+        };
+        const auto add = [&](auto j) __attribute__((always_inline)) {
+            constexpr int J = decltype(j)::value;
+            const float both = scale[J] * p_scale;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    acc[i][4 * kHalf + J][r] = __builtin_fmaf(part[J & 1][i][r], both, acc[i][4 * kHalf + J][r]);
+                }
+            }
+        };
+        constexpr std::integral_constant<int, 0> k0{};
+        constexpr std::integral_constant<int, 1> k1{};
+        constexpr std::integral_constant<int, 2> k2{};
+        constexpr std::integral_constant<int, 3> k3{};
+        __builtin_amdgcn_s_setprio(1);
+        const bool whole = height >= 64 * kHalf + 64;
+        block(k0), block(k1), add(k0);
+        if (whole) block(k2);
+        add(k1);
+        if (whole) block(k3), add(k2), add(k3);
+        __builtin_amdgcn_s_setprio(0);
+    };
+    const unsigned scales_at = lds + kWideLds + static_cast<unsigned>(q_wave + (lane & 15)) * 4;
+    // Slots as in wide_product_kernel.
+    if (height > 64) {
+        issue0(0);
+        issue1(0);
+        issue0(1);
+        issue1(1);
+        arrived1(0);
+        barrier();
+        if (group == 1) barrier();
+        for (int s = 0; s < stages; ++s) {
+            const unsigned at = lds + static_cast<unsigned>(s % 2) * kWideStage;
+            const unsigned of = scales_at + static_cast<unsigned>(s % 2) * kScaleBytes;
+            float others[4];
+            if (works) read_pq8(rq, rp, at + kWideOperand, at, of, oq, op, scale);
+            // The scales of the other rows, before the next ones take their place.
+            if (works) read_scales(of + 256, others);
+            if (s > 0) issue1(s + 1);
+            if (group == 1) arrived1(s);
+            barrier();
+            if (works) multiply(std::integral_constant<int, 0>{});
+            if (group == 0) arrived1(s);
+            barrier();
+            if (works) read_q8(rq, at + kWideOperand * 3 / 2, oq);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) scale[j] = others[j];
+            issue0(s + 2);
+            if (group == 1) arrived0(s + 1);
+            barrier();
+            if (works) multiply(std::integral_constant<int, 1>{});
+            p_scale = p_scales[s + 1 < stages ? s + 1 : s];
+            if (group == 0) arrived0(s + 1);
+            if (s + 1 < stages || group == 0) barrier();
+        }
+    } else {
+        const auto issue = [&](int s, unsigned place) __attribute__((always_inline)) {
+            if (s < stages) load0(s, ring + place * kFlatStage, static_cast<int>(place));
+        };
+        const auto arrived = [&](int s) __attribute__((always_inline)) {
+            if (s + 1 < stages) {
+                asm volatile("s_waitcnt vmcnt(7)" ::: "memory");
+            } else {
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            }
+        };
+        issue(0, 0);
+        issue(1, 1);
+        arrived(0);
+        if (group == 1) issue(2, 2);
+        barrier();
+        if (group == 1) barrier();
+        unsigned place = 0;
+        for (int s = 0; s < stages; ++s) {
+            const unsigned at = lds + place * kFlatStage, before = place == 0 ? 2 : place - 1;
+            if (works) read_pq8(rq, rp, at + kWideOperand, at, scales_at + place * kScaleBytes, oq, op, scale);
+            if (group == 0) {
+                issue(s + 2, before);
+            } else {
+                arrived(s + 1);
+            }
+            barrier();
+            if (group == 1) issue(s + 3, place);
+            if (works) multiply(std::integral_constant<int, 0>{});
+            p_scale = p_scales[s + 1 < stages ? s + 1 : s];
+            if (group == 0) arrived(s + 1);
+            if (s + 1 < stages || group == 0) barrier();
+            place = place == 2 ? 0 : place + 1;
+        }
+    }
+
+    if constexpr (sizeof(OUT) == 2) {
+        char *mine = ring + wave * 16384;
+        typedef OUT t4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int row = 16 * j + (lane & 15);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                t4 v;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = static_cast<OUT>(acc[i][j][r]);
+                const int chunk = 2 * i + (lane >> 5);
+                *reinterpret_cast<t4 *>(mine + row * 128 + ((chunk ^ (row & 7)) << 4) + (lane >> 4 & 1) * 8) = v;
+            }
+        }
+        rows_from_lds(mine, out, w.out_stride, height, q0 + q_wave, q_rows, p0 + p_wave, w.pn, lane);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int row = 16 * j + (lane & 15), qi = q0 + q_wave + row;
+            if (row >= height || qi >= q_rows) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int pi = p0 + p_wave + 16 * i + 4 * (lane >> 4);
+                float f[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) f[r] = acc[i][j][r];
+                if (pi < w.pn) store_some<OUT, 4>(out + static_cast<size_t>(qi) * w.out_stride + pi, w.pn - pi, f);
             }
         }
     }

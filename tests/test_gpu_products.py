@@ -221,7 +221,7 @@ def test_products_far_offsets():
 # 8 bits
 # ---------------------------------------------------------------------------
 FP8_SHAPES = [(1, 1, 1, 1), (5, 2, 130, 16), (20, 3, 40, 127), (130, 4, 129, 300), (300, 5, 264, 512), (77, 2, 33, 1041),
-              (9, 40, 256, 384), (600, 2, 384, 256)]
+              (9, 40, 256, 384), (600, 2, 384, 256), (1500, 4, 264, 208), (900, 3, 520, 1040), (700, 3, 136, 16)]
 
 
 def eight_bits(gen, n, E, N, K):
@@ -657,8 +657,8 @@ def test_kernel_timing():
     rs.prof_reset()
 
 
-@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
-@pytest.mark.parametrize("N,K", [(264, 200), (520, 8), (136, 1000)])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16", "8 bits"])
+@pytest.mark.parametrize("N,K", [(264, 208), (520, 8), (136, 1008)])
 def test_products_tiles_of_every_height(N, K, dtype):
     """Experts whose last tile has any number of rows, among many stages and one."""
     note(f"heights {dtype} N={N} K={K}")
@@ -666,6 +666,15 @@ def test_products_tiles_of_every_height(N, K, dtype):
     E, n, gen = len(counts), sum(counts) + 70, generator(N)
     o = torch.tensor([40] + counts, device="cuda").cumsum(0).to(torch.int32)
     s = po.spans(o, E, n)
+    if dtype == "8 bits":
+        (q, qs), (w, ws) = eight_bits(gen, n, E, N, K)
+        x, m, none = po.expand(q, qs), po.expand_weights(w, ws), torch.zeros(n, N, device="cuda")
+        exact, size = po.product(x, s, m, none)
+        lost = po.fp8_lost(x, s, m, none)
+        for out in DTYPES:
+            bound = po.product_bound(exact, size, K // 32 + 8, out) + lost
+            close(rs.expert_products_fp8(q, qs, o, w, ws, DTYPES[out]), exact, bound, out)
+        return
     x, w, g = normal(gen, (n, K), dtype), normal(gen, (E, N, K), dtype, K ** -0.5), normal(gen, (n, N), dtype)
     exact, size = po.product(x, s, w, torch.zeros(n, N, device="cuda"))
     close(rs.expert_products(x, o, w), exact, po.product_bound(exact, size, K, dtype), "product")
