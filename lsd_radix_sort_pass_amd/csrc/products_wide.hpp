@@ -489,66 +489,67 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
             __builtin_amdgcn_sched_barrier(0);
         };
         Operands op, oq;
-        // Multiplies rows 64 HALF .. of the group with the operands read last.
-        const auto multiply = [&](int s, auto half) __attribute__((always_inline)) {
-            constexpr int kHalf = decltype(half)::value;
-            const auto steps = [&](auto from, auto blocks) __attribute__((always_inline)) {
+        // Multiplies rows 64 HALF .. of the group, 32 times BLOCKS, with the operands read
+        // last.
+        const auto multiply = [&](int s, auto half, auto blocks) __attribute__((always_inline)) {
+            constexpr int kHalf = decltype(half)::value, kBlocks = decltype(blocks)::value;
+            const auto step = [&](int k) __attribute__((always_inline)) {
 #pragma unroll
-                for (int k = from; k < from + 2; ++k) {
+                for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                        for (int j = 0; j < blocks; ++j) {
-                            acc[i][2 * kHalf + j] = mma32<T>(op.f[i][k], oq.f[j][k], acc[i][2 * kHalf + j]);
-                        }
+                    for (int j = 0; j < kBlocks; ++j) {
+                        acc[i][2 * kHalf + j] = mma32<T>(op.f[i][k], oq.f[j][k], acc[i][2 * kHalf + j]);
                     }
                 }
             };
-            const bool second = c_n - s * kStep > kStep / 2;  // (zeros otherwise)
             __builtin_amdgcn_s_setprio(1);
-            if (height >= 64 * kHalf + 64) {
-                steps(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{});
-                if (second) steps(std::integral_constant<int, 2>{}, std::integral_constant<int, 2>{});
-            } else {
-                steps(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{});
-                if (second) steps(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{});
-            }
+            step(0), step(1);
+            if (c_n - s * kStep > kStep / 2) step(2), step(3);  // (zeros otherwise)
             __builtin_amdgcn_s_setprio(0);
         };
+        constexpr std::integral_constant<int, 0> k0{};
+        constexpr std::integral_constant<int, 1> k1{};
+        constexpr std::integral_constant<int, 2> k2{};
         // Slots: group 0 reads in the even ones and multiplies in the odd ones, group 1
         // the other way round, a slot later.  Group 1 is the last to multiply, and nobody
         // waits for that.
-        if (height > 64) {
-            // What group 0 reads of stage s in slots 4 s and 4 s + 2, group 1 has read at the
-            // end of slots 4 s + 1 and 4 s + 3: from then on stage s + 2 takes its place.
-            // Both groups have waited for it before group 0's slots 4 s + 8 and 4 s + 10.
+        // Tiles of more than 128 rows.  What group 0 reads of stage s in slots 4 s and
+        // 4 s + 2, group 1 has read at the end of slots 4 s + 1 and 4 s + 3: from then on
+        // stage s + 2 takes its place.  Both groups have waited for it before group 0's slots
+        // 4 s + 8 and 4 s + 10.
+        const auto tall = [&](auto others) __attribute__((always_inline)) {
             issue0(0);
             issue1(0);
             issue0(1);
-            issue1(1);
-            arrived1(0);
+            if (stages > 1) {
+                asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+            } else {
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            }
             barrier();
             if (group == 1) barrier();
+#pragma nounroll
             for (int s = 0; s < stages; ++s) {
                 const unsigned at = lds + static_cast<unsigned>(s % 2) * kWideStage;
                 if (works) read_pq<Q_ACROSS, P_ACROSS>(rq, rp, at + kWideOperand, at, oq, op);
-                if (s > 0) issue1(s + 1);
+                issue1(s + 1);
                 if (group == 1) arrived1(s);
                 barrier();
-                if (works) multiply(s, std::integral_constant<int, 0>{});
+                if (works) multiply(s, k0, k2);
                 if (group == 0) arrived1(s);
                 barrier();
                 if (works) read_q<Q_ACROSS>(rq, at + kWideOperand * 3 / 2, oq);
                 issue0(s + 2);
                 if (group == 1) arrived0(s + 1);
                 barrier();
-                if (works) multiply(s, std::integral_constant<int, 1>{});
+                if (works) multiply(s, k1, others);
                 if (group == 0) arrived0(s + 1);
                 if (s + 1 < stages || group == 0) barrier();
             }
-        } else {
-            // Group 0 reads stage s in slot 2 s, group 1 in the next; from slot 2 s + 2 on
-            // stage s + 3 takes its place.  It is read first in slot 2 s + 6.
+        };
+        // The others.  Group 0 reads stage s in slot 2 s, group 1 in the next; from slot
+        // 2 s + 2 on stage s + 3 takes its place.  It is read first in slot 2 s + 6.
+        const auto flat = [&](auto rows) __attribute__((always_inline)) {
             const auto issue = [&](int s, unsigned place) __attribute__((always_inline)) {
                 if (s < stages) load0(s, ring + place * kFlatStage);
             };
@@ -566,6 +567,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
             barrier();
             if (group == 1) barrier();
             unsigned place = 0;
+#pragma nounroll
             for (int s = 0; s < stages; ++s) {
                 const unsigned at = lds + place * kFlatStage, before = place == 0 ? 2 : place - 1;
                 if (works) read_pq<Q_ACROSS, P_ACROSS>(rq, rp, at + kWideOperand, at, oq, op);
@@ -576,11 +578,20 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
                 }
                 barrier();
                 if (group == 1) issue(s + 3, place);
-                if (works) multiply(s, std::integral_constant<int, 0>{});
+                if (works) multiply(s, k0, rows);
                 if (group == 0) arrived(s + 1);
                 if (s + 1 < stages || group == 0) barrier();
                 place = place == 2 ? 0 : place + 1;
             }
+        };
+        if (height == 128) {
+            tall(k2);
+        } else if (height == 96) {
+            tall(k1);
+        } else if (height == 64) {
+            flat(k2);
+        } else {
+            flat(k1);
         }
     }
 
@@ -613,7 +624,10 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
 // matrix, and are added to the sums in float32: 16 x 16 of them at a time, while the next
 // are multiplied.  The scales of the rows come with the stage.
 // ---------------------------------------------------------------------------
-constexpr int kScaleBytes = 2048;  // of a stage: 256 rows, and room for as many loads that nobody reads
+// Scales of a stage: of the first 64 rows of both groups, then of their others, each
+// with room for what the six waves bring whose loads nobody reads (all waves load as
+// often, as they count their own).
+constexpr int kScaleBytes = 4096;
 
 struct Reader8 {
     unsigned at[2];
@@ -655,20 +669,12 @@ __device__ __forceinline__ void read_pq8(const Reader8 &rq, const Reader8 &rp, u
 #endif
 }
 
-__device__ __forceinline__ void read_q8(const Reader8 &r, unsigned base, Operands8 &q) {
+__device__ __forceinline__ void read_q8(const Reader8 &r, unsigned base, unsigned scales, Operands8 &q,
+                                        float (&scale)[4]) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    asm volatile(RS_READ_8(0, 1, 2, 3, 4, 5, 6, 7, 8, 9) "s_waitcnt lgkmcnt(0)"
-                 : RS_8_OUT(q)
-                 : "v"(base + r.at[0]), "v"(base + r.at[1])
-                 : "memory");
-#endif
-}
-
-__device__ __forceinline__ void read_scales(unsigned scales, float (&scale)[4]) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    asm volatile(RS_READ_SCALES(0, 1, 2, 3, 4) "s_waitcnt lgkmcnt(0)"
-                 : "=&v"(scale[0]), "=&v"(scale[1]), "=&v"(scale[2]), "=&v"(scale[3])
-                 : "v"(scales)
+    asm volatile(RS_READ_8(0, 1, 2, 3, 4, 5, 6, 7, 12, 13) RS_READ_SCALES(8, 9, 10, 11, 14) "s_waitcnt lgkmcnt(0)"
+                 : RS_8_OUT(q), "=&v"(scale[0]), "=&v"(scale[1]), "=&v"(scale[2]), "=&v"(scale[3])
+                 : "v"(base + r.at[0]), "v"(base + r.at[1]), "v"(scales)
                  : "memory");
 #endif
 }
@@ -715,15 +721,14 @@ __global__ __launch_bounds__(kWideThreads) void wide_fp8_kernel(const ProductWor
     const unsigned lds = lds_address(ring);
     const bool works = q0 + q_wave < q_rows && p0 + p_wave < w.pn;
 
-    // Scales: wave k brings those of 64 rows, k of 4, a row a lane.
-    const float *scale_base = uniform(w.q_scales + t.rows.lo + q0);
-    const int scale_row = (wave & 3) * 64 + lane;
-    const unsigned scale_offset = 4u * static_cast<unsigned>(scale_row < left ? scale_row : left - 1);
-    const auto load_scales = [&](int place) __attribute__((always_inline)) {
-        const auto from = __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(scale_base), 0, 0x7FFFFFFF, 0x00020000);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr)(ring + kWideLds + place * kScaleBytes + wave * 256), 4,
-                                                 static_cast<int>(scale_offset), 0, 0, 0);
-        scale_base += w.num_rows;
+    // Scales: waves 0 and 1 bring those of a group's 64 rows, a row a lane.
+    const float *scale_base0 = uniform(w.q_scales + t.rows.lo + q0), *scale_base1 = scale_base0;
+    const auto load_scales = [&](const float *&base, int first, int to) __attribute__((always_inline)) {
+        const int row = (wave & 1) * height + first + lane;
+        const auto from = __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(base), 0, 0x7FFFFFFF, 0x00020000);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr)(ring + kWideLds + to + wave * 256), 4,
+                                                 4 * (row < left ? row : left - 1), 0, 0, 0);
+        base += w.num_rows;
     };
     // Of the matrix: one for the wave's 64 columns and a stage.
     const int p_block = p0 + p_wave < w.pn ? (p0 + p_wave) / kScaleBlock : 0;
@@ -731,9 +736,9 @@ __global__ __launch_bounds__(kWideThreads) void wide_fp8_kernel(const ProductWor
     const auto *p_scales = (const __attribute__((address_space(4))) float *)uniform(
         w.p_scales + (static_cast<size_t>(t.expert) * p_blocks + p_block) * stages);
 
-    // Seven loads a wave: p, the first rows and the scales of stage s; two: the others.
+    // Seven loads a wave: p, the first rows and their scales of stage s; three: the others.
     const auto load0 = [&](int s, char *to, int place) __attribute__((always_inline)) {
-        load_scales(place);
+        load_scales(scale_base0, 0, place * kScaleBytes);
         fp.load(to, wave, lane, c_n - s * kStep);
         f0.load(to + kWideOperand, wave, lane, c_n - s * kStep);
     };
@@ -741,18 +746,20 @@ __global__ __launch_bounds__(kWideThreads) void wide_fp8_kernel(const ProductWor
         if (s < stages) load0(s, ring + s % 2 * kWideStage, s % 2);
     };
     const auto issue1 = [&](int s) __attribute__((always_inline)) {
-        if (s < stages) f1.load(ring + s % 2 * kWideStage + kWideOperand * 3 / 2, wave, lane, c_n - s * kStep);
+        if (s >= stages) return;
+        load_scales(scale_base1, 64, s % 2 * kScaleBytes + kScaleBytes / 2);
+        f1.load(ring + s % 2 * kWideStage + kWideOperand * 3 / 2, wave, lane, c_n - s * kStep);
     };
     const auto arrived0 = [&](int s) __attribute__((always_inline)) {
         if (s + 1 < stages) {
-            asm volatile("s_waitcnt vmcnt(9)" ::: "memory");
+            asm volatile("s_waitcnt vmcnt(10)" ::: "memory");
         } else if (s < stages) {
-            asm volatile("s_waitcnt vmcnt(2)" ::: "memory");
+            asm volatile("s_waitcnt vmcnt(3)" ::: "memory");
         }
     };
     const auto arrived1 = [&](int s) __attribute__((always_inline)) {
         if (s + 1 < stages) {
-            asm volatile("s_waitcnt vmcnt(9)" ::: "memory");
+            asm volatile("s_waitcnt vmcnt(10)" ::: "memory");
         } else {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         }
@@ -764,72 +771,92 @@ __global__ __launch_bounds__(kWideThreads) void wide_fp8_kernel(const ProductWor
     };
     Operands8 op, oq;
     float scale[4], p_scale = p_scales[0];
-    const auto multiply = [&](auto half) __attribute__((always_inline)) {
-        constexpr int kHalf = decltype(half)::value;
-        f32x4 part[2][4];
-        const auto block = [&](auto j) __attribute__((always_inline)) {
-            constexpr int J = decltype(j)::value;
+    f32x4 part[2][4] = {};
+    float last_scale = 0.0f;
+    const auto block = [&](auto j) __attribute__((always_inline)) {
+        constexpr int J = decltype(j)::value;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) part[J & 1][i] = mma16_fp8(op.f[i][0], op.f[i][1], oq.f[J][0], oq.f[J][1]);
-        };
-        const auto add = [&](auto j) __attribute__((always_inline)) {
-            constexpr int J = decltype(j)::value;
-            const float both = scale[J] * p_scale;
+        for (int i = 0; i < 4; ++i) part[J & 1][i] = mma16_fp8(op.f[i][0], op.f[i][1], oq.f[J][0], oq.f[J][1]);
+    };
+    const auto add = [&](auto half, auto j, float both) __attribute__((always_inline)) {
+        constexpr int kHalf = decltype(half)::value, J = decltype(j)::value;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    acc[i][4 * kHalf + J][r] = __builtin_fmaf(part[J & 1][i][r], both, acc[i][4 * kHalf + J][r]);
-                }
+            for (int r = 0; r < 4; ++r) {
+                acc[i][4 * kHalf + J][r] = __builtin_fmaf(part[J & 1][i][r], both, acc[i][4 * kHalf + J][r]);
             }
-        };
-        constexpr std::integral_constant<int, 0> k0{};
-        constexpr std::integral_constant<int, 1> k1{};
-        constexpr std::integral_constant<int, 2> k2{};
-        constexpr std::integral_constant<int, 3> k3{};
+        }
+    };
+    constexpr std::integral_constant<int, 0> k0{};
+    constexpr std::integral_constant<int, 1> k1{};
+    constexpr std::integral_constant<int, 2> k2{};
+    constexpr std::integral_constant<int, 3> k3{};
+    // Multiplies rows 64 HALF .. of the group, 16 times BLOCKS (2 or 4), with the
+    // operands read last, and adds all but the last 16 rows' results, which finish() does
+    // beside the other group's products.
+    const auto multiply = [&](auto half, auto blocks) __attribute__((always_inline)) {
         __builtin_amdgcn_s_setprio(1);
-        const bool whole = height >= 64 * kHalf + 64;
-        block(k0), block(k1), add(k0);
-        if (whole) block(k2);
-        add(k1);
-        if (whole) block(k3), add(k2), add(k3);
+        block(k0), block(k1), add(half, k0, scale[0] * p_scale);
+        if constexpr (decltype(blocks)::value == 4) {
+            block(k2), add(half, k1, scale[1] * p_scale), block(k3), add(half, k2, scale[2] * p_scale);
+        }
+        last_scale = scale[decltype(blocks)::value - 1] * p_scale;
+        // An instruction for the matrix unit, then four for the others.
+        __builtin_amdgcn_sched_group_barrier(0x8, 5, 0);
+#pragma unroll
+        for (int i = 0; i < 4 * decltype(blocks)::value - 5; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        }
         __builtin_amdgcn_s_setprio(0);
     };
-    const unsigned scales_at = lds + kWideLds + static_cast<unsigned>(q_wave + (lane & 15)) * 4;
+    const auto finish = [&](auto half, auto blocks) __attribute__((always_inline)) {
+        add(half, std::integral_constant<int, decltype(blocks)::value - 1>{}, last_scale);
+    };
+    constexpr std::integral_constant<int, 4> k4{};
+    const unsigned scales_at = lds + kWideLds + static_cast<unsigned>(group * 64 + (lane & 15)) * 4;
     // Slots as in wide_product_kernel.
-    if (height > 64) {
+    const auto tall = [&](auto others) __attribute__((always_inline)) {
         issue0(0);
         issue1(0);
         issue0(1);
-        issue1(1);
-        arrived1(0);
+        if (stages > 1) {
+            asm volatile("s_waitcnt vmcnt(7)" ::: "memory");
+        } else {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
         barrier();
         if (group == 1) barrier();
+#pragma nounroll
         for (int s = 0; s < stages; ++s) {
             const unsigned at = lds + static_cast<unsigned>(s % 2) * kWideStage;
             const unsigned of = scales_at + static_cast<unsigned>(s % 2) * kScaleBytes;
-            float others[4];
-            if (works) read_pq8(rq, rp, at + kWideOperand, at, of, oq, op, scale);
-            // The scales of the other rows, before the next ones take their place.
-            if (works) read_scales(of + 256, others);
-            if (s > 0) issue1(s + 1);
+            if (works) {
+                read_pq8(rq, rp, at + kWideOperand, at, of, oq, op, scale);
+                finish(k1, others);  // of the stage before
+            }
+            issue1(s + 1);
             if (group == 1) arrived1(s);
             barrier();
-            if (works) multiply(std::integral_constant<int, 0>{});
+            if (works) multiply(k0, k4);
             if (group == 0) arrived1(s);
             barrier();
-            if (works) read_q8(rq, at + kWideOperand * 3 / 2, oq);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) scale[j] = others[j];
+            if (works) {
+                read_q8(rq, at + kWideOperand * 3 / 2, of + kScaleBytes / 2, oq, scale);
+                finish(k0, k4);
+            }
             issue0(s + 2);
             if (group == 1) arrived0(s + 1);
             barrier();
-            if (works) multiply(std::integral_constant<int, 1>{});
+            if (works) multiply(k1, others);
             p_scale = p_scales[s + 1 < stages ? s + 1 : s];
             if (group == 0) arrived0(s + 1);
             if (s + 1 < stages || group == 0) barrier();
         }
-    } else {
+        if (works) finish(k1, others);
+    };
+    const auto flat = [&](auto rows) __attribute__((always_inline)) {
         const auto issue = [&](int s, unsigned place) __attribute__((always_inline)) {
             if (s < stages) load0(s, ring + place * kFlatStage, static_cast<int>(place));
         };
@@ -847,9 +874,13 @@ __global__ __launch_bounds__(kWideThreads) void wide_fp8_kernel(const ProductWor
         barrier();
         if (group == 1) barrier();
         unsigned place = 0;
+#pragma nounroll
         for (int s = 0; s < stages; ++s) {
             const unsigned at = lds + place * kFlatStage, before = place == 0 ? 2 : place - 1;
-            if (works) read_pq8(rq, rp, at + kWideOperand, at, scales_at + place * kScaleBytes, oq, op, scale);
+            if (works) {
+                read_pq8(rq, rp, at + kWideOperand, at, scales_at + place * kScaleBytes, oq, op, scale);
+                finish(k0, rows);
+            }
             if (group == 0) {
                 issue(s + 2, before);
             } else {
@@ -857,12 +888,22 @@ __global__ __launch_bounds__(kWideThreads) void wide_fp8_kernel(const ProductWor
             }
             barrier();
             if (group == 1) issue(s + 3, place);
-            if (works) multiply(std::integral_constant<int, 0>{});
+            if (works) multiply(k0, rows);
             p_scale = p_scales[s + 1 < stages ? s + 1 : s];
             if (group == 0) arrived(s + 1);
             if (s + 1 < stages || group == 0) barrier();
             place = place == 2 ? 0 : place + 1;
         }
+        if (works) finish(k0, rows);
+    };
+    if (height == 128) {
+        tall(k4);
+    } else if (height == 96) {
+        tall(k2);
+    } else if (height == 64) {
+        flat(k4);
+    } else {
+        flat(k2);
     }
 
     if constexpr (sizeof(OUT) == 2) {
