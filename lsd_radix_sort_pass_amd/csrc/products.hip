@@ -5,6 +5,7 @@
 #include "gates.hpp"
 #include "launch.hpp"
 #include "products.hpp"
+#include "products_few.hpp"
 #include "products_wide.hpp"
 
 // Named here, as the host's pass does not emit all of those that only calls within
@@ -62,6 +63,30 @@ bool wide_pays(const rs::ProductWork<T, OUT> &w, bool ragged_c) {
     return rows >= 96 && w.pn > 128 && (!ragged_c || w.qn > 128);
 }
 
+// Rows of an expert up to which few_rows_kernel is faster than 128 x 128 tiles.
+constexpr size_t kFewRows = 64;
+
+template <class T, class OUT>
+bool few_pays(const rs::ProductWork<T, OUT> &w) {
+    return w.num_rows <= kFewRows * static_cast<size_t>(w.experts) && w.cn >= static_cast<int>(16 / sizeof(T));
+}
+
+template <class T, class OUT>
+bool launch_few(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
+    const size_t each = w.num_rows / static_cast<size_t>(w.experts);
+    const auto go = [&](auto kernel, int strips, int rows) {
+        const size_t height = static_cast<size_t>(16 * rows);
+        const size_t q_tiles = w.num_rows / height + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1;
+        const size_t p_tiles = (static_cast<size_t>(w.pn) + 16 * strips - 1) / static_cast<size_t>(16 * strips);
+        return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] {
+            run_kernel(kernel, static_cast<unsigned>(q_tiles * p_tiles), rs::kFewThreads, stream, w);
+        });
+    };
+    if (each <= 12) return go(rs::few_rows_kernel<T, OUT, 2, 1>, 2, 1);
+    if (each <= 28) return go(rs::few_rows_kernel<T, OUT, 2, 2>, 2, 2);
+    return go(rs::few_rows_kernel<T, OUT, 2, 4>, 2, 4);
+}
+
 // Whether the wide kernel can take an operand: its 16-byte chunks are aligned, a
 // tile spans less than 2^31 bytes, and a row has a chunk (across: whole ones).
 bool feeds(const void *p, size_t stride, size_t expert, int width, bool across, size_t elem) {
@@ -91,6 +116,9 @@ bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
                 return go(rs::wide_product_kernel<T, RAGGED_C, Q_ACROSS, P_ACROSS>);
             }
         }
+    }
+    if constexpr (!RAGGED_C && !Q_ACROSS && !P_ACROSS) {
+        if (few_pays(w)) return launch_few(w, stream);
     }
     const size_t p_tiles = (static_cast<size_t>(w.pn) + 127) / 128;
     size_t q_tiles;
