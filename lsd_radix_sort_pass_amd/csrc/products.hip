@@ -1,6 +1,7 @@
 // products.hip -- C ABI of the experts' own work (matrix products of sorted
 // rows, rows in 8 bits, gated rows): argument checks and launches.
 #include <algorithm>
+#include <cmath>
 
 #include "gates.hpp"
 #include "launch.hpp"
@@ -57,35 +58,7 @@ bool addressable(Span s) { return s.lo <= s.hi && s.hi - s.lo < (size_t{1} << 62
 
 size_t align_to(size_t x, size_t by) { return (x + by - 1) / by * by; }
 
-template <class T, class OUT>
-bool wide_pays(const rs::ProductWork<T, OUT> &w, bool ragged_c) {
-    const size_t rows = w.num_rows / static_cast<size_t>(w.experts);
-    return rows >= 96 && w.pn > 128 && (!ragged_c || w.qn > 128);
-}
-
-// Rows of an expert up to which few_rows_kernel is faster than 128 x 128 tiles.
-constexpr size_t kFewRows = 64;
-
-template <class T, class OUT>
-bool few_pays(const rs::ProductWork<T, OUT> &w) {
-    return w.num_rows <= kFewRows * static_cast<size_t>(w.experts) && w.cn >= static_cast<int>(16 / sizeof(T));
-}
-
-template <class T, class OUT>
-bool launch_few(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
-    const size_t each = w.num_rows / static_cast<size_t>(w.experts);
-    const auto go = [&](auto kernel, int strips, int rows) {
-        const size_t height = static_cast<size_t>(16 * rows);
-        const size_t q_tiles = w.num_rows / height + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1;
-        const size_t p_tiles = (static_cast<size_t>(w.pn) + 16 * strips - 1) / static_cast<size_t>(16 * strips);
-        return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] {
-            run_kernel(kernel, static_cast<unsigned>(q_tiles * p_tiles), rs::kFewThreads, stream, w);
-        });
-    };
-    if (each <= 12) return go(rs::few_rows_kernel<T, OUT, 2, 1>, 2, 1);
-    if (each <= 28) return go(rs::few_rows_kernel<T, OUT, 2, 2>, 2, 2);
-    return go(rs::few_rows_kernel<T, OUT, 2, 4>, 2, 4);
-}
+size_t parts(size_t x, size_t by) { return (x + by - 1) / by; }
 
 // Whether the wide kernel can take an operand: its 16-byte chunks are aligned, a
 // tile spans less than 2^31 bytes, and a row has a chunk (across: whole ones).
@@ -95,41 +68,127 @@ bool feeds(const void *p, size_t stride, size_t expert, int width, bool across, 
            width >= static_cast<int>(chunk) && (!across || static_cast<size_t>(width) % chunk == 0);
 }
 
+// ---------------------------------------------------------------------------
+// Which kernel takes a product of rows, by estimates of their times in us (with 4
+// to 6 for the launch and its beginning).  The experts are taken to have equally
+// many rows.
+//
+// Tiles go round the 256 CUs: the wide kernel's stage of 128 bytes of c takes 0.55 us, as
+// long as its loads are on their way, and more for a tile full of rows; but
+// memory gives no more than 6 TB/s.  The kernel for few rows reads weights at 5 to
+// 6 TB/s, and its rows again for each of its strips, at 6.5 TB/s.  Tiles of 128 x 128 take
+// 0.85 us for 128 bytes of c, and 1.5 if two share every CU; in float32 2.6 and 4.5.
+// Measured, in us, wide / few rows / square (bfloat16, rows x experts x out x in):
+// 8 of 64 x 2048 x 2048 24 / 12 / 32, 512 of 64 x 4096 x 4096 346 / 424 / -, 16 of one x
+// 8192 x 8192 75 / 28 / 107, 128 of one 95 / 88 / 101, 256 of one 154 / 172 / 102, 300 of 16
+// x 2048 x 2048 27 / 33 / 33, 512 of 8 x 1024 x 1024 16 / 10 / 18, 2048 of 8 26 / 26 / 19;
+// e4m3 256 of 128 x 2048 x 4096 166 / 143 / 310.
+// ---------------------------------------------------------------------------
+struct Estimate {
+    double rows_each, experts_used, weight_bytes, stages;
+    bool bytes, words;  // operands of 8, of 32 bits
+
+    template <class T, class OUT>
+    explicit Estimate(const rs::ProductWork<T, OUT> &w) : bytes(sizeof(T) == 1), words(sizeof(T) == 4) {
+        const double n = static_cast<double>(w.num_rows), e = static_cast<double>(w.experts);
+        experts_used = std::max(1.0, e * (1.0 - std::exp(-n / e)));  // by rows that choose at random
+        rows_each = n / experts_used;
+        weight_bytes = experts_used * w.pn * w.cn * static_cast<double>(sizeof(T));
+        stages = static_cast<double>(parts(static_cast<size_t>(w.cn) * sizeof(T), 128));
+    }
+    double tiles(double height, double width, double pn) const {
+        return experts_used * std::ceil(rows_each / height) * std::ceil(pn / width);
+    }
+    double wide(double pn) const {
+        const double t = tiles(rs::kWide, rs::kWide, pn);
+        const double stage = 0.55 + (t > 128 ? 1.1 : 0.65) * std::min(1.0, rows_each / rs::kWide);
+        return 6 + std::max(std::ceil(t / 256) * stages * stage, weight_bytes / (bytes ? 5.5e6 : 6e6));
+    }
+    double few(double pn) const {
+        const double weights = weight_bytes / (bytes ? 6e6 : 5.2e6);
+        const double rows = experts_used * rows_each * stages * 128 * std::ceil(pn / 32) / 6.5e6;
+        return 4 + std::max(weights, rows) + 0.25 * std::min(weights, rows);
+    }
+    double square(double pn) const {
+        const double t = tiles(128, 128, pn);
+        return 4 + stages * std::max(words ? 2.6 : 0.85, (words ? 4.5 : 1.5) * (t <= 256 ? 0.0 : std::ceil(t / 512)));
+    }
+};
+
+// Enqueues few_rows_kernel: as few rows as the experts have on average fill the
+// matrix instruction's 16 columns up; two strips a workgroup of four waves where
+// every CU has a workgroup then, or else one strip and more waves for the
+// contraction: one row, 4096 x 4096 bfloat16, 11.8 us with two strips and 4 waves, 8.7 with one
+// and 16; 16 rows, 8192 x 8192, 35 and 39.
+template <class T, class OUT>
+bool launch_few(const rs::ProductWork<T, OUT> &w, const Estimate &e, hipStream_t stream) {
+    const auto with_rows = [&](auto rows) {
+        constexpr int R = decltype(rows)::value;
+        const size_t q_tiles = w.num_rows / (16 * R) + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1;
+        const auto go = [&](auto kernel, int waves, size_t p_tiles) {
+            return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] {
+                run_kernel(kernel, static_cast<unsigned>(q_tiles * p_tiles), 64 * waves, stream, w);
+            });
+        };
+        const size_t strips = parts(static_cast<size_t>(w.pn), 16);
+        const double groups = e.tiles(16 * R, 16, w.pn);
+        if (groups >= 512) return go(rs::few_rows_kernel<T, OUT, 4, 2, R>, 4, parts(strips, 2));
+        constexpr int kWaves = R == 4 ? 8 : 16;  // (16 would have registers for a step at a time)
+        return go(rs::few_rows_kernel<T, OUT, kWaves, 1, R>, kWaves, strips);
+    };
+    if (e.rows_each <= 12) return with_rows(IntC<1>{});
+    if (e.rows_each <= 28) return with_rows(IntC<2>{});
+    return with_rows(IntC<4>{});
+}
+
 // Enqueues the product of w, whose results are q by p (RAGGED_C: of each expert).
 template <class T, class OUT, bool RAGGED_C, bool Q_ACROSS, bool P_ACROSS>
 bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
+    bool wide = false;
     if constexpr (sizeof(T) <= 2) {
-        const size_t p_tiles = (static_cast<size_t>(w.pn) + rs::kWide - 1) / rs::kWide;
+        const size_t p_tiles = parts(static_cast<size_t>(w.pn), rs::kWide);
         const size_t tiles = RAGGED_C
-            ? align_to((static_cast<size_t>(w.qn) + rs::kWide - 1) / rs::kWide * p_tiles, rs::kXcds) * static_cast<size_t>(w.experts)
-            : align_to((w.num_rows / rs::kWide + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1) * p_tiles, rs::kXcds);
-        if (tiles <= (size_t{1} << 30) && feeds(w.q, w.q_stride, 0, Q_ACROSS ? w.qn : w.cn, Q_ACROSS, sizeof(T)) &&
-            feeds(w.p, w.p_stride, w.p_expert, P_ACROSS ? w.pn : w.cn, P_ACROSS, sizeof(T)) && wide_pays(w, RAGGED_C)) {
-            const auto go = [&](auto kernel) {
-                return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] {
-                    run_kernel(kernel, static_cast<unsigned>(tiles), rs::kWideThreads, stream, w);
-                });
-            };
-            if constexpr (sizeof(T) == 1) {
-                return go(rs::wide_fp8_kernel<OUT>);
-            } else {
-                return go(rs::wide_product_kernel<T, RAGGED_C, Q_ACROSS, P_ACROSS>);
+            ? align_to(parts(static_cast<size_t>(w.qn), rs::kWide) * p_tiles, rs::kXcds) * static_cast<size_t>(w.experts)
+            : align_to((w.num_rows / rs::kWide + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1) * p_tiles,
+                       rs::kXcds);
+        wide = tiles <= (size_t{1} << 30) && feeds(w.q, w.q_stride, 0, Q_ACROSS ? w.qn : w.cn, Q_ACROSS, sizeof(T)) &&
+               feeds(w.p, w.p_stride, w.p_expert, P_ACROSS ? w.pn : w.cn, P_ACROSS, sizeof(T));
+        const auto go = [&](auto kernel) {
+            return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] {
+                run_kernel(kernel, static_cast<unsigned>(tiles), rs::kWideThreads, stream, w);
+            });
+        };
+        if constexpr (RAGGED_C) {
+            // Below a stage of rows, what counts is that results are written from many CUs.
+            if (wide && w.num_rows >= 64 * static_cast<size_t>(w.experts) && w.pn > 128 && w.qn > 128) {
+                return go(rs::wide_product_kernel<T, true, true, true>);
+            }
+        } else {
+            const Estimate e(w);
+            if (wide && e.wide(w.pn) > e.square(w.pn)) wide = false;
+            if (wide && (P_ACROSS || e.wide(w.pn) <= e.few(w.pn))) {
+                if constexpr (sizeof(T) == 1) {
+                    return go(rs::wide_fp8_kernel<OUT>);
+                } else {
+                    return go(rs::wide_product_kernel<T, RAGGED_C, Q_ACROSS, P_ACROSS>);
+                }
             }
         }
     }
-    if constexpr (!RAGGED_C && !Q_ACROSS && !P_ACROSS) {
-        if (few_pays(w)) return launch_few(w, stream);
+    if constexpr (!RAGGED_C && !P_ACROSS) {
+        const Estimate e(w);
+        // (Workgroups of 65536 rows and 2^20 channels at most: below 2^31.)
+        if (w.cn >= static_cast<int>(16 / sizeof(T)) && w.num_rows <= 65536 &&
+            (wide || e.few(w.pn) < e.square(w.pn))) {
+            return launch_few(w, e, stream);
+        }
     }
-    const size_t p_tiles = (static_cast<size_t>(w.pn) + 127) / 128;
-    size_t q_tiles;
-    if (RAGGED_C) {
-        q_tiles = (static_cast<size_t>(w.qn) + 127) / 128 * static_cast<size_t>(w.experts);
-    } else {
-        // Each expert's last tile may be a part, and so may that of the rows of none.
-        q_tiles = w.num_rows / 128 + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1;
-    }
-    const size_t jobs = q_tiles * p_tiles;
-    const unsigned grid = static_cast<unsigned>(std::min<size_t>(jobs, size_t{1} << 24));
+    const size_t p_tiles = parts(static_cast<size_t>(w.pn), 128);
+    // Each expert's last tile may be a part, and so may that of the rows of none.
+    const size_t q_tiles = RAGGED_C
+        ? parts(static_cast<size_t>(w.qn), 128) * static_cast<size_t>(w.experts)
+        : w.num_rows / 128 + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1;
+    const unsigned grid = static_cast<unsigned>(std::min<size_t>(q_tiles * p_tiles, size_t{1} << 24));
     return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] {
         run_kernel(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS>, grid, 256, stream, w);
     });

@@ -2,18 +2,16 @@
 // the weights are read once and used for so few rows that memory bounds the product.
 //
 // A workgroup takes 16 * STRIPS output channels of an expert and up to 16 * ROWS of
-// its rows.  Its four waves share the contraction, 128 bytes of it a step in turn, so
-// that they read 512 bytes of each weight row together, straight into the registers
-// that the matrix instruction reads: no weight is used twice in a workgroup.  In the
-// end the waves' sums are joined in LDS, in the order of the waves.
+// its rows.  Its waves share the contraction, 128 bytes of it a step in turn, so
+// that they read adjacent parts of each weight row together, straight into the
+// registers that the matrix instruction reads: no weight is used twice in a workgroup.
+// In the end the waves' sums are joined in LDS, in the order of the waves.
 #pragma once
 
 #include "products.hpp"
 
 namespace rs {
 
-constexpr int kFewThreads = 256;
-constexpr int kFewWaves = kFewThreads / 64;
 constexpr int kFewAhead = 4;  // steps whose loads are in flight together
 
 // The 16 bytes of a row at element `at`, zeros behind `width`.  WHOLE: they exist.
@@ -25,11 +23,11 @@ __device__ __forceinline__ i32x4 row_chunk(const T *row, int at, int width) {
     return cut<T>(load16(reinterpret_cast<const char *>(row + from)), at, width);
 }
 
-template <class T, class OUT, int STRIPS, int ROWS>
-__global__ __launch_bounds__(kFewThreads) void few_rows_kernel(const ProductWork<T, OUT> w) {
+template <class T, class OUT, int WAVES, int STRIPS, int ROWS>
+__global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(const ProductWork<T, OUT> w) {
     constexpr bool kFp8 = std::is_same_v<T, fp8>;
     constexpr int V = 16 / static_cast<int>(sizeof(T)), kStepC = 8 * V;
-    __shared__ __align__(16) f32x4 sums[kFewWaves - 1][STRIPS * ROWS][64];
+    __shared__ __align__(16) f32x4 sums[WAVES - 1][STRIPS * ROWS][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = lane & 15, g = lane >> 4;
     const int num_rows = static_cast<int>(w.num_rows), c_n = w.cn;
@@ -70,7 +68,7 @@ __global__ __launch_bounds__(kFewThreads) void few_rows_kernel(const ProductWork
     const size_t p_blocks = (static_cast<size_t>(w.pn) + kScaleBlock - 1) / kScaleBlock;
     const float *ps = kFp8 ? w.p_scales + (static_cast<size_t>(t.expert) * p_blocks + p0 / kScaleBlock) * blocks : nullptr;
 
-    // AHEAD steps from element c on, kFewWaves steps apart.
+    // AHEAD steps from element c on, WAVES steps apart.
     const auto steps = [&](int c, auto ahead, auto whole) __attribute__((always_inline)) {
         constexpr int kAhead = decltype(ahead)::value;
         constexpr bool kWhole = decltype(whole)::value;
@@ -78,7 +76,7 @@ __global__ __launch_bounds__(kFewThreads) void few_rows_kernel(const ProductWork
         float scale[kAhead][ROWS];
 #pragma unroll
         for (int a = 0; a < kAhead; ++a) {
-            const int at = c + a * kFewWaves * kStepC + g * V;
+            const int at = c + a * WAVES * kStepC + g * V;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -87,7 +85,7 @@ __global__ __launch_bounds__(kFewThreads) void few_rows_kernel(const ProductWork
                 for (int j = 0; j < ROWS; ++j) fq[a][j][h] = row_chunk<T, kWhole>(qr[j], at + 4 * V * h, c_n);
             }
             if constexpr (kFp8) {
-                const int block = c / kScaleBlock + a * kFewWaves;
+                const int block = c / kScaleBlock + a * WAVES;
 #pragma unroll
                 for (int j = 0; j < ROWS; ++j) {
                     const int r = 16 * j + i < left ? 16 * j + i : left - 1;
@@ -115,12 +113,17 @@ __global__ __launch_bounds__(kFewThreads) void few_rows_kernel(const ProductWork
             }
         }
     };
-    int c = wave * kStepC;
-    constexpr int kSpan = kFewWaves * kStepC;
+    // The workgroups of an XCD begin at different places: rows whose stride is a large
+    // power of two stand in the same channel of its L2, and all would ask that one.
+    constexpr int kSpan = WAVES * kStepC, kBatch = kFewAhead * kSpan;
+    const int batches = c_n / kBatch;
+    int batch = batches > 0 ? static_cast<int>(blockIdx.x / 8 % static_cast<unsigned>(batches)) : 0;
 #pragma nounroll
-    for (; c + (kFewAhead - 1) * kSpan + kStepC <= c_n; c += kFewAhead * kSpan) {
-        steps(c, std::integral_constant<int, kFewAhead>{}, std::true_type{});
+    for (int b = 0; b < batches; ++b) {
+        steps(batch * kBatch + wave * kStepC, std::integral_constant<int, kFewAhead>{}, std::true_type{});
+        batch = batch + 1 < batches ? batch + 1 : 0;
     }
+    int c = batches * kBatch + wave * kStepC;
 #pragma nounroll
     for (; c + kStepC <= c_n; c += kSpan) steps(c, std::integral_constant<int, 1>{}, std::true_type{});
     if (c < c_n) steps(c, std::integral_constant<int, 1>{}, std::false_type{});
@@ -140,7 +143,7 @@ __global__ __launch_bounds__(kFewThreads) void few_rows_kernel(const ProductWork
         for (int s = 0; s < STRIPS; ++s) {
             f32x4 all = acc[s][j];
 #pragma unroll
-            for (int k = 0; k < kFewWaves - 1; ++k) all += sums[k][s * ROWS + j][lane];
+            for (int k = 0; k < WAVES - 1; ++k) all += sums[k][s * ROWS + j][lane];
             const int r = 16 * j + i, pi = p0 + 16 * s + 4 * g;
             float f[4];
 #pragma unroll
