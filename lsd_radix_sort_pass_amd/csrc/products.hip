@@ -68,6 +68,14 @@ bool feeds(const void *p, size_t stride, size_t expert, int width, bool across, 
            width >= static_cast<int>(chunk) && (!across || static_cast<size_t>(width) % chunk == 0);
 }
 
+// Whether both operands' rows begin at 16 bytes.
+template <class T, class OUT>
+bool aligned_rows(const rs::ProductWork<T, OUT> &w) {
+    constexpr size_t kChunk = 16 / sizeof(T);
+    return aligned(w.q, 16) && aligned(w.p, 16) && w.q_stride % kChunk == 0 && w.p_stride % kChunk == 0 &&
+           w.p_expert % kChunk == 0;
+}
+
 // ---------------------------------------------------------------------------
 // Which kernel takes a product of rows, by estimates of their times in us (with 4
 // to 6 for the launch and its beginning).  The experts are taken to have equally
@@ -76,12 +84,14 @@ bool feeds(const void *p, size_t stride, size_t expert, int width, bool across, 
 // Tiles go round the 256 CUs: the wide kernel's stage of 128 bytes of c takes 0.55 us, as
 // long as its loads are on their way, and more for a tile full of rows; but
 // memory gives no more than 6 TB/s.  The kernel for few rows reads weights at 5 to
-// 6 TB/s, and its rows again for each of its strips, at 6.5 TB/s.  Tiles of 128 x 128 take
-// 0.85 us for 128 bytes of c, and 1.5 if two share every CU; in float32 2.6 and 4.5.
+// 6 TB/s, and its rows again for each of its strips, at 6.5 TB/s, or 1.1 if they do not
+// begin at 16 bytes (in float32 it multiplies at 75 TFLOP/s).  Square tiles take 0.85 us for 128 bytes of c, and 1.5 if two share
+// every CU; of 64 x 64 in float32 1, and 0.52 of a CU's time.
 // Measured, in us, wide / few rows / square (bfloat16, rows x experts x out x in):
 // 8 of 64 x 2048 x 2048 24 / 12 / 32, 512 of 64 x 4096 x 4096 346 / 424 / -, 16 of one x
 // 8192 x 8192 75 / 28 / 107, 128 of one 95 / 88 / 101, 256 of one 154 / 172 / 102, 300 of 16
-// x 2048 x 2048 27 / 33 / 33, 512 of 8 x 1024 x 1024 16 / 10 / 18, 2048 of 8 26 / 26 / 19;
+// x 2048 x 2048 27 / 33 / 33, 512 of 8 x 1024 x 1024 16 / 10 / 18, 2048 of 8 26 / 26 / 19,
+// 1000 of 7 x 1001 x 1537 - / 79 / 34, 40 of 7 - / 18 / 34;
 // e4m3 256 of 128 x 2048 x 4096 166 / 143 / 310.
 // ---------------------------------------------------------------------------
 struct Estimate {
@@ -104,14 +114,17 @@ struct Estimate {
         const double stage = 0.55 + (t > 128 ? 1.1 : 0.65) * std::min(1.0, rows_each / rs::kWide);
         return 6 + std::max(std::ceil(t / 256) * stages * stage, weight_bytes / (bytes ? 5.5e6 : 6e6));
     }
-    double few(double pn) const {
+    // apart: rows that do not begin at 16 bytes.
+    double few(double pn, bool apart) const {
         const double weights = weight_bytes / (bytes ? 6e6 : 5.2e6);
-        const double rows = experts_used * rows_each * stages * 128 * std::ceil(pn / 32) / 6.5e6;
+        const double passes = experts_used * rows_each * stages * std::ceil(pn / 32);  // of 128 bytes of a row
+        const double rows = passes * (apart ? 128 / 1.1e6 : words ? 2.0 * 32 * 32 / 75e6 : 128 / 6.5e6);
         return 4 + std::max(weights, rows) + 0.25 * std::min(weights, rows);
     }
     double square(double pn) const {
-        const double t = tiles(128, 128, pn);
-        return 4 + stages * std::max(words ? 2.6 : 0.85, (words ? 4.5 : 1.5) * (t <= 256 ? 0.0 : std::ceil(t / 512)));
+        const double t = words ? tiles(64, 64, pn) : tiles(128, 128, pn);
+        const double step = words ? std::max(1.0, 0.52 * t / 256) : t <= 256 ? 0.85 : 1.5 * std::ceil(t / 512);
+        return 4 + std::max(stages * step, weight_bytes / 3.5e6);
     }
 };
 
@@ -166,7 +179,7 @@ bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
         } else {
             const Estimate e(w);
             if (wide && e.wide(w.pn) > e.square(w.pn)) wide = false;
-            if (wide && (P_ACROSS || e.wide(w.pn) <= e.few(w.pn))) {
+            if (wide && (P_ACROSS || e.wide(w.pn) <= e.few(w.pn, false))) {
                 if constexpr (sizeof(T) == 1) {
                     return go(rs::wide_fp8_kernel<OUT>);
                 } else {
@@ -179,19 +192,28 @@ bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
         const Estimate e(w);
         // (Workgroups of 65536 rows and 2^20 channels at most: below 2^31.)
         if (w.cn >= static_cast<int>(16 / sizeof(T)) && w.num_rows <= 65536 &&
-            (wide || e.few(w.pn) < e.square(w.pn))) {
+            (wide || e.few(w.pn, !aligned_rows(w)) < e.square(w.pn))) {
             return launch_few(w, e, stream);
         }
     }
-    const size_t p_tiles = parts(static_cast<size_t>(w.pn), 128);
+    const int least = std::min(Q_ACROSS ? w.qn : w.cn, P_ACROSS ? w.pn : w.cn);  // width of a row
+    constexpr size_t kSide = rs::kSquare<T>;
+    const size_t p_tiles = parts(static_cast<size_t>(w.pn), kSide);
     // Each expert's last tile may be a part, and so may that of the rows of none.
     const size_t q_tiles = RAGGED_C
-        ? parts(static_cast<size_t>(w.qn), 128) * static_cast<size_t>(w.experts)
-        : w.num_rows / 128 + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1;
+        ? parts(static_cast<size_t>(w.qn), kSide) * static_cast<size_t>(w.experts)
+        : w.num_rows / kSide + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1;
     const unsigned grid = static_cast<unsigned>(std::min<size_t>(q_tiles * p_tiles, size_t{1} << 24));
-    return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] {
-        run_kernel(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS>, grid, 256, stream, w);
-    });
+    const auto go = [&](auto kernel) {
+        return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] { run_kernel(kernel, grid, 256, stream, w); });
+    };
+    if (least < static_cast<int>(16 / sizeof(T))) {
+        return go(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS, 1, true>);
+    }
+    if (sizeof(T) < 4 && !aligned_rows(w)) {
+        return go(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS, 1, false>);
+    }
+    return go(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS, 2, false>);
 }
 
 rs::Divider divider(size_t by) {

@@ -153,61 +153,71 @@ __device__ __forceinline__ f32x4 mma16_fp8(i32x4 p0, i32x4 p1, i32x4 q0, i32x4 q
                                                             0x7F7F7F7F);
 }
 
-// ---------------------------------------------------------------------------
-// Tiles of an operand in LDS
-// ---------------------------------------------------------------------------
-// A tile holds 128 bytes of c for each of 128 rows (along), or the elements of
-// 128 columns for as many steps of c as fill 16 KiB (across).  Its 16-byte
-// chunks (along) and 32-byte units (across) are exchanged so that the 16 or 32 lanes
-// that LDS serves at once (256 bytes, all 64 banks) meet every bank once.
-constexpr int kTileBytes = 16384;
-
+// 32 x 32 results, 16 elements of c: lane l holds row l % 32 of an operand and its
+// 16-byte chunk l / 32; the result's lane l holds column q = l % 32 and in element
+// i the row p = 8 (i / 4) + 4 (l / 32) + i % 4.
 template <class T>
-constexpr int kStep = 128 / static_cast<int>(sizeof(T));  // elements of c in a tile
-
-// Byte address in a tile of 16-byte chunk `chunk` of row `row`.
-template <class T, bool ACROSS>
-__device__ __forceinline__ int tile_at(int row, int chunk) {
-    if constexpr (!ACROSS) {
-        return row * 128 + ((chunk ^ (row >> 1 & 7)) << 4);
-    } else if constexpr (sizeof(T) == 2) {
-        const int turn = (row & 3) | ((row >> 1) & 4);
-        return row * 256 + ((chunk ^ (turn << 1)) << 4);
+__device__ __forceinline__ f32x16 mma32(i32x4 p, i32x4 q, f32x16 c) {
+    if constexpr (std::is_same_v<T, bf16>) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, p), __builtin_bit_cast(bf16x8, q), c, 0,
+                                                       0, 0);
     } else {
-        return row * 512 + ((chunk ^ ((row >> 2 & 3) << 2)) << 4);
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, p), __builtin_bit_cast(f16x8, q), c, 0, 0,
+                                                      0);
     }
 }
 
-template <class T, bool ACROSS>
-constexpr int kChunksPerRow = ACROSS ? 128 * static_cast<int>(sizeof(T)) / 16 : 8;
+// ---------------------------------------------------------------------------
+// Tiles of an operand in LDS
+// ---------------------------------------------------------------------------
+// A tile holds 128 bytes of c for each of SIDE rows (along), or the elements of SIDE
+// columns for as many steps of c (across).  Its 16-byte chunks are exchanged so that
+// the lanes that LDS serves at once (256 bytes, all 64 banks) meet every bank once.
+template <class T>
+constexpr int kStep = 128 / static_cast<int>(sizeof(T));  // elements of c in a tile
 
-// The 16 bytes that lane `lane` feeds into the matrix instruction `half` (of 2)
-// of rows (along) or columns (across) mn .. mn + 15 of a tile.
-template <class T, bool ACROSS>
-__device__ __forceinline__ i32x4 fragment(const char *tile, int mn, int half, int lane) {
-    const int i = lane & 15, g = lane >> 4;
-    if constexpr (!ACROSS) {
-        return *reinterpret_cast<const i32x4 *>(tile + tile_at<T, false>(mn + i, g + 4 * half));
+template <class T, int SIDE, bool ACROSS>
+constexpr int kChunksPerRow = ACROSS ? SIDE * static_cast<int>(sizeof(T)) / 16 : 8;
+
+// Byte address in a tile of 16-byte chunk `chunk` of row `row`.
+template <class T, int SIDE, bool ACROSS>
+__device__ __forceinline__ int tile_at(int row, int chunk) {
+    const int turn = !ACROSS ? row >> 1 & 7
+        : sizeof(T) == 4     ? (row >> 2 & 3) << 2
+                             : (row & 3) << 2;
+    return row * (kChunksPerRow<T, SIDE, ACROSS> * 16) + ((chunk ^ turn) << 4);
+}
+
+// What a lane feeds into the matrix instructions of a tile for rows (along) or columns
+// (across) mn and those behind it: in 16 bits 32 of them, one of four steps; else 16,
+// one of two halves.
+template <class T, int SIDE, bool ACROSS>
+__device__ __forceinline__ i32x4 fragment(const char *tile, int mn, int part, int lane) {
+    if constexpr (sizeof(T) == 2 && !ACROSS) {
+        return *reinterpret_cast<const i32x4 *>(tile + tile_at<T, SIDE, false>(mn + (lane & 31), 2 * part + (lane >> 5)));
     } else if constexpr (sizeof(T) == 2) {
         // Two reads that turn 4 rows of 16 elements into 4 elements of each column.
+        const int i = lane & 15, g = lane >> 4;
         union {
-            s16x4 part[2];
+            s16x4 half[2];
             i32x4 all;
         } f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int row = 32 * half + 8 * g + 4 * h + (i >> 2);
-            const char *at = tile + tile_at<T, true>(row, (mn >> 3) + (i >> 1 & 1)) + (i & 1) * 8;
-            f.part[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4 *)(at));
+            const int row = 16 * part + 8 * (g >> 1) + 4 * h + (i >> 2), col = mn + 16 * (g & 1);
+            const char *at = tile + tile_at<T, SIDE, true>(row, (col >> 3) + (i >> 1 & 1)) + (i & 1) * 8;
+            f.half[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(at));
         }
         return f.all;
+    } else if constexpr (!ACROSS) {
+        return *reinterpret_cast<const i32x4 *>(tile + tile_at<T, SIDE, false>(mn + (lane & 15), (lane >> 4) + 4 * part));
     } else {
+        const int col = mn + (lane & 15);
         i32x4 f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int row = 4 * (g + 4 * half) + j, col = mn + i;
-            f[j] = *reinterpret_cast<const int *>(tile + tile_at<T, true>(row, col >> 2) + (col & 3) * 4);
+            const int row = 4 * ((lane >> 4) + 4 * part) + j;
+            f[j] = *reinterpret_cast<const int *>(tile + tile_at<T, SIDE, true>(row, col >> 2) + (col & 3) * 4);
         }
         return f;
     }
@@ -229,35 +239,47 @@ __device__ __forceinline__ i32x4 cut(i32x4 raw, int at, int width) {
 }
 
 // A tile's elements on their way from memory through registers to LDS, for
-// operands of any alignment, width and stride.  256 threads, 4 chunks each; the
-// loads are clamped into range, without a branch between them, and what they
-// should not have read is cleared before it is stored.
-template <class T, bool ACROSS>
+// operands of any alignment, width and stride, by 256 threads.  The loads are clamped
+// into range, without a branch between them, and what they should not have read is
+// cleared before it is stored.  NARROW: rows of less than 16 bytes, element by element.
+template <class T, int SIDE, bool ACROSS, bool NARROW>
 struct Staging {
     static constexpr int V = 16 / static_cast<int>(sizeof(T));
-    static constexpr int kChunks = kChunksPerRow<T, ACROSS>;
-    i32x4 raw[4];
+    static constexpr int kChunks = kChunksPerRow<T, SIDE, ACROSS>;
+    static constexpr int kLoads = SIDE / 32;
+    const T *from[kLoads];  // along: the row; across: the column
+    size_t stride;
+    int rows, width, first;  // of the operand's matrix, and the tile's first row (along) or column (across)
 
-    // rows: those of the operand's matrix that exist; width: elements of a row;
-    // row0, col0: the tile's first.
-    __device__ __forceinline__ void load(const T *base, size_t stride, int rows, int width, int row0, int col0, int tid) {
-        if (width >= V) {
+    __device__ __forceinline__ void set(const T *base, size_t stride_, int rows_, int width_, int first_, int tid) {
+        stride = stride_, rows = rows_, width = width_, first = first_;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int id = i * 256 + tid;
-                int r = row0 + id / kChunks, c = col0 + id % kChunks * V;
-                r = r < rows ? r : rows - 1;
-                c = c < width - V ? c : width - V;
-                raw[i] = load16(reinterpret_cast<const char *>(base + static_cast<size_t>(r) * stride + c));
+        for (int i = 0; i < kLoads; ++i) {
+            const int id = i * 256 + tid;
+            if constexpr (ACROSS) {
+                const int c = first + id % kChunks * V;
+                from[i] = base + (NARROW ? 0 : c < width - V ? c : width - V);
+            } else {
+                const int r = first + id / kChunks;
+                from[i] = base + static_cast<size_t>(r < rows ? r : rows - 1) * stride;
             }
-        } else {
+        }
+    }
+
+    // The chunks of the step that begins at c.
+    __device__ __forceinline__ void load(i32x4 (&raw)[kLoads], int c, int tid) const {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int id = i * 256 + tid;
-                int r = row0 + id / kChunks;
-                const int c = col0 + id % kChunks * V;
-                r = r < rows ? r : rows - 1;
-                const T *row = base + static_cast<size_t>(r) * stride;
+        for (int i = 0; i < kLoads; ++i) {
+            const int id = i * 256 + tid;
+            const T *p = from[i];
+            int at = ACROSS ? first + id % kChunks * V : c + id % kChunks * V;
+            if constexpr (ACROSS) {
+                const int r = c + id / kChunks;
+                p += static_cast<size_t>(r < rows ? r : rows - 1) * stride;
+            } else if constexpr (!NARROW) {
+                p += at < width - V ? at : width - V;
+            }
+            if constexpr (NARROW) {
                 union {
                     T e[V];
                     i32x4 all;
@@ -265,31 +287,47 @@ struct Staging {
                 u.all = i32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    if (c + j < width) u.e[j] = row[c + j];
+                    if (at + j < width) u.e[j] = p[at + j];
                 }
                 raw[i] = u.all;
+            } else {
+                raw[i] = load16(reinterpret_cast<const char *>(p));
             }
         }
     }
 
-    __device__ __forceinline__ void store(char *tile, int rows, int width, int row0, int col0, int tid) {
-        const bool whole = row0 + 1024 / kChunks <= rows && col0 + kChunks * V <= width;
+    __device__ __forceinline__ void store(i32x4 (&raw)[kLoads], char *tile, int c, int tid) const {
+        const bool whole = ACROSS ? first + SIDE <= width && c + kStep<T> <= rows : c + kStep<T> <= width;
         if (!whole) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int id = i * 256 + tid, c = col0 + id % kChunks * V;
-                if (width >= V) raw[i] = cut<T>(raw[i], c, width);
-                // Rows of the other kind hold results of their own, which are not stored.
-                if (ACROSS && row0 + id / kChunks >= rows) raw[i] = i32x4{0, 0, 0, 0};
+            for (int i = 0; i < kLoads; ++i) {
+                const int id = i * 256 + tid;
+                if constexpr (!NARROW) raw[i] = cut<T>(raw[i], (ACROSS ? first : c) + id % kChunks * V, width);
+                // (Rows of the other kind hold results of their own, which are not stored.)
+                if (ACROSS && c + id / kChunks >= rows) raw[i] = i32x4{0, 0, 0, 0};
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kLoads; ++i) {
             const int id = i * 256 + tid;
-            *reinterpret_cast<i32x4 *>(tile + tile_at<T, ACROSS>(id / kChunks, id % kChunks)) = raw[i];
+            *reinterpret_cast<i32x4 *>(tile + tile_at<T, SIDE, ACROSS>(id / kChunks, id % kChunks)) = raw[i];
         }
     }
 };
+
+// ---------------------------------------------------------------------------
+// Waits for this wave's reads and writes of LDS and for the other waves, but not
+// for loads from memory on their way to registers.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void lds_barrier() {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#endif
+    __builtin_amdgcn_s_barrier();
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" ::: "memory");
+#endif
+}
 
 // ---------------------------------------------------------------------------
 // Zeros in rows of no expert: 128 of them (fewer at their end), columns
@@ -310,32 +348,41 @@ __device__ __forceinline__ void clear_tile(OUT *out, size_t stride, int width, R
 }
 
 // ---------------------------------------------------------------------------
-// The product of any sizes, alignments and strides: 128 x 128 results a
-// workgroup of four waves, 64 x 64 a wave; the next tiles' loads are in flight
-// while the present ones are multiplied.
+// The product of any sizes, alignments and strides: SIDE x SIDE results a workgroup of
+// four waves, a quarter each; the loads of the next AHEAD steps are in flight while the
+// present one is multiplied.  Two take less time where rows begin at 16 bytes (1024 rows
+// 4096 x 4096 bfloat16 57 us, 69 with one), but more where they do not, as the 32 KiB cache has to hold the lines that two steps share (4003
+// rows of 7 experts 1001 x 1537 float16 52 us, 45 with one).  SIDE is 128 in 16 and 8 bits, 64
+// takes up to 1.7 times as long; in 32 bits, where the matrix instructions take eight
+// times as long, 64 fills the CUs more evenly: the gradients of 4093 rows of 8 experts
+// 515 x 1030 119 us, 169 with 128.
 // ---------------------------------------------------------------------------
-template <class T, class OUT, bool RAGGED_C, bool Q_ACROSS, bool P_ACROSS>
-__global__ __launch_bounds__(256, 2) void product_kernel(const ProductWork<T, OUT> w) {
+template <class T>
+constexpr int kSquare = sizeof(T) == 4 ? 64 : 128;
+
+template <class T, class OUT, bool RAGGED_C, bool Q_ACROSS, bool P_ACROSS, int AHEAD, bool NARROW>
+__global__ __launch_bounds__(256, kSquare<T> == 64 ? 4 : 2) void product_kernel(const ProductWork<T, OUT> w) {
     constexpr bool kFp8 = std::is_same_v<T, fp8>;
-    __shared__ __align__(16) char q_tile[kTileBytes];
-    __shared__ __align__(16) char p_tile[kTileBytes];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int q_wave = (wave >> 1) * 64, p_wave = (wave & 1) * 64;
+    constexpr int SIDE = kSquare<T>, kHalf = SIDE / 2;
+    __shared__ __align__(16) char q_tile[SIDE * 128];
+    __shared__ __align__(16) char p_tile[SIDE * 128];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int q_wave = (wave >> 1) * kHalf, p_wave = (wave & 1) * kHalf;
     const int num_rows = static_cast<int>(w.num_rows);
 
-    const unsigned p_tiles = static_cast<unsigned>((w.pn + 127) / 128);
-    const unsigned q_tiles = RAGGED_C ? static_cast<unsigned>((w.qn + 127) / 128) : 0;
+    const unsigned p_tiles = static_cast<unsigned>((w.pn + SIDE - 1) / SIDE);
+    const unsigned q_tiles = RAGGED_C ? static_cast<unsigned>((w.qn + SIDE - 1) / SIDE) : 0;
     for (size_t job = blockIdx.x;; job += gridDim.x) {
         const T *q = w.q, *p = w.p;
         OUT *out = w.out;
         int q0, q_rows, c_n, expert;
-        const int p0 = static_cast<int>(job % p_tiles) * 128;
+        const int p0 = static_cast<int>(job % p_tiles) * SIDE;
         int first_row = 0;
         if constexpr (RAGGED_C) {
             const size_t t = job / p_tiles, e = t / q_tiles;
             if (e >= static_cast<size_t>(w.experts)) break;
             expert = static_cast<int>(e);
-            q0 = static_cast<int>(t % q_tiles) * 128;
+            q0 = static_cast<int>(t % q_tiles) * SIDE;
             q_rows = w.qn;
             const RowSpan r = rows_of(w.offsets, expert, num_rows);
             c_n = r.hi - r.lo;
@@ -345,15 +392,15 @@ __global__ __launch_bounds__(256, 2) void product_kernel(const ProductWork<T, OU
         } else {
             const size_t t = job / p_tiles;
             if (t > 0x7FFFFFFFu) break;
-            const RowTile f = find_tile(w.offsets, w.experts, num_rows, 128, static_cast<int>(t));
+            const RowTile f = find_tile(w.offsets, w.experts, num_rows, SIDE, static_cast<int>(t));
             if (f.expert < 0) break;
             expert = f.expert;
             if (expert == w.experts) {
                 if (!w.clear) break;
-                clear_tile(out, w.out_stride, w.pn, f, 128, num_rows, p0, 128);
+                clear_tile(out, w.out_stride, w.pn, f, SIDE, num_rows, p0, SIDE);
                 continue;
             }
-            q0 = f.tile * 128;
+            q0 = f.tile * SIDE;
             q_rows = f.rows.hi - f.rows.lo;
             c_n = w.cn;
             first_row = f.rows.lo;
@@ -362,86 +409,113 @@ __global__ __launch_bounds__(256, 2) void product_kernel(const ProductWork<T, OU
             p += static_cast<size_t>(expert) * w.p_expert;
         }
 
-        f32x4 acc[4][4];
+        // In 16 bits 32 x 32 results an instruction, else 16 x 16.
+        constexpr int kSide = sizeof(T) == 2 ? 32 : 16, kCount = kHalf / kSide;
+        using Acc = std::conditional_t<sizeof(T) == 2, f32x16, f32x4>;
+        Acc acc[kCount][kCount];
 #pragma unroll
         for (auto &a : acc) {
 #pragma unroll
-            for (auto &b : a) b = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (auto &b : a) b = Acc{};
         }
-        Staging<T, Q_ACROSS> sq;
-        Staging<T, P_ACROSS> sp;
-        const int q_have = Q_ACROSS ? c_n : q_rows, q_width = Q_ACROSS ? w.qn : c_n;
-        const int p_have = P_ACROSS ? c_n : w.pn, p_width = P_ACROSS ? w.pn : c_n;
-        const auto load = [&](int c) {
-            sq.load(q, w.q_stride, q_have, q_width, Q_ACROSS ? c : q0, Q_ACROSS ? q0 : c, tid);
-            sp.load(p, w.p_stride, p_have, p_width, P_ACROSS ? c : p0, P_ACROSS ? p0 : c, tid);
+        Staging<T, SIDE, Q_ACROSS, NARROW> sq;
+        Staging<T, SIDE, P_ACROSS, NARROW> sp;
+        i32x4 raw_q[AHEAD][SIDE / 32], raw_p[AHEAD][SIDE / 32];
+        // (What lies behind the end is loaded from before it, and not used: a load in a
+        // branch would have to be waited for before the next.)
+        const auto load = [&](int c, auto set) __attribute__((always_inline)) {
+            sq.load(raw_q[decltype(set)::value], c, tid);
+            sp.load(raw_p[decltype(set)::value], c, tid);
         };
-        if (c_n > 0) load(0);
-        for (int c = 0; c < c_n; c += kStep<T>) {
-            __syncthreads();
-            sq.store(q_tile, q_have, q_width, Q_ACROSS ? c : q0, Q_ACROSS ? q0 : c, tid);
-            sp.store(p_tile, p_have, p_width, P_ACROSS ? c : p0, P_ACROSS ? p0 : c, tid);
-            __syncthreads();
-            if (c + kStep<T> < c_n) load(c + kStep<T>);
-            if constexpr (kFp8) {
+        const auto step = [&](int c, auto set) __attribute__((always_inline)) {
+            lds_barrier();
+            sq.store(raw_q[decltype(set)::value], q_tile, c, tid);
+            sp.store(raw_p[decltype(set)::value], p_tile, c, tid);
+            lds_barrier();
+            [[maybe_unused]] float scale[kCount];
+            if constexpr (kFp8) {  // (before the loads that nothing waits for yet)
                 const int block = c / kScaleBlock, blocks = (w.cn + kScaleBlock - 1) / kScaleBlock;
                 const int p_blocks = (w.pn + kScaleBlock - 1) / kScaleBlock;
                 const float ps = w.p_scales[(static_cast<size_t>(expert) * p_blocks + p0 / kScaleBlock) * blocks + block];
-                float scale[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < kCount; ++j) {
                     int r = q0 + q_wave + 16 * j + (lane & 15);
                     r = r < q_rows ? r : q_rows - 1;
                     scale[j] = ps * w.q_scales[block * w.num_rows + first_row + r];
                 }
-                i32x4 fp[4][2], fq[4][2];
+            }
+            load(c + AHEAD * kStep<T>, set);
+            if constexpr (kFp8) {
+                i32x4 fp[kCount][2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        fp[i][h] = fragment<T, false>(p_tile, p_wave + 16 * i, h, lane);
-                        fq[i][h] = fragment<T, false>(q_tile, q_wave + 16 * i, h, lane);
-                    }
+                    for (int i = 0; i < kCount; ++i) fp[i][h] = fragment<T, SIDE, false>(p_tile, p_wave + 16 * i, h, lane);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int j = 0; j < kCount; ++j) {
+                    const i32x4 fq0 = fragment<T, SIDE, false>(q_tile, q_wave + 16 * j, 0, lane);
+                    const i32x4 fq1 = fragment<T, SIDE, false>(q_tile, q_wave + 16 * j, 1, lane);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const f32x4 part = mma16_fp8(fp[i][0], fp[i][1], fq[j][0], fq[j][1]);
+                    for (int i = 0; i < kCount; ++i) {
+                        const f32x4 part = mma16_fp8(fp[i][0], fp[i][1], fq0, fq1);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(part[r], scale[j], acc[i][j][r]);
                     }
                 }
             } else {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    i32x4 fp[4], fq[4];
+                for (int k = 0; k < (sizeof(T) == 2 ? 4 : 2); ++k) {
+                    i32x4 fp[kCount], fq[kCount];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        fp[i] = fragment<T, P_ACROSS>(p_tile, p_wave + 16 * i, h, lane);
-                        fq[i] = fragment<T, Q_ACROSS>(q_tile, q_wave + 16 * i, h, lane);
+                    for (int i = 0; i < kCount; ++i) {
+                        fp[i] = fragment<T, SIDE, P_ACROSS>(p_tile, p_wave + kSide * i, k, lane);
+                        fq[i] = fragment<T, SIDE, Q_ACROSS>(q_tile, q_wave + kSide * i, k, lane);
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < kCount; ++i) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[i][j] = mma16<T>(fp[i], fq[j], acc[i][j]);
+                        for (int j = 0; j < kCount; ++j) {
+                            if constexpr (sizeof(T) == 2) {
+                                acc[i][j] = mma32<T>(fp[i], fq[j], acc[i][j]);
+                            } else {
+                                acc[i][j] = mma16<T>(fp[i], fq[j], acc[i][j]);
+                            }
+                        }
                     }
                 }
             }
+        };
+        if (c_n > 0) {
+            sq.set(q, w.q_stride, Q_ACROSS ? c_n : q_rows, Q_ACROSS ? w.qn : c_n, q0, tid);
+            sp.set(p, w.p_stride, P_ACROSS ? c_n : w.pn, P_ACROSS ? w.pn : c_n, p0, tid);
+            constexpr std::integral_constant<int, 0> first{};
+            constexpr std::integral_constant<int, AHEAD - 1> second{};
+            load(0, first);
+            if constexpr (AHEAD == 2) load(kStep<T>, second);
+#pragma nounroll
+            for (int c = 0; c < c_n; c += AHEAD * kStep<T>) {
+                step(c, first);
+                if constexpr (AHEAD == 2) {
+                    if (c + kStep<T> < c_n) step(c + kStep<T>, second);
+                }
+            }
         }
-        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int qi = q0 + q_wave + 16 * j + (lane & 15);
+        for (int j = 0; j < kCount; ++j) {
+            const int qi = q0 + q_wave + kSide * j + lane % kSide;
             if (qi >= q_rows) continue;
             OUT *row = out + static_cast<size_t>(qi) * w.out_stride;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int pi = p0 + p_wave + 16 * i + 4 * (lane >> 4);
-                float f[4];
+            for (int i = 0; i < kCount; ++i) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) f[r] = acc[i][j][r];
-                if (pi < w.pn) store_some<OUT, 4>(row + pi, w.pn - pi, f);
+                for (int a = 0; a < (sizeof(T) == 2 ? 4 : 1); ++a) {
+                    const int pi = p0 + p_wave + kSide * i + 8 * a + 4 * (lane / kSide);
+                    float f[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) f[r] = acc[i][j][4 * a + r];
+                    if (pi < w.pn) store_some<OUT, 4>(row + pi, w.pn - pi, f);
+                }
             }
         }
     }

@@ -170,20 +170,6 @@ __device__ __forceinline__ void read_pq(const Reader<Q_ACROSS, Q_ACROSS ? 16 : 8
 #endif
 }
 
-// 32 x 32 results, 16 elements of c: lane l holds row l % 32 of an operand and its
-// 16-byte chunk l / 32; the result's lane l holds column q = l % 32 and in element
-// i the row p = 8 (i / 4) + 4 (l / 32) + i % 4.
-template <class T>
-__device__ __forceinline__ f32x16 mma32(i32x4 p, i32x4 q, f32x16 c) {
-    if constexpr (std::is_same_v<T, bf16>) {
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, p), __builtin_bit_cast(bf16x8, q), c, 0,
-                                                       0, 0);
-    } else {
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, p), __builtin_bit_cast(f16x8, q), c, 0, 0,
-                                                      0);
-    }
-}
-
 // The same pointer in every lane, in scalar registers.
 template <class T>
 __device__ __forceinline__ const T *uniform(const T *p) {
