@@ -227,6 +227,13 @@ bool with_act(int act, F &&f) {
     return act == RS_ACT_GELU ? f(IntC<rs::kActGelu>{}) : f(IntC<rs::kActSilu>{});
 }
 
+// Calls f(IntC of a rs::Row) for rows of `width` elements, `vec` of them 16 bytes.
+template <class F>
+bool with_row(int width, int vec, F &&f) {
+    if (width < vec) return f(IntC<rs::kNarrowRow>{});
+    return width % 8 == 0 ? f(IntC<rs::kWholeRow>{}) : f(IntC<rs::kRaggedRow>{});
+}
+
 bool good_gate(int dtype, int act, int width) {
     return dtype_bytes(dtype) != 0 && (act == RS_ACT_SILU || act == RS_ACT_GELU) && width >= 1 && width <= kMaxWidth / 2;
 }
@@ -299,22 +306,19 @@ rs_status quantize_rows(const void *rows, int dtype, size_t num_rows, int width,
     rs::GateWork w{};
     w.rows = rows, w.out = out, w.scales = scales, w.rows_stride = rows_stride, w.out_stride = out_stride;
     w.offsets = offsets, w.experts = experts, w.num_rows = num_rows, w.width = width, w.clear = all != 0;
-    const auto across = static_cast<unsigned>((blocks + rs::kQuantizeBlocks - 1) / rs::kQuantizeBlocks);
-    const dim3 grid(across, static_cast<unsigned>(std::min<size_t>((num_rows + 15) / 16, 65535)));
+    const int per_group = gate ? rs::kQuantizeBlocks<true> : rs::kQuantizeBlocks<false>;
+    const dim3 grid(static_cast<unsigned>(parts(blocks, static_cast<size_t>(per_group))),
+                    static_cast<unsigned>(std::min<size_t>(parts(num_rows, 16), 65535)));
     const bool ok = with_dtype(dtype, [&](auto zero) {
         using T = decltype(zero);
         const auto go = [&](auto kernel) {
             return launch_kernel(RS_KERNEL_QUANTIZE, stream,
                                  [&] { run_kernel(kernel, grid, rs::kGateBlock, stream, w); });
         };
-        const bool whole = width % 8 == 0;
-        if (!gate) {
-            return whole ? go(rs::quantize_rows_kernel<T, 0, false, true>) : go(rs::quantize_rows_kernel<T, 0, false, false>);
-        }
-        return with_act(act, [&](auto a) {
-            constexpr int kAct = decltype(a)::value;
-            return whole ? go(rs::quantize_rows_kernel<T, kAct, true, true>)
-                         : go(rs::quantize_rows_kernel<T, kAct, true, false>);
+        return with_row(width, rs::kVec<T>, [&](auto row) {
+            constexpr int kRow = decltype(row)::value;
+            if (!gate) return go(rs::quantize_rows_kernel<T, 0, false, kRow>);
+            return with_act(act, [&](auto a) { return go(rs::quantize_rows_kernel<T, decltype(a)::value, true, kRow>); });
         });
     });
     return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
@@ -457,8 +461,11 @@ rs_status rs_quantize_weights(const void *weights, int dtype, int experts, int o
     const rs::QuantizeWeightsWork w{weights, out, scales, weights_stride, weights_expert, experts, out_width, in_width};
     const unsigned grid = static_cast<unsigned>(std::min<size_t>(blocks, kMaxGrid));
     const bool ok = with_dtype(dtype, [&](auto zero) {
-        return launch_kernel(RS_KERNEL_QUANTIZE, stream, [&] {
-            run_kernel(rs::quantize_weights_kernel<decltype(zero)>, grid, rs::kGateBlock, stream, w);
+        using T = decltype(zero);
+        return with_row(in_width, rs::kVec<T>, [&](auto row) {
+            return launch_kernel(RS_KERNEL_QUANTIZE, stream, [&] {
+                run_kernel(rs::quantize_weights_kernel<T, decltype(row)::value>, grid, rs::kGateBlock, stream, w);
+            });
         });
     });
     return ok ? RS_SUCCESS : RS_ERROR_LAUNCH;
