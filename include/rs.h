@@ -418,7 +418,8 @@ rs_status rs_combine_rows_backward_all(const void *grad_out, int dtype, size_t t
  * elements.  Products are summed in float32 in a fixed order (in blocks, by matrix
  * instructions, which add the products of a block in an order of their own)
  * and rounded once.  1 <= widths <= RS_MAX_ROW_WIDTH, experts <=
- * RS_MAX_EXPERTS, num_rows <= RS_MAX_SLOTS. */
+ * RS_MAX_EXPERTS, num_rows <= RS_MAX_PRODUCT_ROWS. */
+#define RS_MAX_PRODUCT_ROWS ((size_t)1 << 30)
 
 /* out[r][n] = sum over k of weights[e][n][k] * rows[r][k], e the expert of row r. */
 rs_status rs_expert_products(const void *rows, int dtype, size_t num_rows, int in_width, size_t rows_stride,
@@ -444,7 +445,10 @@ rs_status rs_expert_products_backward(const void *grad, int dtype, size_t num_ro
  *   out[r][n] = sum over b < B of row_scales[b][r] * weight_scales[e][n / RS_SCALE_BLOCK][b]
  *               * sum over k of block b of rows[r][k] * weights[e][n][k],
  * out in dtype.  row_scales [B][num_rows] and weight_scales
- * [experts][ceil(out_width / RS_SCALE_BLOCK)][B] are contiguous. */
+ * [experts][ceil(out_width / RS_SCALE_BLOCK)][B] are contiguous.  The products of a
+ * block are added by the matrix instruction, which keeps of each what stands at
+ * most 18 binary digits below the largest of them: a block's sum is off by up to
+ * 2^-11 of its largest product, a few 10^-4 of the result, whatever dtype is. */
 #define RS_SCALE_BLOCK 128
 rs_status rs_expert_products_fp8(const uint8_t *rows, const float *row_scales, size_t num_rows, int in_width,
                                  size_t rows_stride, const int32_t *offsets, int experts, const uint8_t *weights,

@@ -28,7 +28,7 @@ constexpr int kMaxWidth = RS_MAX_ROW_WIDTH;
 constexpr size_t kMaxExpertStride = size_t{1} << 50;
 
 bool good_groups(const int32_t *offsets, int experts, size_t num_rows) {
-    if (experts < 1 || experts > RS_MAX_EXPERTS || num_rows > RS_MAX_SLOTS) return false;
+    if (experts < 1 || experts > RS_MAX_EXPERTS || num_rows > RS_MAX_PRODUCT_ROWS) return false;
     return offsets == nullptr ? experts == 1 : aligned(offsets, 4);
 }
 

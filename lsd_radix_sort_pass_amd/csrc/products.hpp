@@ -330,20 +330,21 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 // ---------------------------------------------------------------------------
-// Zeros in rows of no expert: 128 of them (fewer at their end), columns
-// [col, col + 128).
+// Zeros in `height` rows of no expert (fewer at their end), `columns` of them from col on,
+// by all of the workgroup's threads, 16 bytes a thread.
 // ---------------------------------------------------------------------------
 template <class OUT>
 __device__ __forceinline__ void clear_tile(OUT *out, size_t stride, int width, RowTile t, int height, int num_rows,
                                            int col, int columns) {
-    const int rest = t.rows.lo + num_rows - t.rows.hi, first = t.tile * height;
-    const int rows = rest - first < height ? rest - first : height;
-    const int wide = width - col < columns ? width - col : columns;
-    for (int i = threadIdx.x; i < rows * columns; i += blockDim.x) {
-        const int c = i % columns;
-        int r = first + i / columns;
+    constexpr int V = kVec<OUT>;
+    const int rest = t.rows.lo + (num_rows - t.rows.hi), first = t.tile * height;
+    const int rows = rest - first < height ? rest - first : height, chunks = columns / V;
+    const float zeros[V] = {};
+    for (int i = threadIdx.x; i < rows * chunks; i += blockDim.x) {
+        const int c = col + i % chunks * V;
+        int r = first + i / chunks;
         r = r < t.rows.lo ? r : r - t.rows.lo + t.rows.hi;
-        if (c < wide) out[static_cast<size_t>(r) * stride + col + c] = OUT{};
+        if (c < width) store_some<OUT, V>(out + static_cast<size_t>(r) * stride + c, width - c, zeros);
     }
 }
 

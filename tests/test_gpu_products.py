@@ -217,6 +217,43 @@ def test_products_far_offsets():
     assert torch.equal(far[0], near[0]) and torch.equal(far[1], near[1])
 
 
+def test_products_far_offsets_of_tiles():
+    """The same for many rows: 1200 of them 8 MiB apart, matrices 4 GiB apart."""
+    note("far offsets of tiles")
+    gen = generator(10)
+    n, E, N, K, stride = 1200, 3, 272, 328, 1 << 22
+    x = torch.empty(n * stride, dtype=torch.bfloat16, device="cuda").as_strided((n, K), (stride, 1))
+    w = torch.empty(2 * (1 << 31) + N * K, dtype=torch.bfloat16, device="cuda").as_strided((E, N, K), (1 << 31, K, 1))
+    x.copy_(normal(gen, (n, K), "bfloat16")), w.copy_(normal(gen, (E, N, K), "bfloat16"))
+    o = torch.tensor([0, 500, 510, 1100], dtype=torch.int32, device="cuda")
+    assert torch.equal(rs.expert_products(x, o, w), rs.expert_products(x.contiguous(), o, w.contiguous()))
+    g = normal(gen, (n, N), "bfloat16")
+    far = rs.expert_products_backward(g, o, w, x)
+    near = rs.expert_products_backward(g, o, w.contiguous(), x.contiguous())
+    assert torch.equal(far[0], near[0]) and torch.equal(far[1], near[1])
+
+
+def test_products_of_a_shard():
+    """A rank that holds few of the experts: most rows are other ranks', NaN here, and
+    results for them zeros, or left as they were."""
+    note("shard")
+    gen = generator(12)
+    n, E, N, K = 3000, 2, 264, 136
+    o = torch.tensor([0, 300, 430], dtype=torch.int32, device="cuda")
+    for dtype in DTYPES:
+        x, w = normal(gen, (n, K), dtype), normal(gen, (E, N, K), dtype)
+        want = rs.expert_products(x[:430].contiguous(), o, w)
+        x[430:] = float("nan")
+        got = rs.expert_products(x, o, w)
+        s = po.spans(o, E, n)
+        exact, size = po.product(x, s, w, torch.zeros(n, N, device="cuda"))
+        close(got, exact, po.product_bound(exact, size, K, dtype), "product")
+        close(want, exact[:430], po.product_bound(exact, size, K, dtype)[:430], "its rows alone")
+        held = torch.full((n, N + 1), 7.0, dtype=DTYPES[dtype], device="cuda")[:, 1:]
+        rs.expert_products(x, o, w, out=held)
+        assert torch.equal(held[:430], got[:430]) and (held[430:] == 7).all()
+
+
 # ---------------------------------------------------------------------------
 # 8 bits
 # ---------------------------------------------------------------------------

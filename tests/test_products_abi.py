@@ -20,7 +20,8 @@ def lib():
     return _lib.load()
 
 
-GROUPS = (dict(experts=0), dict(experts=1025), dict(experts=-1), dict(offsets=None), dict(offsets=B + 2), dict(rows_n=2**31))
+GROUPS = (dict(experts=0), dict(experts=1025), dict(experts=-1), dict(offsets=None), dict(offsets=B + 2), dict(rows_n=2**31),
+          dict(rows_n=2**30 + 1))
 
 
 def test_product_checks(lib):
@@ -115,6 +116,7 @@ def test_python_refuses_host_tensors():
 def test_constants_match_the_header():
     src = open(__file__.replace("tests/test_products_abi.py", "include/rs.h")).read()
     assert f"#define RS_SCALE_BLOCK {rs.SCALE_BLOCK}\n" in src
+    assert "#define RS_MAX_PRODUCT_ROWS ((size_t)1 << 30)\n" in src
 
 
 # The oracle itself.
