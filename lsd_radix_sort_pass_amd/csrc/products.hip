@@ -163,7 +163,7 @@ bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
         const size_t tiles = RAGGED_C
             ? align_to(parts(static_cast<size_t>(w.qn), rs::kWide) * p_tiles, rs::kXcds) * static_cast<size_t>(w.experts)
             : align_to((w.num_rows / rs::kWide + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1) * p_tiles,
-                       rs::kXcds);
+                       rs::kXcds) + rs::kXcds;  // (eighths of those of experts, and of none)
         wide = tiles <= (size_t{1} << 30) && feeds(w.q, w.q_stride, 0, Q_ACROSS ? w.qn : w.cn, Q_ACROSS, sizeof(T)) &&
                feeds(w.p, w.p_stride, w.p_expert, P_ACROSS ? w.pn : w.cn, P_ACROSS, sizeof(T));
         const auto go = [&](auto kernel) {
@@ -210,7 +210,8 @@ bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
     if (least < static_cast<int>(16 / sizeof(T))) {
         return go(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS, 1, true>);
     }
-    if (sizeof(T) < 4 && !aligned_rows(w)) {
+    // (Rows that take less than two steps are not worth the registers of a second.)
+    if (sizeof(T) < 4 && (!aligned_rows(w) || (RAGGED_C && w.num_rows < 128 * static_cast<size_t>(w.experts)))) {
         return go(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS, 1, false>);
     }
     return go(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS, 2, false>);

@@ -349,6 +349,37 @@ __device__ __forceinline__ void clear_tile(OUT *out, size_t stride, int width, R
 }
 
 // ---------------------------------------------------------------------------
+// A wave's results to rows: from its own part of LDS, which holds rows of 64 results of
+// 16 bits, their chunks exchanged, so that 8 lanes write 128 bytes of a row.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int result_at(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
+
+template <class OUT>
+__device__ __forceinline__ void rows_from_lds(const char *mine, OUT *out, size_t stride, int height, int q_first,
+                                              int q_rows, int p_first, int pn, int lane) {
+#pragma unroll 4
+    for (int k = 0; k < height / 8; ++k) {
+        const int row = 8 * k + (lane >> 3), chunk = lane & 7;
+        const i32x4 v = *reinterpret_cast<const i32x4 *>(mine + result_at(row, chunk));
+        const int qi = q_first + row, pi = p_first + 8 * chunk, have = pn - pi;
+        if (qi >= q_rows || have <= 0) continue;
+        OUT *to = out + static_cast<size_t>(qi) * stride + pi;
+        if (have >= 8) {
+            *reinterpret_cast<i32x4_any *>(to) = v;
+        } else {
+            union {
+                i32x4 all;
+                OUT e[8];
+            } u{v};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (e < have) to[e] = u.e[e];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
 // The product of any sizes, alignments and strides: SIDE x SIDE results a workgroup of
 // four waves, a quarter each; the loads of the next AHEAD steps are in flight while the
 // present one is multiplied.  Two take less time where rows begin at 16 bytes (1024 rows
@@ -362,11 +393,11 @@ template <class T>
 constexpr int kSquare = sizeof(T) == 4 ? 64 : 128;
 
 template <class T, class OUT, bool RAGGED_C, bool Q_ACROSS, bool P_ACROSS, int AHEAD, bool NARROW>
-__global__ __launch_bounds__(256, kSquare<T> == 64 ? 4 : 2) void product_kernel(const ProductWork<T, OUT> w) {
+__global__ __launch_bounds__(256, kSquare<T> == 64 ? 4 : sizeof(T) == 1 ? 2 : 4 - AHEAD) void product_kernel(const ProductWork<T, OUT> w) {
     constexpr bool kFp8 = std::is_same_v<T, fp8>;
     constexpr int SIDE = kSquare<T>, kHalf = SIDE / 2;
-    __shared__ __align__(16) char q_tile[SIDE * 128];
-    __shared__ __align__(16) char p_tile[SIDE * 128];
+    __shared__ __align__(16) char both_tiles[2 * SIDE * 128];
+    char *const q_tile = both_tiles, *const p_tile = both_tiles + SIDE * 128;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q_wave = (wave >> 1) * kHalf, p_wave = (wave & 1) * kHalf;
     const int num_rows = static_cast<int>(w.num_rows);
@@ -501,6 +532,28 @@ __global__ __launch_bounds__(256, kSquare<T> == 64 ? 4 : 2) void product_kernel(
                     if (c + kStep<T> < c_n) step(c + kStep<T>, second);
                 }
             }
+        }
+        if constexpr (sizeof(OUT) == 2) {
+            lds_barrier();  // (the tiles have been read)
+            char *mine = both_tiles + wave * 8192;
+            typedef OUT t4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+            for (int j = 0; j < kCount; ++j) {
+                const int row = kSide * j + lane % kSide;
+#pragma unroll
+                for (int i = 0; i < kCount; ++i) {
+#pragma unroll
+                    for (int a = 0; a < (sizeof(T) == 2 ? 4 : 1); ++a) {
+                        t4 v;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) v[r] = static_cast<OUT>(acc[i][j][4 * a + r]);
+                        const int p = kSide * i + 8 * a + 4 * (lane / kSide);
+                        *reinterpret_cast<t4 *>(mine + result_at(row, p / 8) + p % 8 * 2) = v;
+                    }
+                }
+            }
+            rows_from_lds(mine, out, w.out_stride, 64, q0 + q_wave, q_rows, p0 + p_wave, w.pn, lane);
+            continue;
         }
 #pragma unroll
         for (int j = 0; j < kCount; ++j) {

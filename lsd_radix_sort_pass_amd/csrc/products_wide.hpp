@@ -285,56 +285,73 @@ __device__ __forceinline__ void within(int local, int q_tiles, int p_tiles, Wide
     t.p = r / deep;
 }
 
-// Of ragged rows: block b of `grid` workgroups.
-__device__ inline WideTile wide_rows_tile(const int32_t *offsets, int experts, int num_rows, int height, int p_tiles,
-                                          bool clear, unsigned b) {
+// Of ragged rows: workgroup b's.  Every wave finds it by itself.  The tiles of rows of no
+// expert, which take no time to speak of, are shared out after the others.
+__device__ inline WideTile wide_rows_tile(const int32_t *offsets, int experts, int num_rows, int p_tiles, bool clear,
+                                          unsigned b) {
     WideTile t{-1, 0, 0, {0, num_rows}};
     const int lane = threadIdx.x & 63;
-    int all = 0, before = 0, from = num_rows;
-    if (offsets == nullptr) {
-        all = tiles_of(num_rows, height);
-    } else {
-        for (int base = 0; base < experts; base += 64) {
-            const RowSpan r = rows_of(offsets, base + lane < experts ? base + lane : experts - 1, num_rows);
-            const int tiles = base + lane < experts ? tiles_of(r.hi - r.lo, height) : 0;
-            all += __builtin_amdgcn_readlane(wave_prefix(tiles, lane), 63);
+    const unsigned xcd = b % kXcds;
+    unsigned at = b / kXcds, job = 0;
+    // Whether the workgroup's place on its XCD is within the share of `tiles` times
+    // p_tiles jobs; then `job` is its own, or there is none left (past).
+    bool past = false;
+    const auto takes = [&](int tiles) {
+        const unsigned jobs = static_cast<unsigned>(tiles) * static_cast<unsigned>(p_tiles);
+        const unsigned chunk = (jobs + kXcds - 1) / kXcds;
+        if (at >= chunk) {
+            at -= chunk;
+            return false;
         }
-        before = row_bound(offsets, 0, num_rows), from = row_bound(offsets, experts, num_rows);
-        from = from < before ? before : from;
-    }
-    const int rest = clear ? tiles_of(before + (num_rows - from), height) : 0;
-    const unsigned jobs = static_cast<unsigned>(all + rest) * static_cast<unsigned>(p_tiles);
-    const unsigned chunk = (jobs + kXcds - 1) / kXcds, at = b / kXcds;
-    unsigned job = b % kXcds * chunk + at;
-    if (at >= chunk || job >= jobs) return t;
+        job = xcd * chunk + at;
+        past = job >= jobs;
+        return !past;
+    };
     if (offsets == nullptr) {
-        t.expert = 0;
-        within(static_cast<int>(job), all, p_tiles, t);
+        const int all = tiles_of(num_rows, kWide);
+        if (takes(all)) {
+            t.expert = 0;
+            within(static_cast<int>(job), all, p_tiles, t);
+        }
         return t;
     }
-    if (job >= static_cast<unsigned>(all) * p_tiles) {
+    // Rows and tiles of up to 64 experts, a lane each, and the tiles up to it.
+    RowSpan r{0, 0};
+    int tiles = 0, upto = 0, all = 0;
+    const auto look = [&](int base) {
+        r = rows_of(offsets, base + lane < experts ? base + lane : experts - 1, num_rows);
+        tiles = base + lane < experts ? tiles_of(r.hi - r.lo, kWide) : 0;
+        upto = wave_prefix(tiles, lane);
+        return __builtin_amdgcn_readlane(upto, 63);
+    };
+    for (int base = 0; base < experts; base += 64) all += look(base);
+    if (takes(all)) {
+        const int tile = static_cast<int>(job / static_cast<unsigned>(p_tiles));
+        int gone = 0;
+        for (int base = 0; base < experts; base += 64) {
+            const int sum = experts <= 64 ? all : look(base);  // (up to 64: they are there)
+            if (tile - gone < sum) {
+                const int found = __ffsll(static_cast<unsigned long long>(__ballot(upto > tile - gone))) - 1;
+                const int first = gone + __builtin_amdgcn_readlane(upto - tiles, found);
+                t.expert = base + found;
+                t.rows = {__builtin_amdgcn_readlane(r.lo, found), __builtin_amdgcn_readlane(r.hi, found)};
+                within(static_cast<int>(job - static_cast<unsigned>(first) * static_cast<unsigned>(p_tiles)),
+                       __builtin_amdgcn_readlane(tiles, found), p_tiles, t);
+                return t;
+            }
+            gone += sum;
+        }
+        return t;
+    }
+    if (past || !clear) return t;
+    const int before = row_bound(offsets, 0, num_rows);
+    int from = row_bound(offsets, experts, num_rows);
+    from = from < before ? before : from;
+    const int rest = tiles_of(before + (num_rows - from), kWide);
+    if (takes(rest)) {
         t.expert = experts;
         t.rows = {before, from};
-        within(static_cast<int>(job - static_cast<unsigned>(all) * p_tiles), rest, p_tiles, t);
-        return t;
-    }
-    int tile = static_cast<int>(job / p_tiles);
-    for (int base = 0; base < experts; base += 64) {
-        const RowSpan r = rows_of(offsets, base + lane < experts ? base + lane : experts - 1, num_rows);
-        const int tiles = base + lane < experts ? tiles_of(r.hi - r.lo, height) : 0;
-        const int upto = wave_prefix(tiles, lane), sum = __builtin_amdgcn_readlane(upto, 63);
-        if (tile < sum) {
-            const int found = __ffsll(static_cast<unsigned long long>(__ballot(upto > tile))) - 1;
-            const int first = __builtin_amdgcn_readlane(upto - tiles, found);
-            t.expert = base + found;
-            t.rows = {__builtin_amdgcn_readlane(r.lo, found), __builtin_amdgcn_readlane(r.hi, found)};
-            // (Tiles before this chunk of experts are gone from `tile`, not from `job`.)
-            const unsigned gone = job / p_tiles - static_cast<unsigned>(tile);
-            within(static_cast<int>(job - (gone + first) * static_cast<unsigned>(p_tiles)),
-                   __builtin_amdgcn_readlane(tiles, found), p_tiles, t);
-            return t;
-        }
-        tile -= sum;
+        within(static_cast<int>(job), rest, p_tiles, t);
     }
     return t;
 }
@@ -351,33 +368,6 @@ __device__ inline WideTile wide_weights_tile(int experts, int q_tiles, int p_til
     return t;
 }
 
-// The results of a wave to rows: through its own 16 KiB of LDS, which hold 128 rows of
-// 64 results of 16 bits, so that 8 lanes write 128 bytes of a row.
-template <class OUT>
-__device__ __forceinline__ void rows_from_lds(const char *mine, OUT *out, size_t stride, int height, int q_first,
-                                              int q_rows, int p_first, int pn, int lane) {
-#pragma unroll 4
-    for (int k = 0; k < height / 8; ++k) {
-        const int row = 8 * k + (lane >> 3), chunk = lane & 7;
-        const i32x4 v = *reinterpret_cast<const i32x4 *>(mine + row * 128 + ((chunk ^ (row & 7)) << 4));
-        const int qi = q_first + row, pi = p_first + 8 * chunk, have = pn - pi;
-        if (qi >= q_rows || have <= 0) continue;
-        OUT *to = out + static_cast<size_t>(qi) * stride + pi;
-        if (have >= 8) {
-            *reinterpret_cast<i32x4_any *>(to) = v;
-        } else {
-            union {
-                i32x4 all;
-                OUT e[8];
-            } u{v};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (e < have) to[e] = u.e[e];
-            }
-        }
-    }
-}
-
 template <class T, bool RAGGED_C, bool Q_ACROSS, bool P_ACROSS>
 __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const ProductWork<T, T> w) {
     __shared__ __align__(1024) char ring[kWideLds];
@@ -390,7 +380,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
     int q_rows, c_n;
     const WideTile t = RAGGED_C
         ? wide_weights_tile(w.experts, (w.qn + kWide - 1) / kWide, p_tiles, blockIdx.x)
-        : wide_rows_tile(w.offsets, w.experts, num_rows, kWide, p_tiles, w.clear, blockIdx.x);
+        : wide_rows_tile(w.offsets, w.experts, num_rows, p_tiles, w.clear, blockIdx.x);
     if (t.expert < 0) return;
     const int q0 = t.q * kWide, p0 = t.p * kWide;
     if constexpr (RAGGED_C) {
@@ -597,7 +587,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[r] = static_cast<T>(acc[i][j][4 * a + r]);
                 const int chunk = 4 * i + a;
-                *reinterpret_cast<t4 *>(mine + row * 128 + ((chunk ^ (row & 7)) << 4) + (lane >> 5) * 8) = v;
+                *reinterpret_cast<t4 *>(mine + result_at(row, chunk) + (lane >> 5) * 8) = v;
             }
         }
     }
@@ -671,7 +661,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_fp8_kernel(const ProductWor
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int group = wave >> 2, p_wave = (wave & 3) * 64;
     const int num_rows = static_cast<int>(w.num_rows), p_tiles = (w.pn + kWide - 1) / kWide;
-    const WideTile t = wide_rows_tile(w.offsets, w.experts, num_rows, kWide, p_tiles, w.clear, blockIdx.x);
+    const WideTile t = wide_rows_tile(w.offsets, w.experts, num_rows, p_tiles, w.clear, blockIdx.x);
     if (t.expert < 0) return;
     const int q0 = t.q * kWide, p0 = t.p * kWide;
     OUT *out = w.out;
@@ -904,7 +894,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_fp8_kernel(const ProductWor
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[r] = static_cast<OUT>(acc[i][j][r]);
                 const int chunk = 2 * i + (lane >> 5);
-                *reinterpret_cast<t4 *>(mine + row * 128 + ((chunk ^ (row & 7)) << 4) + (lane >> 4 & 1) * 8) = v;
+                *reinterpret_cast<t4 *>(mine + result_at(row, chunk) + (lane >> 4 & 1) * 8) = v;
             }
         }
         rows_from_lds(mine, out, w.out_stride, height, q0 + q_wave, q_rows, p0 + p_wave, w.pn, lane);
