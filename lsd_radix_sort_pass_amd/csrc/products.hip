@@ -60,6 +60,11 @@ size_t align_to(size_t x, size_t by) { return (x + by - 1) / by * by; }
 
 size_t parts(size_t x, size_t by) { return (x + by - 1) / by; }
 
+// Workgroups of a launch whose tiles may be many: below 2^32 threads, all that a launch
+// counts to.
+constexpr size_t kMostTiles = size_t{1} << 22;
+static_assert(kMostTiles * rs::kWideThreads < size_t{1} << 32);
+
 // Whether the wide kernel can take an operand: its 16-byte chunks are aligned, a
 // tile spans less than 2^31 bytes, and a row has a chunk (across: whole ones).
 bool feeds(const void *p, size_t stride, size_t expert, int width, bool across, size_t elem) {
@@ -164,7 +169,7 @@ bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
             ? align_to(parts(static_cast<size_t>(w.qn), rs::kWide) * p_tiles, rs::kXcds) * static_cast<size_t>(w.experts)
             : align_to((w.num_rows / rs::kWide + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1) * p_tiles,
                        rs::kXcds) + rs::kXcds;  // (eighths of those of experts, and of none)
-        wide = tiles <= (size_t{1} << 30) && feeds(w.q, w.q_stride, 0, Q_ACROSS ? w.qn : w.cn, Q_ACROSS, sizeof(T)) &&
+        wide = tiles <= kMostTiles && feeds(w.q, w.q_stride, 0, Q_ACROSS ? w.qn : w.cn, Q_ACROSS, sizeof(T)) &&
                feeds(w.p, w.p_stride, w.p_expert, P_ACROSS ? w.pn : w.cn, P_ACROSS, sizeof(T));
         const auto go = [&](auto kernel) {
             return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] {
@@ -190,8 +195,10 @@ bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
     }
     if constexpr (!RAGGED_C && !P_ACROSS) {
         const Estimate e(w);
-        // (Workgroups of 65536 rows and 2^20 channels at most: below 2^31.)
-        if (w.cn >= static_cast<int>(16 / sizeof(T)) && w.num_rows <= 65536 &&
+        // (A strip and up to 1024 threads, or where strips are many two and 256.)
+        const size_t strips = parts(static_cast<size_t>(w.pn), 16) *
+            (w.num_rows / 16 + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1);
+        if (w.cn >= static_cast<int>(16 / sizeof(T)) && w.num_rows <= 65536 && strips <= 4 * kMostTiles &&
             (wide || e.few(w.pn, !aligned_rows(w)) < e.square(w.pn))) {
             return launch_few(w, e, stream);
         }
@@ -203,7 +210,7 @@ bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
     const size_t q_tiles = RAGGED_C
         ? parts(static_cast<size_t>(w.qn), kSide) * static_cast<size_t>(w.experts)
         : w.num_rows / kSide + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1;
-    const unsigned grid = static_cast<unsigned>(std::min<size_t>(q_tiles * p_tiles, size_t{1} << 24));
+    const unsigned grid = static_cast<unsigned>(std::min<size_t>(q_tiles * p_tiles, kMostTiles));
     const auto go = [&](auto kernel) {
         return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] { run_kernel(kernel, grid, 256, stream, w); });
     };

@@ -233,6 +233,35 @@ def test_products_far_offsets_of_tiles():
     assert torch.equal(far[0], near[0]) and torch.equal(far[1], near[1])
 
 
+@pytest.mark.parametrize("dtype,N,K", [("bfloat16", 1 << 19, 8), ("float32", 1 << 20, 1)])
+def test_products_of_many_tiles(dtype, N, K):
+    """More tiles than a launch has workgroups: a row of each of 1024 experts, which share
+    one matrix.  Small whole numbers, whose sums are exact."""
+    note(f"many tiles {dtype}")
+    gen = generator(11)
+    E = 1024
+    x = torch.randint(-2, 3, (E, K), generator=gen, device="cuda").to(DTYPES[dtype])
+    w = torch.randint(-2, 3, (1, N, K), generator=gen, device="cuda").to(DTYPES[dtype])
+    o = torch.arange(E + 1, dtype=torch.int32, device="cuda")
+    got = rs.expert_products(x, o, w.expand(E, N, K))
+    for first in range(0, N, 1 << 16):
+        part = slice(first, first + (1 << 16))
+        want = sum(x[:, k, None].float() * w[0, part, k].float() for k in range(K))
+        assert torch.equal(got[:, part].float(), want)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_products_of_one_operand_twice(dtype):
+    """Rows that are their results' gradient as well."""
+    note(f"one operand twice {dtype}")
+    gen = generator(13)
+    n, E, N = 700, 2, 264
+    x, w = normal(gen, (n, N), dtype), normal(gen, (E, N, N), dtype)
+    o = torch.tensor([0, 300, 690], dtype=torch.int32, device="cuda")
+    twice, once = rs.expert_products_backward(x, o, w, x), rs.expert_products_backward(x, o, w, x.clone())
+    assert torch.equal(twice[0], once[0]) and torch.equal(twice[1], once[1])
+
+
 def test_products_of_a_shard():
     """A rank that holds few of the experts: most rows are other ranks', NaN here, and
     results for them zeros, or left as they were."""
