@@ -207,12 +207,16 @@ bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
     constexpr size_t kSide = rs::kSquare<T>;
     const size_t p_tiles = parts(static_cast<size_t>(w.pn), kSide);
     // Each expert's last tile may be a part, and so may that of the rows of none.
-    const size_t q_tiles = RAGGED_C
-        ? parts(static_cast<size_t>(w.qn), kSide) * static_cast<size_t>(w.experts)
-        : w.num_rows / kSide + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1;
-    const unsigned grid = static_cast<unsigned>(std::min<size_t>(q_tiles * p_tiles, kMostTiles));
+    const size_t jobs = RAGGED_C
+        ? align_to(parts(static_cast<size_t>(w.qn), kSide) * p_tiles, rs::kXcds) * static_cast<size_t>(w.experts)
+        : align_to((w.num_rows / kSide + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1) * p_tiles,
+                   rs::kXcds) + rs::kXcds;
+    if (jobs > size_t{1} << 31) return false;  // (whose results no memory holds)
+    rs::ProductWork<T, OUT> work = w;
+    work.jobs = static_cast<unsigned>(jobs);
+    const unsigned grid = static_cast<unsigned>(std::min(jobs, kMostTiles));
     const auto go = [&](auto kernel) {
-        return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] { run_kernel(kernel, grid, 256, stream, w); });
+        return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] { run_kernel(kernel, grid, 256, stream, work); });
     };
     if (least < static_cast<int>(16 / sizeof(T))) {
         return go(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS, 1, true>);

@@ -52,6 +52,7 @@ struct ProductWork {
     int experts;
     int qn, pn, cn;  // widths; of the ragged one of qn and cn: 0
     bool clear;      // write zeros to the rows of no expert
+    unsigned jobs;   // tiles at most (of the square ones, which workgroups take in turn)
 };
 
 // ---------------------------------------------------------------------------
@@ -119,6 +120,111 @@ __device__ inline RowTile find_tile(const int32_t *offsets, int experts, int num
     const int before = row_bound(offsets, 0, num_rows), end = row_bound(offsets, experts, num_rows);
     const int from = end < before ? before : end;
     return {t < tiles_of(before + (num_rows - from), height) ? experts : -1, t, {before, from}};
+}
+
+// ---------------------------------------------------------------------------
+// Which tile a workgroup takes.  Consecutive workgroups go to the eight XCDs in
+// turn, each with an L2 of its own: XCD x takes tiles that stand together.  Within an
+// expert they go over kTurn tiles of q, then p, so that the 32 workgroups of an XCD share
+// both operands.
+// ---------------------------------------------------------------------------
+constexpr int kXcds = 8;
+constexpr int kTurn = 4;
+
+struct ResultTile {
+    int expert;  // -1: none; `experts`: rows of no expert
+    int q, p;    // tiles
+    RowSpan rows;
+};
+
+__device__ __forceinline__ void within(int local, int q_tiles, int p_tiles, ResultTile &t) {
+    const int turn = local / (kTurn * p_tiles), left = q_tiles - turn * kTurn, r = local - turn * kTurn * p_tiles;
+    const int deep = left < kTurn ? left : kTurn;
+    t.q = turn * kTurn + r % deep;
+    t.p = r / deep;
+}
+
+// Of ragged rows: workgroup b's.  Every wave finds it by itself.  The tiles of rows of no
+// expert, which take no time to speak of, are shared out after the others.
+__device__ inline ResultTile rows_tile(const int32_t *offsets, int experts, int num_rows, int height, int p_tiles,
+                                      bool clear, unsigned b) {
+    ResultTile t{-1, 0, 0, {0, num_rows}};
+    const int lane = threadIdx.x & 63;
+    const unsigned xcd = b % kXcds;
+    unsigned at = b / kXcds, job = 0;
+    // Whether the workgroup's place on its XCD is within the share of `tiles` times
+    // p_tiles jobs; then `job` is its own, or there is none left (past).
+    bool past = false;
+    const auto takes = [&](int tiles) {
+        const unsigned jobs = static_cast<unsigned>(tiles) * static_cast<unsigned>(p_tiles);
+        const unsigned chunk = (jobs + kXcds - 1) / kXcds;
+        if (at >= chunk) {
+            at -= chunk;
+            return false;
+        }
+        job = xcd * chunk + at;
+        past = job >= jobs;
+        return !past;
+    };
+    if (offsets == nullptr) {
+        const int all = tiles_of(num_rows, height);
+        if (takes(all)) {
+            t.expert = 0;
+            within(static_cast<int>(job), all, p_tiles, t);
+        }
+        return t;
+    }
+    // Rows and tiles of up to 64 experts, a lane each, and the tiles up to it.
+    RowSpan r{0, 0};
+    int tiles = 0, upto = 0, all = 0;
+    const auto look = [&](int base) {
+        r = rows_of(offsets, base + lane < experts ? base + lane : experts - 1, num_rows);
+        tiles = base + lane < experts ? tiles_of(r.hi - r.lo, height) : 0;
+        upto = wave_prefix(tiles, lane);
+        return __builtin_amdgcn_readlane(upto, 63);
+    };
+    for (int base = 0; base < experts; base += 64) all += look(base);
+    if (takes(all)) {
+        const int tile = static_cast<int>(job / static_cast<unsigned>(p_tiles));
+        int gone = 0;
+        for (int base = 0; base < experts; base += 64) {
+            const int sum = experts <= 64 ? all : look(base);  // (up to 64: they are there)
+            if (tile - gone < sum) {
+                const int found = __ffsll(static_cast<unsigned long long>(__ballot(upto > tile - gone))) - 1;
+                const int first = gone + __builtin_amdgcn_readlane(upto - tiles, found);
+                t.expert = base + found;
+                t.rows = {__builtin_amdgcn_readlane(r.lo, found), __builtin_amdgcn_readlane(r.hi, found)};
+                within(static_cast<int>(job - static_cast<unsigned>(first) * static_cast<unsigned>(p_tiles)),
+                       __builtin_amdgcn_readlane(tiles, found), p_tiles, t);
+                return t;
+            }
+            gone += sum;
+        }
+        return t;
+    }
+    if (past || !clear) return t;
+    const int before = row_bound(offsets, 0, num_rows);
+    int from = row_bound(offsets, experts, num_rows);
+    from = from < before ? before : from;
+    const int rest = tiles_of(before + (num_rows - from), height);
+    if (takes(rest)) {
+        t.expert = experts;
+        t.rows = {before, from};
+        within(static_cast<int>(job), rest, p_tiles, t);
+    }
+    return t;
+}
+
+// Of the weights' gradient: every expert has the same tiles.
+__device__ inline ResultTile weights_tile(int experts, int q_tiles, int p_tiles, unsigned b) {
+    ResultTile t{-1, 0, 0, {0, 0}};
+    const unsigned tiles = static_cast<unsigned>(q_tiles) * static_cast<unsigned>(p_tiles);
+    const unsigned chunk = (tiles + kXcds - 1) / kXcds, e = b / (chunk * kXcds), local = b % (chunk * kXcds);
+    const unsigned job = local % kXcds * chunk + local / kXcds;
+    if (e >= static_cast<unsigned>(experts) || job >= tiles) return t;
+    t.expert = static_cast<int>(e);
+    within(static_cast<int>(job), q_tiles, p_tiles, t);
+    return t;
 }
 
 // ---------------------------------------------------------------------------
@@ -402,44 +508,35 @@ __global__ __launch_bounds__(256, kSquare<T> == 64 ? 4 : sizeof(T) == 1 ? 2 : 4 
     const int q_wave = (wave >> 1) * kHalf, p_wave = (wave & 1) * kHalf;
     const int num_rows = static_cast<int>(w.num_rows);
 
-    const unsigned p_tiles = static_cast<unsigned>((w.pn + SIDE - 1) / SIDE);
-    const unsigned q_tiles = RAGGED_C ? static_cast<unsigned>((w.qn + SIDE - 1) / SIDE) : 0;
-    for (size_t job = blockIdx.x;; job += gridDim.x) {
+    const int p_tiles = (w.pn + SIDE - 1) / SIDE, q_tiles = (w.qn + SIDE - 1) / SIDE;
+    for (unsigned job = blockIdx.x; job < w.jobs; job += gridDim.x) {
+        const ResultTile t = RAGGED_C ? weights_tile(w.experts, q_tiles, p_tiles, job)
+                                      : rows_tile(w.offsets, w.experts, num_rows, SIDE, p_tiles, w.clear, job);
+        if (t.expert < 0) continue;
+        const int q0 = t.q * SIDE, p0 = t.p * SIDE, expert = t.expert;
         const T *q = w.q, *p = w.p;
         OUT *out = w.out;
-        int q0, q_rows, c_n, expert;
-        const int p0 = static_cast<int>(job % p_tiles) * SIDE;
-        int first_row = 0;
+        int q_rows, c_n, first_row = 0;
         if constexpr (RAGGED_C) {
-            const size_t t = job / p_tiles, e = t / q_tiles;
-            if (e >= static_cast<size_t>(w.experts)) break;
-            expert = static_cast<int>(e);
-            q0 = static_cast<int>(t % q_tiles) * SIDE;
-            q_rows = w.qn;
             const RowSpan r = rows_of(w.offsets, expert, num_rows);
+            q_rows = w.qn;
             c_n = r.hi - r.lo;
             q += static_cast<size_t>(r.lo) * w.q_stride;
             p += static_cast<size_t>(r.lo) * w.p_stride;
-            out += e * w.out_expert;
+            out += static_cast<size_t>(expert) * w.out_expert;
         } else {
-            const size_t t = job / p_tiles;
-            if (t > 0x7FFFFFFFu) break;
-            const RowTile f = find_tile(w.offsets, w.experts, num_rows, SIDE, static_cast<int>(t));
-            if (f.expert < 0) break;
-            expert = f.expert;
             if (expert == w.experts) {
-                if (!w.clear) break;
-                clear_tile(out, w.out_stride, w.pn, f, SIDE, num_rows, p0, SIDE);
+                clear_tile(out, w.out_stride, w.pn, RowTile{expert, t.q, t.rows}, SIDE, num_rows, p0, SIDE);
                 continue;
             }
-            q0 = f.tile * SIDE;
-            q_rows = f.rows.hi - f.rows.lo;
+            q_rows = t.rows.hi - t.rows.lo;
             c_n = w.cn;
-            first_row = f.rows.lo;
+            first_row = t.rows.lo;
             q += static_cast<size_t>(first_row) * w.q_stride;
             out += static_cast<size_t>(first_row) * w.out_stride;
             p += static_cast<size_t>(expert) * w.p_expert;
         }
+        if (static_cast<unsigned>(q0) >= static_cast<unsigned>(q_rows) || p0 >= w.pn) continue;
 
         // In 16 bits 32 x 32 results an instruction, else 16 x 16.
         constexpr int kSide = sizeof(T) == 2 ? 32 : 16, kCount = kHalf / kSide;

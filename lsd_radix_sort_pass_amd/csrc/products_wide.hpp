@@ -263,111 +263,6 @@ struct Feeder {
     }
 };
 
-// ---------------------------------------------------------------------------
-// Which tile a workgroup takes.  Consecutive workgroups go to the eight XCDs in
-// turn, each with an L2 of its own: XCD x takes tiles that stand together.  Within an
-// expert they go over kTurn tiles of q, then p, so that the 32 workgroups of an XCD share
-// both operands.
-// ---------------------------------------------------------------------------
-constexpr int kXcds = 8;
-constexpr int kTurn = 4;
-
-struct WideTile {
-    int expert;  // -1: none; `experts`: rows of no expert
-    int q, p;    // tiles
-    RowSpan rows;
-};
-
-__device__ __forceinline__ void within(int local, int q_tiles, int p_tiles, WideTile &t) {
-    const int turn = local / (kTurn * p_tiles), left = q_tiles - turn * kTurn, r = local - turn * kTurn * p_tiles;
-    const int deep = left < kTurn ? left : kTurn;
-    t.q = turn * kTurn + r % deep;
-    t.p = r / deep;
-}
-
-// Of ragged rows: workgroup b's.  Every wave finds it by itself.  The tiles of rows of no
-// expert, which take no time to speak of, are shared out after the others.
-__device__ inline WideTile wide_rows_tile(const int32_t *offsets, int experts, int num_rows, int p_tiles, bool clear,
-                                          unsigned b) {
-    WideTile t{-1, 0, 0, {0, num_rows}};
-    const int lane = threadIdx.x & 63;
-    const unsigned xcd = b % kXcds;
-    unsigned at = b / kXcds, job = 0;
-    // Whether the workgroup's place on its XCD is within the share of `tiles` times
-    // p_tiles jobs; then `job` is its own, or there is none left (past).
-    bool past = false;
-    const auto takes = [&](int tiles) {
-        const unsigned jobs = static_cast<unsigned>(tiles) * static_cast<unsigned>(p_tiles);
-        const unsigned chunk = (jobs + kXcds - 1) / kXcds;
-        if (at >= chunk) {
-            at -= chunk;
-            return false;
-        }
-        job = xcd * chunk + at;
-        past = job >= jobs;
-        return !past;
-    };
-    if (offsets == nullptr) {
-        const int all = tiles_of(num_rows, kWide);
-        if (takes(all)) {
-            t.expert = 0;
-            within(static_cast<int>(job), all, p_tiles, t);
-        }
-        return t;
-    }
-    // Rows and tiles of up to 64 experts, a lane each, and the tiles up to it.
-    RowSpan r{0, 0};
-    int tiles = 0, upto = 0, all = 0;
-    const auto look = [&](int base) {
-        r = rows_of(offsets, base + lane < experts ? base + lane : experts - 1, num_rows);
-        tiles = base + lane < experts ? tiles_of(r.hi - r.lo, kWide) : 0;
-        upto = wave_prefix(tiles, lane);
-        return __builtin_amdgcn_readlane(upto, 63);
-    };
-    for (int base = 0; base < experts; base += 64) all += look(base);
-    if (takes(all)) {
-        const int tile = static_cast<int>(job / static_cast<unsigned>(p_tiles));
-        int gone = 0;
-        for (int base = 0; base < experts; base += 64) {
-            const int sum = experts <= 64 ? all : look(base);  // (up to 64: they are there)
-            if (tile - gone < sum) {
-                const int found = __ffsll(static_cast<unsigned long long>(__ballot(upto > tile - gone))) - 1;
-                const int first = gone + __builtin_amdgcn_readlane(upto - tiles, found);
-                t.expert = base + found;
-                t.rows = {__builtin_amdgcn_readlane(r.lo, found), __builtin_amdgcn_readlane(r.hi, found)};
-                within(static_cast<int>(job - static_cast<unsigned>(first) * static_cast<unsigned>(p_tiles)),
-                       __builtin_amdgcn_readlane(tiles, found), p_tiles, t);
-                return t;
-            }
-            gone += sum;
-        }
-        return t;
-    }
-    if (past || !clear) return t;
-    const int before = row_bound(offsets, 0, num_rows);
-    int from = row_bound(offsets, experts, num_rows);
-    from = from < before ? before : from;
-    const int rest = tiles_of(before + (num_rows - from), kWide);
-    if (takes(rest)) {
-        t.expert = experts;
-        t.rows = {before, from};
-        within(static_cast<int>(job), rest, p_tiles, t);
-    }
-    return t;
-}
-
-// Of the weights' gradient: every expert has the same tiles.
-__device__ inline WideTile wide_weights_tile(int experts, int q_tiles, int p_tiles, unsigned b) {
-    WideTile t{-1, 0, 0, {0, 0}};
-    const unsigned tiles = static_cast<unsigned>(q_tiles) * static_cast<unsigned>(p_tiles);
-    const unsigned chunk = (tiles + kXcds - 1) / kXcds, e = b / (chunk * kXcds), local = b % (chunk * kXcds);
-    const unsigned job = local % kXcds * chunk + local / kXcds;
-    if (e >= static_cast<unsigned>(experts) || job >= tiles) return t;
-    t.expert = static_cast<int>(e);
-    within(static_cast<int>(job), q_tiles, p_tiles, t);
-    return t;
-}
-
 template <class T, bool RAGGED_C, bool Q_ACROSS, bool P_ACROSS>
 __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const ProductWork<T, T> w) {
     __shared__ __align__(1024) char ring[kWideLds];
@@ -378,9 +273,9 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
     const T *q = w.q, *p = w.p;
     T *out = w.out;
     int q_rows, c_n;
-    const WideTile t = RAGGED_C
-        ? wide_weights_tile(w.experts, (w.qn + kWide - 1) / kWide, p_tiles, blockIdx.x)
-        : wide_rows_tile(w.offsets, w.experts, num_rows, p_tiles, w.clear, blockIdx.x);
+    const ResultTile t = RAGGED_C
+        ? weights_tile(w.experts, (w.qn + kWide - 1) / kWide, p_tiles, blockIdx.x)
+        : rows_tile(w.offsets, w.experts, num_rows, kWide, p_tiles, w.clear, blockIdx.x);
     if (t.expert < 0) return;
     const int q0 = t.q * kWide, p0 = t.p * kWide;
     if constexpr (RAGGED_C) {
@@ -661,7 +556,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_fp8_kernel(const ProductWor
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int group = wave >> 2, p_wave = (wave & 3) * 64;
     const int num_rows = static_cast<int>(w.num_rows), p_tiles = (w.pn + kWide - 1) / kWide;
-    const WideTile t = wide_rows_tile(w.offsets, w.experts, num_rows, p_tiles, w.clear, blockIdx.x);
+    const ResultTile t = rows_tile(w.offsets, w.experts, num_rows, kWide, p_tiles, w.clear, blockIdx.x);
     if (t.expert < 0) return;
     const int q0 = t.q * kWide, p0 = t.p * kWide;
     OUT *out = w.out;
