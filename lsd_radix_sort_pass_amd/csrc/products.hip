@@ -7,6 +7,7 @@
 #include "launch.hpp"
 #include "products.hpp"
 #include "products_few.hpp"
+#include "products_split.hpp"
 #include "products_wide.hpp"
 
 // Named here, as the host's pass does not emit all of those that only calls within
@@ -82,54 +83,81 @@ bool aligned_rows(const rs::ProductWork<T, OUT> &w) {
 }
 
 // ---------------------------------------------------------------------------
-// Which kernel takes a product of rows, by estimates of their times in us (with 4
-// to 6 for the launch and its beginning).  The experts are taken to have equally
-// many rows.
+// Which kernel takes a product, by estimates of their times in us (with 4 to 6 for the
+// launch and its beginning).  The experts are taken to have equally many rows.
 //
 // Tiles go round the 256 CUs: the wide kernel's stage of 128 bytes of c takes 0.55 us, as
 // long as its loads are on their way, and more for a tile full of rows; but
-// memory gives no more than 6 TB/s.  The kernel for few rows reads weights at 5 to
-// 6 TB/s, and its rows again for each of its strips, at 6.5 TB/s, or 1.1 if they do not
-// begin at 16 bytes (in float32 it multiplies at 75 TFLOP/s).  Square tiles take 0.85 us for 128 bytes of c, and 1.5 if two share
-// every CU; of 64 x 64 in float32 1, and 0.52 of a CU's time.
-// Measured, in us, wide / few rows / square (bfloat16, rows x experts x out x in):
-// 8 of 64 x 2048 x 2048 24 / 12 / 32, 512 of 64 x 4096 x 4096 346 / 424 / -, 16 of one x
-// 8192 x 8192 75 / 28 / 107, 128 of one 95 / 88 / 101, 256 of one 154 / 172 / 102, 300 of 16
-// x 2048 x 2048 27 / 33 / 33, 512 of 8 x 1024 x 1024 16 / 10 / 18, 2048 of 8 26 / 26 / 19,
-// 1000 of 7 x 1001 x 1537 - / 79 / 34, 40 of 7 - / 18 / 34;
-// e4m3 256 of 128 x 2048 x 4096 166 / 143 / 310.
+// memory gives no more than 6 TB/s; a tile of the weights' gradient, whose stages are few, begins
+// and ends in 6 (3.5 for two square ones).  The kernel for few rows reads weights at 5 to
+// 6 TB/s, and its rows again for each of its strips, at 25.4 GB/s a CU, or 4.3 if they do not
+// begin at 16 bytes (in float32 it multiplies at 75 TFLOP/s).  Square tiles take 0.85 us for
+// 128 bytes of c, 1.25 if rows do not begin at 16 bytes, and 1.5 if two share
+// every CU; of 64 x 64 in float32 1, and 0.52 of a CU's time.  Tiles whose contraction is split
+// take 1.4 us for eight times 128 bytes on half of the CUs and 1.75 on all, in 8 bits 2.2 and 2.6, where
+// rows do not begin at 16 bytes 1.9 and 3.
+// Measured, in us, wide / few rows / square / split (bfloat16, rows x experts x out x in):
+// 8 of 64 x 2048 x 2048 24 / 12 / 32 / -, 512 of 64 x 4096 x 4096 346 / 424 / - / -, 16 of one x
+// 8192 x 8192 75 / 28 / 107 / -, 128 of one 95 / 88 / 101 / 33, 256 of one 154 / 172 / 102 / 62,
+// 300 of 16 x 2048 x 2048 27 / 33 / 33 / 24, 512 of 8 x 1024 x 1024 16 / 10 / 18 / 8, 2048 of 8 26 / 26 / 15 / -,
+// 1000 of 7 x 1001 x 1537 - / 79 / 34 / 27, 40 of 7 - / 18 / 34 / 15, 5003 of 7 - / - / 41 / 78,
+// 64 of one x 1024 x 8192 - / 38 / - / 28, 256 of one x 4096 x 4096 - / - / 46 / 20;
+// e4m3 256 of 128 x 2048 x 4096 166 / 143 / 310 / -, 128 of one x 4096 x 8192 - / 28 / - / 24; rows' gradient,
+// 128 of one x 4096 x 4096 52 / - / - / 19; weights' gradient, 8192 of one x 1024 x 1024 172 / - / - / 34, 9076 of
+// 2 x 128 x 512 - / - / 58 / 18, 4096 of 8 x 1024 x 1024 20 / - / 18 / 41, 16384 of 64 x 1024 x 2048 128 / - / 167 / -.
 // ---------------------------------------------------------------------------
+constexpr double kTwoStrips = 512;  // workgroups of few_rows_kernel, of one strip, from which on they take two
+
 struct Estimate {
-    double rows_each, experts_used, weight_bytes, stages;
+    double rows_each, experts_used, weight_bytes, stages, pn;
     bool bytes, words;  // operands of 8, of 32 bits
+    bool apart;         // rows that do not begin at 16 bytes
+    bool ragged_c;
 
     template <class T, class OUT>
-    explicit Estimate(const rs::ProductWork<T, OUT> &w) : bytes(sizeof(T) == 1), words(sizeof(T) == 4) {
+    Estimate(const rs::ProductWork<T, OUT> &w, bool of_weights)
+        : pn(w.pn), bytes(sizeof(T) == 1), words(sizeof(T) == 4), apart(!aligned_rows(w)), ragged_c(of_weights) {
         const double n = static_cast<double>(w.num_rows), e = static_cast<double>(w.experts);
+        if (ragged_c) {
+            experts_used = e, rows_each = w.qn;
+            weight_bytes = e * w.pn * w.qn * static_cast<double>(sizeof(T));
+            stages = std::ceil(n / e * static_cast<double>(sizeof(T)) / 128);
+            return;
+        }
         experts_used = std::max(1.0, e * (1.0 - std::exp(-n / e)));  // by rows that choose at random
         rows_each = n / experts_used;
         weight_bytes = experts_used * w.pn * w.cn * static_cast<double>(sizeof(T));
         stages = static_cast<double>(parts(static_cast<size_t>(w.cn) * sizeof(T), 128));
     }
-    double tiles(double height, double width, double pn) const {
+    double tiles(double height, double width) const {
         return experts_used * std::ceil(rows_each / height) * std::ceil(pn / width);
     }
-    double wide(double pn) const {
-        const double t = tiles(rs::kWide, rs::kWide, pn);
+    double wide() const {
+        const double t = tiles(rs::kWide, rs::kWide);
         const double stage = 0.55 + (t > 128 ? 1.1 : 0.65) * std::min(1.0, rows_each / rs::kWide);
-        return 6 + std::max(std::ceil(t / 256) * stages * stage, weight_bytes / (bytes ? 5.5e6 : 6e6));
+        return 6 + std::max(std::ceil(t / 256) * (stages * stage + (ragged_c ? 6 : 0)), weight_bytes / (bytes ? 5.5e6 : 6e6));
     }
-    // apart: rows that do not begin at 16 bytes.
-    double few(double pn, bool apart) const {
+    int few_rows() const { return rows_each <= 12 ? 1 : rows_each <= 28 ? 2 : 4; }  // 16 of them each
+    double few() const {
         const double weights = weight_bytes / (bytes ? 6e6 : 5.2e6);
-        const double passes = experts_used * rows_each * stages * std::ceil(pn / 32);  // of 128 bytes of a row
-        const double rows = passes * (apart ? 128 / 1.1e6 : words ? 2.0 * 32 * 32 / 75e6 : 128 / 6.5e6);
+        const int height = 16 * few_rows();
+        const double groups = tiles(height, 16) >= kTwoStrips ? tiles(height, 32) : tiles(height, 16);
+        const double taken = (std::min(rows_each, 1.0 * height) + height) / 2;  // (loads of rows that do not exist count half)
+        double rows = std::ceil(groups / 256) * taken * stages * 128 / (apart ? 4.3e3 : 25.4e3);
+        if (words) rows = std::max(rows, experts_used * rows_each * stages * std::ceil(pn / 32) * 2.0 * 32 * 32 / 75e6);
         return 4 + std::max(weights, rows) + 0.25 * std::min(weights, rows);
     }
-    double square(double pn) const {
-        const double t = words ? tiles(64, 64, pn) : tiles(128, 128, pn);
-        const double step = words ? std::max(1.0, 0.52 * t / 256) : t <= 256 ? 0.85 : 1.5 * std::ceil(t / 512);
-        return 4 + std::max(stages * step, weight_bytes / 3.5e6);
+    double square() const {
+        const double t = words ? tiles(64, 64) : tiles(128, 128);
+        const double alone = apart ? 1.25 : 0.85;
+        const double step = words ? std::max(1.0, 0.52 * t / 256) : t <= 256 ? alone : 1.5 * std::ceil(t / 512);
+        const double ends = ragged_c && t > 256 ? 3.5 * std::ceil(t / 512) : 0;
+        return 4 + std::max(stages * step + ends, weight_bytes / 3.5e6);
+    }
+    double split() const {
+        const double t = tiles(rs::kSplitSide, rs::kSplitSide);
+        const double step = t <= 128 ? (apart ? 1.9 : bytes ? 2.2 : 1.4) : (apart ? 3.0 : bytes ? 2.6 : 1.75);
+        return 4 + std::max(std::ceil(t / 256) * (std::ceil(stages / rs::kSplitWaves) * step + 2), weight_bytes / 3.5e6);
     }
 };
 
@@ -149,78 +177,75 @@ bool launch_few(const rs::ProductWork<T, OUT> &w, const Estimate &e, hipStream_t
             });
         };
         const size_t strips = parts(static_cast<size_t>(w.pn), 16);
-        const double groups = e.tiles(16 * R, 16, w.pn);
-        if (groups >= 512) return go(rs::few_rows_kernel<T, OUT, 4, 2, R>, 4, parts(strips, 2));
+        const double groups = e.tiles(16 * R, 16);
+        if (groups >= kTwoStrips) return go(rs::few_rows_kernel<T, OUT, 4, 2, R>, 4, parts(strips, 2));
         constexpr int kWaves = R == 4 ? 8 : 16;  // (16 would have registers for a step at a time)
         return go(rs::few_rows_kernel<T, OUT, kWaves, 1, R>, kWaves, strips);
     };
-    if (e.rows_each <= 12) return with_rows(IntC<1>{});
-    if (e.rows_each <= 28) return with_rows(IntC<2>{});
+    if (e.few_rows() == 1) return with_rows(IntC<1>{});
+    if (e.few_rows() == 2) return with_rows(IntC<2>{});
     return with_rows(IntC<4>{});
 }
 
 // Enqueues the product of w, whose results are q by p (RAGGED_C: of each expert).
 template <class T, class OUT, bool RAGGED_C, bool Q_ACROSS, bool P_ACROSS>
 bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
-    bool wide = false;
+    const int least = std::min(Q_ACROSS ? w.qn : w.cn, P_ACROSS ? w.pn : w.cn);  // width of a row
+    // Tiles of `side` results, or of rows of none, at most.  Each expert's last tile may be a part, and
+    // so may that of the rows of none; eighths of either go to an XCD.
+    const auto jobs_of = [&](size_t side) {
+        const size_t p_tiles = parts(static_cast<size_t>(w.pn), side);
+        return RAGGED_C
+            ? align_to(parts(static_cast<size_t>(w.qn), side) * p_tiles, rs::kXcds) * static_cast<size_t>(w.experts)
+            : align_to((w.num_rows / side + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1) * p_tiles,
+                       rs::kXcds) + rs::kXcds;
+    };
+    const Estimate e(w, RAGGED_C);
+    constexpr double kNever = 1e30;
+    const bool chunks = least >= static_cast<int>(16 / sizeof(T));  // a row has 16 bytes
+    const double square = e.square();
+    double wide = kNever, few = kNever, split = kNever;
     if constexpr (sizeof(T) <= 2) {
-        const size_t p_tiles = parts(static_cast<size_t>(w.pn), rs::kWide);
-        const size_t tiles = RAGGED_C
-            ? align_to(parts(static_cast<size_t>(w.qn), rs::kWide) * p_tiles, rs::kXcds) * static_cast<size_t>(w.experts)
-            : align_to((w.num_rows / rs::kWide + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1) * p_tiles,
-                       rs::kXcds) + rs::kXcds;  // (eighths of those of experts, and of none)
-        wide = tiles <= kMostTiles && feeds(w.q, w.q_stride, 0, Q_ACROSS ? w.qn : w.cn, Q_ACROSS, sizeof(T)) &&
-               feeds(w.p, w.p_stride, w.p_expert, P_ACROSS ? w.pn : w.cn, P_ACROSS, sizeof(T));
-        const auto go = [&](auto kernel) {
-            return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] {
-                run_kernel(kernel, static_cast<unsigned>(tiles), rs::kWideThreads, stream, w);
-            });
-        };
-        if constexpr (RAGGED_C) {
-            // Below a stage of rows, what counts is that results are written from many CUs.
-            if (wide && w.num_rows >= 64 * static_cast<size_t>(w.experts) && w.pn > 128 && w.qn > 128) {
-                return go(rs::wide_product_kernel<T, true, true, true>);
-            }
-        } else {
-            const Estimate e(w);
-            if (wide && e.wide(w.pn) > e.square(w.pn)) wide = false;
-            if (wide && (P_ACROSS || e.wide(w.pn) <= e.few(w.pn, false))) {
-                if constexpr (sizeof(T) == 1) {
-                    return go(rs::wide_fp8_kernel<OUT>);
-                } else {
-                    return go(rs::wide_product_kernel<T, RAGGED_C, Q_ACROSS, P_ACROSS>);
-                }
-            }
+        // (Below a stage of rows, what counts for the weights' gradient is that it is written from many CUs.)
+        if (jobs_of(rs::kWide) <= kMostTiles && feeds(w.q, w.q_stride, 0, Q_ACROSS ? w.qn : w.cn, Q_ACROSS, sizeof(T)) &&
+            feeds(w.p, w.p_stride, w.p_expert, P_ACROSS ? w.pn : w.cn, P_ACROSS, sizeof(T)) &&
+            (!RAGGED_C || w.num_rows >= 64 * static_cast<size_t>(w.experts))) {
+            wide = e.wide();
         }
+        // (In float32 a CU's matrix units are busy with one tile of 64 x 64.)
+        if (chunks && jobs_of(rs::kSplitSide) <= kMostTiles) split = e.split();
     }
     if constexpr (!RAGGED_C && !P_ACROSS) {
-        const Estimate e(w);
         // (A strip and up to 1024 threads, or where strips are many two and 256.)
         const size_t strips = parts(static_cast<size_t>(w.pn), 16) *
             (w.num_rows / 16 + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1);
-        if (w.cn >= static_cast<int>(16 / sizeof(T)) && w.num_rows <= 65536 && strips <= 4 * kMostTiles &&
-            (wide || e.few(w.pn, !aligned_rows(w)) < e.square(w.pn))) {
-            return launch_few(w, e, stream);
+        if (chunks && w.num_rows <= 65536 && strips <= 4 * kMostTiles) few = e.few();
+        if (few <= std::min({wide, square, split})) return launch_few(w, e, stream);
+    }
+    const auto launch = [&](auto kernel, size_t grid, int threads, const auto &work) {
+        return launch_kernel(RS_KERNEL_PRODUCT, stream,
+                             [&] { run_kernel(kernel, static_cast<unsigned>(grid), threads, stream, work); });
+    };
+    if constexpr (sizeof(T) <= 2) {
+        if (wide <= std::min(square, split)) {
+            if constexpr (sizeof(T) == 1) {
+                return launch(rs::wide_fp8_kernel<OUT>, jobs_of(rs::kWide), rs::kWideThreads, w);
+            } else {
+                return launch(rs::wide_product_kernel<T, RAGGED_C, Q_ACROSS, P_ACROSS>, jobs_of(rs::kWide),
+                              rs::kWideThreads, w);
+            }
+        }
+        if (split < square) {
+            return launch(rs::split_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS>, jobs_of(rs::kSplitSide),
+                          64 * rs::kSplitWaves, w);
         }
     }
-    const int least = std::min(Q_ACROSS ? w.qn : w.cn, P_ACROSS ? w.pn : w.cn);  // width of a row
-    constexpr size_t kSide = rs::kSquare<T>;
-    const size_t p_tiles = parts(static_cast<size_t>(w.pn), kSide);
-    // Each expert's last tile may be a part, and so may that of the rows of none.
-    const size_t jobs = RAGGED_C
-        ? align_to(parts(static_cast<size_t>(w.qn), kSide) * p_tiles, rs::kXcds) * static_cast<size_t>(w.experts)
-        : align_to((w.num_rows / kSide + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1) * p_tiles,
-                   rs::kXcds) + rs::kXcds;
+    const size_t jobs = jobs_of(rs::kSquare<T>);
     if (jobs > size_t{1} << 31) return false;  // (whose results no memory holds)
     rs::ProductWork<T, OUT> work = w;
     work.jobs = static_cast<unsigned>(jobs);
-    const unsigned grid = static_cast<unsigned>(std::min(jobs, kMostTiles));
-    const auto go = [&](auto kernel) {
-        return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] { run_kernel(kernel, grid, 256, stream, work); });
-    };
-    if (least < static_cast<int>(16 / sizeof(T))) {
-        return go(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS, 1, true>);
-    }
+    const auto go = [&](auto kernel) { return launch(kernel, std::min(jobs, kMostTiles), 256, work); };
+    if (!chunks) return go(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS, 1, true>);
     // (Rows that take less than two steps are not worth the registers of a second.)
     if (sizeof(T) < 4 && (!aligned_rows(w) || (RAGGED_C && w.num_rows < 128 * static_cast<size_t>(w.experts)))) {
         return go(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS, 1, false>);

@@ -290,6 +290,7 @@ template <class T, int SIDE, bool ACROSS>
 __device__ __forceinline__ int tile_at(int row, int chunk) {
     const int turn = !ACROSS ? row >> 1 & 7
         : sizeof(T) == 4     ? (row >> 2 & 3) << 2
+        : SIDE == 64         ? (row >> 1 & 1) << 2
                              : (row & 3) << 2;
     return row * (kChunksPerRow<T, SIDE, ACROSS> * 16) + ((chunk ^ turn) << 4);
 }
@@ -345,14 +346,14 @@ __device__ __forceinline__ i32x4 cut(i32x4 raw, int at, int width) {
 }
 
 // A tile's elements on their way from memory through registers to LDS, for
-// operands of any alignment, width and stride, by 256 threads.  The loads are clamped
+// operands of any alignment, width and stride, by THREADS of them.  The loads are clamped
 // into range, without a branch between them, and what they should not have read is
 // cleared before it is stored.  NARROW: rows of less than 16 bytes, element by element.
-template <class T, int SIDE, bool ACROSS, bool NARROW>
+template <class T, int SIDE, bool ACROSS, bool NARROW, int THREADS = 256>
 struct Staging {
     static constexpr int V = 16 / static_cast<int>(sizeof(T));
     static constexpr int kChunks = kChunksPerRow<T, SIDE, ACROSS>;
-    static constexpr int kLoads = SIDE / 32;
+    static constexpr int kLoads = SIDE * 8 / THREADS;
     const T *from[kLoads];  // along: the row; across: the column
     size_t stride;
     int rows, width, first;  // of the operand's matrix, and the tile's first row (along) or column (across)
@@ -361,7 +362,7 @@ struct Staging {
         stride = stride_, rows = rows_, width = width_, first = first_;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int id = i * 256 + tid;
+            const int id = i * THREADS + tid;
             if constexpr (ACROSS) {
                 const int c = first + id % kChunks * V;
                 from[i] = base + (NARROW ? 0 : c < width - V ? c : width - V);
@@ -376,7 +377,7 @@ struct Staging {
     __device__ __forceinline__ void load(i32x4 (&raw)[kLoads], int c, int tid) const {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int id = i * 256 + tid;
+            const int id = i * THREADS + tid;
             const T *p = from[i];
             int at = ACROSS ? first + id % kChunks * V : c + id % kChunks * V;
             if constexpr (ACROSS) {
@@ -407,7 +408,7 @@ struct Staging {
         if (!whole) {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const int id = i * 256 + tid;
+                const int id = i * THREADS + tid;
                 if constexpr (!NARROW) raw[i] = cut<T>(raw[i], (ACROSS ? first : c) + id % kChunks * V, width);
                 // (Rows of the other kind hold results of their own, which are not stored.)
                 if (ACROSS && c + id / kChunks >= rows) raw[i] = i32x4{0, 0, 0, 0};
@@ -415,7 +416,7 @@ struct Staging {
         }
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int id = i * 256 + tid;
+            const int id = i * THREADS + tid;
             *reinterpret_cast<i32x4 *>(tile + tile_at<T, SIDE, ACROSS>(id / kChunks, id % kChunks)) = raw[i];
         }
     }
@@ -489,11 +490,12 @@ __device__ __forceinline__ void rows_from_lds(const char *mine, OUT *out, size_t
 // The product of any sizes, alignments and strides: SIDE x SIDE results a workgroup of
 // four waves, a quarter each; the loads of the next AHEAD steps are in flight while the
 // present one is multiplied.  Two take less time where rows begin at 16 bytes (1024 rows
-// 4096 x 4096 bfloat16 57 us, 69 with one), but more where they do not, as the 32 KiB cache has to hold the lines that two steps share (4003
-// rows of 7 experts 1001 x 1537 float16 52 us, 45 with one).  SIDE is 128 in 16 and 8 bits, 64
-// takes up to 1.7 times as long; in 32 bits, where the matrix instructions take eight
+// 4096 x 4096 bfloat16 55 us, 69 with one), but more where they do not, as the 32 KiB cache
+// has to hold the lines that two steps share (4003 rows of 7 experts 1001 x 1537 float16 47 us,
+// 39 with one; steps of 256 bytes 45; loads of the whole 16-byte words that hold them 65).
+// SIDE is 128 in 16 and 8 bits; in 32 bits, where the matrix instructions take eight
 // times as long, 64 fills the CUs more evenly: the gradients of 4093 rows of 8 experts
-// 515 x 1030 119 us, 169 with 128.
+// 515 x 1030 112 us, 169 with 128.
 // ---------------------------------------------------------------------------
 template <class T>
 constexpr int kSquare = sizeof(T) == 4 ? 64 : 128;

@@ -233,6 +233,36 @@ def test_products_far_offsets_of_tiles():
     assert torch.equal(far[0], near[0]) and torch.equal(far[1], near[1])
 
 
+# (rows, experts, N, K): few results and a long contraction, whole steps of it, a rest, and
+# less than the eight waves have steps; rows whose starts are aligned and not.
+LONG = [(70, 1, 130, 4100), (33, 2, 72, 2048), (200, 3, 65, 1537), (40, 1, 264, 520), (129, 1, 8, 8192)]
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("n,E,N,K", LONG)
+def test_products_long_contraction(n, E, N, K, dtype):
+    note(f"long contraction {dtype} n={n} E={E} N={N} K={K}")
+    gen = generator(n + N + K)
+    o = offsets_of(n, E, "holes")
+    s = po.spans(o, E, n)
+    x, w = normal(gen, (n, K), dtype), normal(gen, (E, N, K), dtype)
+    exact, size = po.product(x, s, w, torch.zeros(n, N, device="cuda"))
+    close(rs.expert_products(x, o, w), exact, po.product_bound(exact, size, K, dtype), "product")
+    # The same lengths the other way round: the rows' gradient over K outputs ...
+    g, w = normal(gen, (n, K), dtype), normal(gen, (E, K, N), dtype)
+    exact, size = po.product(g, s, w.transpose(1, 2), torch.zeros(n, N, device="cuda"))
+    close(rs.expert_products_backward(g, o, w), exact, po.product_bound(exact, size, K, dtype), "gradient of rows")
+    # ... and the weights' over K rows.
+    o = offsets_of(K, E, "holes")
+    s = po.spans(o, E, K)
+    g, x = normal(gen, (K, n), dtype), normal(gen, (K, N), dtype)
+    exact, size = po.product_weights_backward(g, s, x)
+    got = rs.expert_products_backward(g, o, rows=x)
+    close(got, exact, po.product_bound(exact, size, K, dtype), "gradient of weights")
+    g[:int(o[0])], x[int(o[-1]):] = float("nan"), float("inf")      # rows of no expert
+    assert torch.equal(rs.expert_products_backward(g, o, rows=x), got)
+
+
 @pytest.mark.parametrize("dtype,N,K", [("bfloat16", 1 << 19, 8), ("float32", 1 << 20, 1)])
 def test_products_of_many_tiles(dtype, N, K):
     """More tiles than a launch has workgroups: a row of each of 1024 experts, which share
