@@ -89,20 +89,21 @@ bool aligned_rows(const rs::ProductWork<T, OUT> &w) {
 // Tiles go round the 256 CUs: the wide kernel's stage of 128 bytes of c takes 0.55 us, as
 // long as its loads are on their way, and more for a tile full of rows; but
 // memory gives no more than 6 TB/s; a tile of the weights' gradient, whose stages are few, begins
-// and ends in 6 (3.5 for two square ones).  The kernel for few rows reads weights at 5 to
+// and ends in 6 (3.5 for two square ones), one of 8 bits in 4.  The kernel for few rows reads weights at 5 to
 // 6 TB/s, and its rows again for each of its strips, at 25.4 GB/s a CU, or 4.3 if they do not
 // begin at 16 bytes (in float32 it multiplies at 75 TFLOP/s).  Square tiles take 0.85 us for
 // 128 bytes of c, 1.25 if rows do not begin at 16 bytes, and 1.5 if two share
-// every CU; of 64 x 64 in float32 1, and 0.52 of a CU's time.  Tiles whose contraction is split
-// take 1.4 us for eight times 128 bytes on half of the CUs and 1.75 on all, in 8 bits 2.2 and 2.6, where
-// rows do not begin at 16 bytes 1.9 and 3.
+// every CU, in 8 bits 1.4 and 2.6; of 64 x 64 in float32 1, and 0.52 of a CU's time.  Tiles whose
+// contraction is split take 1.4 us for eight times 128 bytes on half of the CUs and 1.75 on all, in 8 bits
+// 2.2, 2.6 and, if they are many, 3.3, where rows do not begin at 16 bytes 1.9 and 3.
 // Measured, in us, wide / few rows / square / split (bfloat16, rows x experts x out x in):
 // 8 of 64 x 2048 x 2048 24 / 12 / 32 / -, 512 of 64 x 4096 x 4096 346 / 424 / - / -, 16 of one x
 // 8192 x 8192 75 / 28 / 107 / -, 128 of one 95 / 88 / 101 / 33, 256 of one 154 / 172 / 102 / 62,
 // 300 of 16 x 2048 x 2048 27 / 33 / 33 / 24, 512 of 8 x 1024 x 1024 16 / 10 / 18 / 8, 2048 of 8 26 / 26 / 15 / -,
 // 1000 of 7 x 1001 x 1537 - / 79 / 34 / 27, 40 of 7 - / 18 / 34 / 15, 5003 of 7 - / - / 41 / 78,
 // 64 of one x 1024 x 8192 - / 38 / - / 28, 256 of one x 4096 x 4096 - / - / 46 / 20;
-// e4m3 256 of 128 x 2048 x 4096 166 / 143 / 310 / -, 128 of one x 4096 x 8192 - / 28 / - / 24; rows' gradient,
+// e4m3 256 of 128 x 2048 x 4096 166 / 143 / 310 / -, 128 of one x 4096 x 8192 - / 28 / - / 24,
+// 2042 of 4 x 896 x 2176 - / - / 27 / 18, 4000 of 8 x 1024 x 2048 36 / - / 28 / -, 25412 of 89 x 321 x 640 34 / - / 30 / -; rows' gradient,
 // 128 of one x 4096 x 4096 52 / - / - / 19; weights' gradient, 8192 of one x 1024 x 1024 172 / - / - / 34, 9076 of
 // 2 x 128 x 512 - / - / 58 / 18, 4096 of 8 x 1024 x 1024 20 / - / 18 / 41, 16384 of 64 x 1024 x 2048 128 / - / 167 / -.
 // ---------------------------------------------------------------------------
@@ -134,8 +135,9 @@ struct Estimate {
     }
     double wide() const {
         const double t = tiles(rs::kWide, rs::kWide);
-        const double stage = 0.55 + (t > 128 ? 1.1 : 0.65) * std::min(1.0, rows_each / rs::kWide);
-        return 6 + std::max(std::ceil(t / 256) * (stages * stage + (ragged_c ? 6 : 0)), weight_bytes / (bytes ? 5.5e6 : 6e6));
+        const double full = bytes ? (t > 128 ? 1.45 : 1.0) : t > 128 ? 1.1 : 0.65;
+        const double stage = 0.55 + full * std::min(1.0, rows_each / rs::kWide), ends = ragged_c ? 6 : bytes ? 4 : 0;
+        return 6 + std::max(std::ceil(t / 256) * (stages * stage + ends), weight_bytes / (bytes ? 5.5e6 : 6e6));
     }
     int few_rows() const { return rows_each <= 12 ? 1 : rows_each <= 28 ? 2 : 4; }  // 16 of them each
     double few() const {
@@ -149,14 +151,15 @@ struct Estimate {
     }
     double square() const {
         const double t = words ? tiles(64, 64) : tiles(128, 128);
-        const double alone = apart ? 1.25 : 0.85;
-        const double step = words ? std::max(1.0, 0.52 * t / 256) : t <= 256 ? alone : 1.5 * std::ceil(t / 512);
+        const double alone = bytes ? 1.4 : apart ? 1.25 : 0.85, two = bytes ? 2.6 : 1.5;
+        const double step = words ? std::max(1.0, 0.52 * t / 256) : t <= 256 ? alone : two * std::ceil(t / 512);
         const double ends = ragged_c && t > 256 ? 3.5 * std::ceil(t / 512) : 0;
         return 4 + std::max(stages * step + ends, weight_bytes / 3.5e6);
     }
     double split() const {
         const double t = tiles(rs::kSplitSide, rs::kSplitSide);
-        const double step = t <= 128 ? (apart ? 1.9 : bytes ? 2.2 : 1.4) : (apart ? 3.0 : bytes ? 2.6 : 1.75);
+        const double some = apart ? 1.9 : bytes ? 2.2 : 1.4, all = apart ? 3.0 : bytes ? 2.6 : 1.75;
+        const double step = t <= 128 ? some : bytes && t > 512 ? 3.3 : all;
         return 4 + std::max(std::ceil(t / 256) * (std::ceil(stages / rs::kSplitWaves) * step + 2), weight_bytes / 3.5e6);
     }
 };
