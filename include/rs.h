@@ -457,8 +457,8 @@ rs_status rs_expert_products_fp8(const uint8_t *rows, const float *row_scales, s
                                  hipStream_t stream);
 
 /* Such operands: with m the largest size of the finite elements of a block, but at
- * least 2^-100, its scale is m / 448 and its elements are e4m3(x * (448 / m)),
- * to nearest even; NaN and infinities become NaN.  all: rows of no expert
+ * least 2^-100, its scale is m * (1 / 448) and its elements are e4m3(x / scale), each
+ * step rounded to float32, all to nearest even; NaN and infinities become NaN.  all: rows of no expert
  * become zeros with the scale of such a block.  out of rs_quantize_weights is
  * contiguous. */
 rs_status rs_quantize_rows(const void *rows, int dtype, size_t num_rows, int width, size_t rows_stride,

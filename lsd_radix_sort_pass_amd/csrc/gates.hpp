@@ -129,9 +129,9 @@ __global__ __launch_bounds__(kGateBlock) void gate_kernel(const GateWork w, cons
 
 // ---------------------------------------------------------------------------
 // Rows to 8 bits.  A block of 128 elements has scale m / 448, m its largest
-// finite size, at least 2^-100 (so that no scale is 0 and no product of two
-// overflows its inverse), and each element becomes e4m3(x * (448 / m)); what is
-// not finite becomes NaN.
+// finite size, at least 2^-100 (so that no scale is 0 and each has an inverse),
+// and each element becomes e4m3(x / scale), the quotient rounded once to float32
+// before; what is not finite becomes NaN.
 // ---------------------------------------------------------------------------
 constexpr float kFp8Max = 448.0f;
 constexpr float kLeastMax = 0x1p-100f;
@@ -141,20 +141,42 @@ __device__ __forceinline__ float finite_size(float x) {
     return a < __builtin_inff() ? a : 0.0f;
 }
 
+// A block's scale, by which its elements are divided.  x / scale comes out of the
+// rounded inverse y by two corrections q += (x - q scale) y: the first leaves q within a
+// step of the quotient, and the second rounds it correctly then (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990),
+// as long as the remainder is exact: where the scale is small, x and scale are taken 2^64
+// times as large, so that remainders of quotients from 2^-11 on stay normal.  (A product
+// with the inverse alone is a step of float32 away, and of bfloat16 rows, whose quotients
+// often stand halfway between two e4m3, one element in 500 came out a step of e4m3 away.)
+struct BlockScale {
+    float scale, up, divisor, inverse;
+
+    // m / 448 as a product, as a division by a number is on tensors.
+    __device__ __forceinline__ explicit BlockScale(float most) : scale(most * (1.0f / kFp8Max)) {
+        up = scale < 0x1p-64f ? 0x1p64f : 1.0f;
+        divisor = scale * up;
+        inverse = 1.0f / divisor;
+    }
+    // At most 448 and a few steps, which are 448 in e4m3; NaN of what is not finite.
+    __device__ __forceinline__ float quotient(float x) const {
+        const float a = x * up;
+        float q = a * inverse;
+        q = __builtin_fmaf(__builtin_fmaf(-q, divisor, a), inverse, q);
+        q = __builtin_fmaf(__builtin_fmaf(-q, divisor, a), inverse, q);
+        return __builtin_copysignf(q, x);  // (of -0 as well)
+    }
+};
+
 // Two e4m3 in bits 0..15 of a word (HI: 16..31 of `old`), rounded to nearest even.
 template <bool HI>
-__device__ __forceinline__ int pack_fp8(float a, float b, float inverse, int old) {
-    const auto one = [&](float x) {
-        const float v = x * inverse;
-        const float c = __builtin_fminf(__builtin_fmaxf(v, -kFp8Max), kFp8Max);
-        return __builtin_fabsf(x) < __builtin_inff() ? c : __builtin_nanf("");
-    };
-    return __builtin_amdgcn_cvt_pk_fp8_f32(one(a), one(b), old, HI);
+__device__ __forceinline__ int pack_fp8(float a, float b, const BlockScale &s, int old) {
+    return __builtin_amdgcn_cvt_pk_fp8_f32(s.quotient(a), s.quotient(b), old, HI);
 }
 
-__device__ __forceinline__ uint2 pack8_fp8(const float (&f)[8], float inverse) {
-    const int lo = pack_fp8<true>(f[2], f[3], inverse, pack_fp8<false>(f[0], f[1], inverse, 0));
-    const int hi = pack_fp8<true>(f[6], f[7], inverse, pack_fp8<false>(f[4], f[5], inverse, 0));
+__device__ __forceinline__ uint2 pack8_fp8(const float (&f)[8], const BlockScale &s) {
+    const int lo = pack_fp8<true>(f[2], f[3], s, pack_fp8<false>(f[0], f[1], s, 0));
+    const int hi = pack_fp8<true>(f[6], f[7], s, pack_fp8<false>(f[4], f[5], s, 0));
     return {static_cast<uint32_t>(lo), static_cast<uint32_t>(hi)};
 }
 
@@ -237,10 +259,11 @@ __global__ __launch_bounds__(kGateBlock) void quantize_rows_kernel(const GateWor
                 most = __builtin_fmaxf(most, finite_size(f[j][i]));
             }
             most = group_max<16>(most);
-            const uint2 v = pack8_fp8(f[j], kFp8Max / most);
+            const BlockScale scale(most);
+            const uint2 v = pack8_fp8(f[j], scale);
             if (have > 0) {
                 store8_fp8(static_cast<uint8_t *>(w.out) + r * w.out_stride + c, have, v);
-                if (g == 0) w.scales[static_cast<size_t>(first + j) * w.num_rows + r] = most / kFp8Max;
+                if (g == 0) w.scales[static_cast<size_t>(first + j) * w.num_rows + r] = scale.scale;
             }
         }
     }
@@ -283,12 +306,13 @@ __global__ __launch_bounds__(kGateBlock) void quantize_weights_kernel(const Quan
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kGateBlock / 64; ++i) most = __builtin_fmaxf(most, found[i]);
-        if (threadIdx.x == 0) w.scales[job] = most / kFp8Max;
+        const BlockScale scale(most);
+        if (threadIdx.x == 0) w.scales[job] = scale.scale;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int r = r0 + 16 * j + sub;
             if (r < w.rows && c < w.width) {
-                store8_fp8(w.out + (e * w.rows + r) * w.width + c, w.width - c, pack8_fp8(f[j], kFp8Max / most));
+                store8_fp8(w.out + (e * w.rows + r) * w.width + c, w.width - c, pack8_fp8(f[j], scale));
             }
         }
     }

@@ -1,0 +1,87 @@
+"""GPU tests of what rows and weights become in 8 bits, to the bit, and of the
+accuracy of products of 8-bit operands."""
+import pytest
+
+torch = pytest.importorskip("torch")
+rs = pytest.importorskip("lsd_radix_sort_pass_amd")
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"float32": torch.float32, "float16": torch.float16, "bfloat16": torch.bfloat16}
+FP8 = torch.float8_e4m3fn
+
+
+def note(msg):
+    print(f"\n[case] {msg}", flush=True)
+
+
+def eight_bits(blocks):
+    """(bits, scales) of blocks (count, size) in float32 on the host: the largest
+    size times 1 / 448, and quotients.  Those of two float32 numbers that are rounded to
+    float64 and then to float32 are the correctly rounded ones (53 >= 2 * 24 + 2 bits)."""
+    size = torch.where(blocks.isfinite(), blocks.abs(), torch.zeros_like(blocks))
+    scale = size.amax(1).clamp(min=2.0 ** -100) * torch.tensor(1.0 / 448, dtype=torch.float32)
+    quotient = (blocks.double() / scale.double()[:, None]).float()
+    bits = quotient.clamp(-448, 448).to(FP8).view(torch.uint8)
+    return torch.where(blocks.isfinite(), bits, torch.full_like(bits, 0x7F)), scale
+
+
+def same(bits, want):
+    """Whether 8-bit values are the same, NaN of either sign."""
+    nan = (want & 0x7F) == 0x7F
+    return bool((((bits & 0x7F) == 0x7F) == nan).all() and torch.equal(bits[~nan], want[~nan]))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("n,K", [(700, 128), (400, 640), (300, 200), (64, 3)])
+def test_quantize_rows_divide_by_the_scale(n, K, dtype):
+    """Numbers of few digits, whose quotients often stand halfway between two
+    e4m3, in blocks of all magnitudes."""
+    note(f"quantize bits {dtype} n={n} K={K}")
+    gen = torch.Generator().manual_seed(n + K)
+    whole = torch.randint(-64, 65, (n, K), generator=gen).float()
+    top = {"float16": 8, "bfloat16": 120, "float32": 120}[dtype]
+    x = whole * torch.exp2(torch.randint(-top - 10, top + 1, (n, 1), generator=gen).float())
+    x[:n // 4] = torch.randn(n // 4, K, generator=gen)
+    x[0] = 0
+    x[1, 0], x[2, K - 1], x[3, K // 2] = float("nan"), float("inf"), float("-inf")
+    x[4] = float(torch.finfo(DTYPES[dtype]).max)
+    x = x.to(DTYPES[dtype])
+    got = rs.quantize_rows(x.cuda())
+    for b in range(0, K, 128):
+        bits, scale = eight_bits(x[:, b:b + 128].float())
+        assert torch.equal(got.scales[b // 128].cpu(), scale)
+        assert same(got.values.view(torch.uint8)[:, b:b + 128].cpu(), bits), f"block {b}"
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_quantize_weights_divide_by_the_scale(dtype):
+    note(f"quantize weights bits {dtype}")
+    gen = torch.Generator().manual_seed(3)
+    E, N, K = 5, 200, 300
+    w = torch.randint(-64, 65, (E, N, K), generator=gen).float()
+    w *= torch.exp2(torch.tensor([0.0, 8.0, -14.0, -30.0, -110.0]))[:, None, None]      # (float16 loses the last two)
+    w = w.to(DTYPES[dtype])
+    got = rs.quantize_weights(w.cuda())
+    for e in range(E):
+        for a in range(0, N, 128):
+            for b in range(0, K, 128):
+                part = w[e, a:a + 128, b:b + 128].float()
+                bits, scale = eight_bits(part.reshape(1, -1))
+                assert float(got.scales[e, a // 128, b // 128]) == float(scale[0])
+                have = got.values.view(torch.uint8)[e, a:a + 128, b:b + 128].cpu().reshape(1, -1)
+                assert same(have, bits), (e, a, b)
+
+
+def test_gate_quantize_rows_divide_by_the_scale():
+    """Gated rows that are exact: silu(64) is 64 in float32, times a number of few digits."""
+    note("gate_quantize bits")
+    gen = torch.Generator().manual_seed(4)
+    b = torch.randint(-64, 65, (300, 256), generator=gen).float()
+    x = torch.cat([torch.full_like(b, 64.0), b], 1)
+    for dtype in DTYPES.values():
+        got = rs.gate_quantize_rows(x.to(dtype).cuda())
+        for k in (0, 128):
+            bits, scale = eight_bits(64.0 * b[:, k:k + 128])
+            assert torch.equal(got.scales[k // 128].cpu(), scale)
+            assert same(got.values.view(torch.uint8)[:, k:k + 128].cpu(), bits)
