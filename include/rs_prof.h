@@ -94,8 +94,8 @@ size_t rs_prof_header_offset(int which);
 /* Per-launch durations recorded while timing was on (after folding the
  * pending events as rs_prof_summary does): the milliseconds of every launch
  * of `kind` whose tag equals `sub` (pass launches are tagged with their pass
- * index 0..7, every other launch with -1; sub < 0 selects every launch of
- * the kind), in launch order.  Copies up to `cap` of them into `ms` (which
+ * index 0..7, products as at rs_prof_product_kernel, every other launch with
+ * -1; sub < 0 selects every launch of the kind), in launch order.  Copies up to `cap` of them into `ms` (which
  * may be NULL) and returns how many there are (0 for a bad kind). */
 size_t rs_prof_samples(int kind, int sub, double *ms, size_t cap);
 
@@ -139,6 +139,24 @@ int rs_prof_ranker(int mode);
  * failed. */
 rs_status rs_prof_lds_rank_probe(const uint32_t *digits, uint32_t *ranks, int blocks, int slots, int unit,
                                  hipStream_t stream);
+
+/* Kernels of the experts' products (rs_expert_products, its gradients and _fp8). */
+typedef enum rs_product_kernel {
+    RS_PRODUCT_SQUARE = 1, /* any sizes, alignments and strides */
+    RS_PRODUCT_FEW = 2,    /* few rows an expert */
+    RS_PRODUCT_SPLIT = 3,  /* few results with a long contraction */
+    RS_PRODUCT_WIDE = 4    /* many rows an expert */
+} rs_product_kernel;
+
+/* The kernel that products take: 0 lets the library choose by the sizes, an
+ * rs_product_kernel is taken wherever it can serve the call's type, sizes and
+ * alignment (elsewhere the library chooses); other values mean 0.  Returns the
+ * previous setting.  Launches of RS_KERNEL_PRODUCT are tagged for
+ * rs_prof_samples with the kernel, that for few rows with RS_PRODUCT_FEW + 16 *
+ * (rows of its tile / 16) + 256 * (output channels / 16).  Tests force each
+ * kernel, so that all of them are covered whatever the sizes.  Not thread-safe
+ * against concurrent calls. */
+int rs_prof_product_kernel(int kernel);
 
 /* Copy n 32-bit words from in to out (device pointers, 4-byte aligned, not
  * overlapping) on `stream`.  Uses 16-byte accesses when both pointers are

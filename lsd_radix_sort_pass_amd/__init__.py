@@ -34,6 +34,7 @@ __all__ = [
     "copy_u32", "prof_enable", "prof_reset", "prof_summary", "prof_small_path", "library_path",
     "error_word", "skipped_passes", "order_flag", "prof_tile_items", "sort_keys_u32_noalloc",
     "NOALLOC_MAX_KEYS", "DeviceGuardError", "prof_samples", "prof_force_giveup", "lds_rank_probe", "prof_ranker",
+    "prof_product_kernel",
     "MAX_CHOICES", "MAX_EXPERTS", "ExpertOrder", "route_topk", "route_topk_backward", "temp_bytes_experts",
     "sort_experts", "dispatch_rows", "dispatch_rows_backward", "combine_rows", "combine_rows_backward",
     "SCALE_BLOCK", "Quantized", "expert_products", "expert_products_backward", "expert_products_fp8", "gate_quantize_rows",
@@ -362,6 +363,13 @@ def prof_ranker(mode: int) -> int:
     ballot match ranker (32-bit keys, experts; see rs_prof_ranker).  Returns the
     previous mode."""
     return int(_lib.load().rs_prof_ranker(int(mode)))
+
+
+def prof_product_kernel(kernel: int) -> int:
+    """Kernel of the experts' products: 0 the library's choice, else an
+    rs_product_kernel where it can serve the call (see
+    rs_prof_product_kernel).  Returns the previous setting."""
+    return int(_lib.load().rs_prof_product_kernel(int(kernel)))
 
 
 def prof_force_giveup(on: bool) -> bool:

@@ -28,6 +28,11 @@ RS_KERNEL_GATE = 10
 RS_KERNEL_QUANTIZE = 11
 RS_KERNEL_KINDS = 12
 
+RS_PRODUCT_SQUARE = 1
+RS_PRODUCT_FEW = 2
+RS_PRODUCT_SPLIT = 3
+RS_PRODUCT_WIDE = 4
+
 # Every function the two public headers declare, with its ctypes signature.
 _VP = ctypes.c_void_p
 _SZ = ctypes.c_size_t
@@ -98,6 +103,7 @@ SIGNATURES = {
     "rs_prof_samples": (_SZ, [_I, _I, ctypes.POINTER(ctypes.c_double), _SZ]),
     "rs_prof_force_giveup": (_I, [_I]),
     "rs_prof_ranker": (_I, [_I]),
+    "rs_prof_product_kernel": (_I, [_I]),
     "rs_prof_lds_rank_probe": (_I, [_VP, _VP, _I, _I, _I, _VP]),
 }
 

@@ -25,6 +25,8 @@ template __global__ void rs::wide_fp8_kernel<rs::bf16>(const rs::ProductWork<rs:
 
 namespace {
 
+int g_product_kernel = 0;  // rs_prof_product_kernel: 0 automatic, else an rs_product_kernel where it can serve
+
 constexpr int kMaxWidth = RS_MAX_ROW_WIDTH;
 constexpr size_t kMaxExpertStride = size_t{1} << 50;
 
@@ -174,16 +176,16 @@ bool launch_few(const rs::ProductWork<T, OUT> &w, const Estimate &e, hipStream_t
     const auto with_rows = [&](auto rows) {
         constexpr int R = decltype(rows)::value;
         const size_t q_tiles = w.num_rows / (16 * R) + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1;
-        const auto go = [&](auto kernel, int waves, size_t p_tiles) {
+        const auto go = [&](auto kernel, int waves, int strips_each, size_t p_tiles) {
             return launch_kernel(RS_KERNEL_PRODUCT, stream, [&] {
                 run_kernel(kernel, static_cast<unsigned>(q_tiles * p_tiles), 64 * waves, stream, w);
-            });
+            }, RS_PRODUCT_FEW + 16 * R + 256 * strips_each);
         };
         const size_t strips = parts(static_cast<size_t>(w.pn), 16);
         const double groups = e.tiles(16 * R, 16);
-        if (groups >= kTwoStrips) return go(rs::few_rows_kernel<T, OUT, 4, 2, R>, 4, parts(strips, 2));
+        if (groups >= kTwoStrips) return go(rs::few_rows_kernel<T, OUT, 4, 2, R>, 4, 2, parts(strips, 2));
         constexpr int kWaves = R == 4 ? 8 : 16;  // (16 would have registers for a step at a time)
-        return go(rs::few_rows_kernel<T, OUT, kWaves, 1, R>, kWaves, strips);
+        return go(rs::few_rows_kernel<T, OUT, kWaves, 1, R>, kWaves, 1, strips);
     };
     if (e.few_rows() == 1) return with_rows(IntC<1>{});
     if (e.few_rows() == 2) return with_rows(IntC<2>{});
@@ -206,8 +208,10 @@ bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
     const Estimate e(w, RAGGED_C);
     constexpr double kNever = 1e30;
     const bool chunks = least >= static_cast<int>(16 / sizeof(T));  // a row has 16 bytes
-    const double square = e.square();
-    double wide = kNever, few = kNever, split = kNever;
+    double square = e.square(), wide = kNever, few = kNever, split = kNever;
+    const auto force = [](double &time, int kernel) {
+        if (g_product_kernel == kernel && time != kNever) time = 0;
+    };
     if constexpr (sizeof(T) <= 2) {
         // (Below a stage of rows, what counts for the weights' gradient is that it is written from many CUs.)
         if (jobs_of(rs::kWide) <= kMostTiles && feeds(w.q, w.q_stride, 0, Q_ACROSS ? w.qn : w.cn, Q_ACROSS, sizeof(T)) &&
@@ -218,36 +222,38 @@ bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
         // (In float32 a CU's matrix units are busy with one tile of 64 x 64.)
         if (chunks && jobs_of(rs::kSplitSide) <= kMostTiles) split = e.split();
     }
+    force(square, RS_PRODUCT_SQUARE), force(wide, RS_PRODUCT_WIDE), force(split, RS_PRODUCT_SPLIT);
     if constexpr (!RAGGED_C && !P_ACROSS) {
         // (A strip and up to 1024 threads, or where strips are many two and 256.)
         const size_t strips = parts(static_cast<size_t>(w.pn), 16) *
             (w.num_rows / 16 + std::min<size_t>(w.num_rows, static_cast<size_t>(w.experts)) + 1);
         if (chunks && w.num_rows <= 65536 && strips <= 4 * kMostTiles) few = e.few();
+        force(few, RS_PRODUCT_FEW);
         if (few <= std::min({wide, square, split})) return launch_few(w, e, stream);
     }
-    const auto launch = [&](auto kernel, size_t grid, int threads, const auto &work) {
+    const auto launch = [&](auto kernel, int which, size_t grid, int threads, const auto &work) {
         return launch_kernel(RS_KERNEL_PRODUCT, stream,
-                             [&] { run_kernel(kernel, static_cast<unsigned>(grid), threads, stream, work); });
+                             [&] { run_kernel(kernel, static_cast<unsigned>(grid), threads, stream, work); }, which);
     };
     if constexpr (sizeof(T) <= 2) {
         if (wide <= std::min(square, split)) {
             if constexpr (sizeof(T) == 1) {
-                return launch(rs::wide_fp8_kernel<OUT>, jobs_of(rs::kWide), rs::kWideThreads, w);
+                return launch(rs::wide_fp8_kernel<OUT>, RS_PRODUCT_WIDE, jobs_of(rs::kWide), rs::kWideThreads, w);
             } else {
-                return launch(rs::wide_product_kernel<T, RAGGED_C, Q_ACROSS, P_ACROSS>, jobs_of(rs::kWide),
-                              rs::kWideThreads, w);
+                return launch(rs::wide_product_kernel<T, RAGGED_C, Q_ACROSS, P_ACROSS>, RS_PRODUCT_WIDE,
+                              jobs_of(rs::kWide), rs::kWideThreads, w);
             }
         }
         if (split < square) {
-            return launch(rs::split_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS>, jobs_of(rs::kSplitSide),
-                          64 * rs::kSplitWaves, w);
+            return launch(rs::split_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS>, RS_PRODUCT_SPLIT,
+                          jobs_of(rs::kSplitSide), 64 * rs::kSplitWaves, w);
         }
     }
     const size_t jobs = jobs_of(rs::kSquare<T>);
     if (jobs > size_t{1} << 31) return false;  // (whose results no memory holds)
     rs::ProductWork<T, OUT> work = w;
     work.jobs = static_cast<unsigned>(jobs);
-    const auto go = [&](auto kernel) { return launch(kernel, std::min(jobs, kMostTiles), 256, work); };
+    const auto go = [&](auto kernel) { return launch(kernel, RS_PRODUCT_SQUARE, std::min(jobs, kMostTiles), 256, work); };
     if (!chunks) return go(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS, 1, true>);
     // (Rows that take less than two steps are not worth the registers of a second.)
     if (sizeof(T) < 4 && (!aligned_rows(w) || (RAGGED_C && w.num_rows < 128 * static_cast<size_t>(w.experts)))) {
@@ -367,6 +373,12 @@ rs_status quantize_rows(const void *rows, int dtype, size_t num_rows, int width,
 }  // namespace
 
 extern "C" {
+
+int rs_prof_product_kernel(int kernel) {
+    const int prev = g_product_kernel;
+    g_product_kernel = kernel >= RS_PRODUCT_SQUARE && kernel <= RS_PRODUCT_WIDE ? kernel : 0;
+    return prev;
+}
 
 rs_status rs_expert_products(const void *rows, int dtype, size_t num_rows, int in_width, size_t rows_stride,
                              const int32_t *offsets, int experts, const void *weights, int out_width,
