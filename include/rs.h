@@ -445,10 +445,11 @@ rs_status rs_expert_products_backward(const void *grad, int dtype, size_t num_ro
  *   out[r][n] = sum over b < B of row_scales[b][r] * weight_scales[e][n / RS_SCALE_BLOCK][b]
  *               * sum over k of block b of rows[r][k] * weights[e][n][k],
  * out in dtype.  row_scales [B][num_rows] and weight_scales
- * [experts][ceil(out_width / RS_SCALE_BLOCK)][B] are contiguous.  The products of a
- * block are added by the matrix instruction, which keeps of each what stands at
+ * [experts][ceil(out_width / RS_SCALE_BLOCK)][B] are contiguous.  For results in
+ * float32 and float16 the products are added in float32.  For bfloat16 those of a
+ * block are added by the 8-bit matrix instruction, which keeps of each what stands at
  * most 18 binary digits below the largest of them: a block's sum is off by up to
- * 2^-11 of its largest product, a few 10^-4 of the result, whatever dtype is. */
+ * 2^-11 of its largest product, a quarter of what rounding to bfloat16 may take. */
 #define RS_SCALE_BLOCK 128
 rs_status rs_expert_products_fp8(const uint8_t *rows, const float *row_scales, size_t num_rows, int in_width,
                                  size_t rows_stride, const int32_t *offsets, int experts, const uint8_t *weights,

@@ -19,9 +19,6 @@
 RS_WIDE(rs::f16)
 RS_WIDE(rs::bf16)
 #undef RS_WIDE
-template __global__ void rs::wide_fp8_kernel<float>(const rs::ProductWork<rs::fp8, float>);
-template __global__ void rs::wide_fp8_kernel<rs::f16>(const rs::ProductWork<rs::fp8, rs::f16>);
-template __global__ void rs::wide_fp8_kernel<rs::bf16>(const rs::ProductWork<rs::fp8, rs::bf16>);
 
 namespace {
 
@@ -97,14 +94,17 @@ bool aligned_rows(const rs::ProductWork<T, OUT> &w) {
 // 128 bytes of c, 1.25 if rows do not begin at 16 bytes, and 1.5 if two share
 // every CU, in 8 bits 1.4 and 2.6; of 64 x 64 in float32 1, and 0.52 of a CU's time.  Tiles whose
 // contraction is split take 1.4 us for eight times 128 bytes on half of the CUs and 1.75 on all, in 8 bits
-// 2.2, 2.6 and, if they are many, 3.3, where rows do not begin at 16 bytes 1.9 and 3.
+// 2.2, 2.6 and, if they are many, 3.3, where rows do not begin at 16 bytes 1.9 and 3.  Whole sums of
+// 8-bit operands take 1.1 to 1.4 times as long, in few rows 1.5 us a round more.
 // Measured, in us, wide / few rows / square / split (bfloat16, rows x experts x out x in):
 // 8 of 64 x 2048 x 2048 24 / 12 / 32 / -, 512 of 64 x 4096 x 4096 346 / 424 / - / -, 16 of one x
 // 8192 x 8192 75 / 28 / 107 / -, 128 of one 95 / 88 / 101 / 33, 256 of one 154 / 172 / 102 / 62,
 // 300 of 16 x 2048 x 2048 27 / 33 / 33 / 24, 512 of 8 x 1024 x 1024 16 / 10 / 18 / 8, 2048 of 8 26 / 26 / 15 / -,
 // 1000 of 7 x 1001 x 1537 - / 79 / 34 / 27, 40 of 7 - / 18 / 34 / 15, 5003 of 7 - / - / 41 / 78,
 // 64 of one x 1024 x 8192 - / 38 / - / 28, 256 of one x 4096 x 4096 - / - / 46 / 20;
-// e4m3 256 of 128 x 2048 x 4096 166 / 143 / 310 / -, 128 of one x 4096 x 8192 - / 28 / - / 24,
+// e4m3 256 of 128 x 2048 x 4096 166 / 143 / 310 / -, 128 of one x 4096 x 8192 - / 28 / - / 24, with
+// whole sums 256 of 128 - / 177 / 350 / 215, 128 of one - / 34 / 138 / 24, 4000 of 8 x 1024 x 2048 - / 84 / 48 / 44,
+// 25412 of 89 x 321 x 640 - / 97 / 35 / 71, 512 of one x 7168 x 4096 - / 117 / 73 / 52, e4m3
 // 2042 of 4 x 896 x 2176 - / - / 27 / 18, 4000 of 8 x 1024 x 2048 36 / - / 28 / -, 25412 of 89 x 321 x 640 34 / - / 30 / -; rows' gradient,
 // 128 of one x 4096 x 4096 52 / - / - / 19; weights' gradient, 8192 of one x 1024 x 1024 172 / - / - / 34, 9076 of
 // 2 x 128 x 512 - / - / 58 / 18, 4096 of 8 x 1024 x 1024 20 / - / 18 / 41, 16384 of 64 x 1024 x 2048 128 / - / 167 / -.
@@ -114,12 +114,13 @@ constexpr double kTwoStrips = 512;  // workgroups of few_rows_kernel, of one str
 struct Estimate {
     double rows_each, experts_used, weight_bytes, stages, pn;
     bool bytes, words;  // operands of 8, of 32 bits
+    bool whole;         // of 8 bits, with whole sums
     bool apart;         // rows that do not begin at 16 bytes
     bool ragged_c;
 
     template <class T, class OUT>
     Estimate(const rs::ProductWork<T, OUT> &w, bool of_weights)
-        : pn(w.pn), bytes(sizeof(T) == 1), words(sizeof(T) == 4), apart(!aligned_rows(w)), ragged_c(of_weights) {
+        : pn(w.pn), bytes(sizeof(T) == 1), words(sizeof(T) == 4), whole(bytes && rs::kWhole8<OUT>), apart(!aligned_rows(w)), ragged_c(of_weights) {
         const double n = static_cast<double>(w.num_rows), e = static_cast<double>(w.experts);
         if (ragged_c) {
             experts_used = e, rows_each = w.qn;
@@ -143,25 +144,27 @@ struct Estimate {
     }
     int few_rows() const { return rows_each <= 12 ? 1 : rows_each <= 28 ? 2 : 4; }  // 16 of them each
     double few() const {
-        const double weights = weight_bytes / (bytes ? 6e6 : 5.2e6);
+        const double weights = weight_bytes / (whole ? 5.2e6 : bytes ? 6e6 : 5.2e6);
         const int height = 16 * few_rows();
         const double groups = tiles(height, 16) >= kTwoStrips ? tiles(height, 32) : tiles(height, 16);
         const double taken = (std::min(rows_each, 1.0 * height) + height) / 2;  // (loads of rows that do not exist count half)
-        double rows = std::ceil(groups / 256) * taken * stages * 128 / (apart ? 4.3e3 : 25.4e3);
+        const double rounds = std::ceil(groups / 256);
+        double rows = rounds * taken * stages * 128 / (apart ? 4.3e3 : 25.4e3);
+        if (whole) rows = 1.3 * rows + 1.5 * (rounds - 1);
         if (words) rows = std::max(rows, experts_used * rows_each * stages * std::ceil(pn / 32) * 2.0 * 32 * 32 / 75e6);
         return 4 + std::max(weights, rows) + 0.25 * std::min(weights, rows);
     }
     double square() const {
         const double t = words ? tiles(64, 64) : tiles(128, 128);
-        const double alone = bytes ? 1.4 : apart ? 1.25 : 0.85, two = bytes ? 2.6 : 1.5;
+        const double alone = whole ? 1.9 : bytes ? 1.4 : apart ? 1.25 : 0.85, two = whole ? 3.6 : bytes ? 2.6 : 1.5;
         const double step = words ? std::max(1.0, 0.52 * t / 256) : t <= 256 ? alone : two * std::ceil(t / 512);
         const double ends = ragged_c && t > 256 ? 3.5 * std::ceil(t / 512) : 0;
         return 4 + std::max(stages * step + ends, weight_bytes / 3.5e6);
     }
     double split() const {
         const double t = tiles(rs::kSplitSide, rs::kSplitSide);
-        const double some = apart ? 1.9 : bytes ? 2.2 : 1.4, all = apart ? 3.0 : bytes ? 2.6 : 1.75;
-        const double step = t <= 128 ? some : bytes && t > 512 ? 3.3 : all;
+        const double some = whole ? 2.6 : apart ? 1.9 : bytes ? 2.2 : 1.4, all = apart ? 3.0 : whole ? 2.9 : bytes ? 2.6 : 1.75;
+        const double step = t <= 128 ? some : bytes && t > 512 ? (whole ? 3.6 : 3.3) : all;
         return 4 + std::max(std::ceil(t / 256) * (std::ceil(stages / rs::kSplitWaves) * step + 2), weight_bytes / 3.5e6);
     }
 };
@@ -216,7 +219,7 @@ bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
         // (Below a stage of rows, what counts for the weights' gradient is that it is written from many CUs.)
         if (jobs_of(rs::kWide) <= kMostTiles && feeds(w.q, w.q_stride, 0, Q_ACROSS ? w.qn : w.cn, Q_ACROSS, sizeof(T)) &&
             feeds(w.p, w.p_stride, w.p_expert, P_ACROSS ? w.pn : w.cn, P_ACROSS, sizeof(T)) &&
-            (!RAGGED_C || w.num_rows >= 64 * static_cast<size_t>(w.experts))) {
+            (!RAGGED_C || w.num_rows >= 64 * static_cast<size_t>(w.experts)) && !(sizeof(T) == 1 && rs::kWhole8<OUT>)) {
             wide = e.wide();
         }
         // (In float32 a CU's matrix units are busy with one tile of 64 x 64.)
@@ -237,8 +240,10 @@ bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
     };
     if constexpr (sizeof(T) <= 2) {
         if (wide <= std::min(square, split)) {
-            if constexpr (sizeof(T) == 1) {
-                return launch(rs::wide_fp8_kernel<OUT>, RS_PRODUCT_WIDE, jobs_of(rs::kWide), rs::kWideThreads, w);
+            if constexpr (sizeof(T) == 1 && rs::kWhole8<OUT>) {
+                return false;  // (not estimated)
+            } else if constexpr (sizeof(T) == 1) {
+                return launch(rs::wide_fp8_kernel, RS_PRODUCT_WIDE, jobs_of(rs::kWide), rs::kWideThreads, w);
             } else {
                 return launch(rs::wide_product_kernel<T, RAGGED_C, Q_ACROSS, P_ACROSS>, RS_PRODUCT_WIDE,
                               jobs_of(rs::kWide), rs::kWideThreads, w);
@@ -255,11 +260,14 @@ bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
     work.jobs = static_cast<unsigned>(jobs);
     const auto go = [&](auto kernel) { return launch(kernel, RS_PRODUCT_SQUARE, std::min(jobs, kMostTiles), 256, work); };
     if (!chunks) return go(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS, 1, true>);
-    // (Rows that take less than two steps are not worth the registers of a second.)
-    if (sizeof(T) < 4 && (!aligned_rows(w) || (RAGGED_C && w.num_rows < 128 * static_cast<size_t>(w.experts)))) {
+    // (Rows that take less than two steps are not worth the registers of a second, and beside
+    // whole sums of 8-bit operands there are none: 4730 us where one step ahead takes 2530.)
+    constexpr bool kOne = sizeof(T) == 1 && rs::kWhole8<OUT>;
+    if (sizeof(T) < 4 && (kOne || !aligned_rows(w) || (RAGGED_C && w.num_rows < 128 * static_cast<size_t>(w.experts)))) {
         return go(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS, 1, false>);
     }
-    return go(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS, 2, false>);
+    if constexpr (!kOne) return go(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS, 2, false>);
+    return false;
 }
 
 rs::Divider divider(size_t by) {

@@ -100,7 +100,7 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(const ProductWork<
 #pragma unroll
                 for (int j = 0; j < ROWS; ++j) {
                     if constexpr (kFp8) {
-                        const f32x4 part = mma16_fp8(fp[a][s][0], fp[a][s][1], fq[a][j][0], fq[a][j][1]);
+                        const f32x4 part = mma16_fp8<kWhole8<OUT>>(fp[a][s][0], fp[a][s][1], fq[a][j][0], fq[a][j][1]);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             acc[s][j][r] = __builtin_fmaf(part[r], scale[a][j], acc[s][j][r]);

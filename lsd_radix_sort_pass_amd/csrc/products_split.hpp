@@ -102,7 +102,7 @@ __global__ __launch_bounds__(64 * kSplitWaves) void split_kernel(const ProductWo
                     const i32x4 fq1 = fragment<T, SIDE, false>(q_tile, 16 * j, 1, lane);
 #pragma unroll
                     for (int i = 0; i < kCount; ++i) {
-                        const f32x4 part = mma16_fp8(fp[i][0], fp[i][1], fq0, fq1);
+                        const f32x4 part = mma16_fp8<kWhole8<OUT>>(fp[i][0], fp[i][1], fq0, fq1);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(part[r], scale[j], acc[i][j][r]);
                     }

@@ -494,6 +494,8 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
 // scale.  Results of a block stand for themselves times the scales of row and
 // matrix, and are added to the sums in float32: 16 x 16 of them at a time, while the next
 // are multiplied.  The scales of the rows come with the stage.
+// Results in bfloat16: the others' sums, taken whole, would need 320 conversions a slot here, as
+// there are no registers for p in float16 (32768 rows of 32 x 4096 x 7168 3570 us, 2530 with square tiles).
 // ---------------------------------------------------------------------------
 // Scales of a stage: of the first 64 rows of both groups, then of their others, each
 // with room for what the six waves bring whose loads nobody reads (all waves load as
@@ -550,8 +552,8 @@ __device__ __forceinline__ void read_q8(const Reader8 &r, unsigned base, unsigne
 #endif
 }
 
-template <class OUT>
-__global__ __launch_bounds__(kWideThreads) void wide_fp8_kernel(const ProductWork<fp8, OUT> w) {
+__global__ __launch_bounds__(kWideThreads) void wide_fp8_kernel(const ProductWork<fp8, bf16> w) {
+    using OUT = bf16;
     __shared__ __align__(1024) char ring[kWideLds + 3 * kScaleBytes];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int group = wave >> 2, p_wave = (wave & 3) * 64;
@@ -647,7 +649,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_fp8_kernel(const ProductWor
     const auto block = [&](auto j) __attribute__((always_inline)) {
         constexpr int J = decltype(j)::value;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) part[J & 1][i] = mma16_fp8(op.f[i][0], op.f[i][1], oq.f[J][0], oq.f[J][1]);
+        for (int i = 0; i < 4; ++i) part[J & 1][i] = mma16_fp8<kWhole8<OUT>>(op.f[i][0], op.f[i][1], oq.f[J][0], oq.f[J][1]);
     };
     const auto add = [&](auto half, auto j, float both) __attribute__((always_inline)) {
         constexpr int kHalf = decltype(half)::value, J = decltype(j)::value;
@@ -777,37 +779,21 @@ __global__ __launch_bounds__(kWideThreads) void wide_fp8_kernel(const ProductWor
         flat(k2);
     }
 
-    if constexpr (sizeof(OUT) == 2) {
-        char *mine = ring + wave * 16384;
-        typedef OUT t4 __attribute__((ext_vector_type(4)));
+    char *mine = ring + wave * 16384;
+    typedef OUT t4 __attribute__((ext_vector_type(4)));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int row = 16 * j + (lane & 15);
+    for (int j = 0; j < 8; ++j) {
+        const int row = 16 * j + (lane & 15);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                t4 v;
+        for (int i = 0; i < 4; ++i) {
+            t4 v;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = static_cast<OUT>(acc[i][j][r]);
-                const int chunk = 2 * i + (lane >> 5);
-                *reinterpret_cast<t4 *>(mine + result_at(row, chunk) + (lane >> 4 & 1) * 8) = v;
-            }
-        }
-        rows_from_lds(mine, out, w.out_stride, height, q0 + q_wave, q_rows, p0 + p_wave, w.pn, lane);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int row = 16 * j + (lane & 15), qi = q0 + q_wave + row;
-            if (row >= height || qi >= q_rows) continue;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int pi = p0 + p_wave + 16 * i + 4 * (lane >> 4);
-                float f[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) f[r] = acc[i][j][r];
-                if (pi < w.pn) store_some<OUT, 4>(out + static_cast<size_t>(qi) * w.out_stride + pi, w.pn - pi, f);
-            }
+            for (int r = 0; r < 4; ++r) v[r] = static_cast<OUT>(acc[i][j][r]);
+            const int chunk = 2 * i + (lane >> 5);
+            *reinterpret_cast<t4 *>(mine + result_at(row, chunk) + (lane >> 4 & 1) * 8) = v;
         }
     }
+    rows_from_lds(mine, out, w.out_stride, height, q0 + q_wave, q_rows, p0 + p_wave, w.pn, lane);
 }
 
 }  // namespace rs

@@ -1,9 +1,14 @@
 """GPU tests of what rows and weights become in 8 bits, to the bit, and of the
 accuracy of products of 8-bit operands."""
+import contextlib
+
 import pytest
+
+import product_oracle as po
 
 torch = pytest.importorskip("torch")
 rs = pytest.importorskip("lsd_radix_sort_pass_amd")
+from lsd_radix_sort_pass_amd import _lib  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +90,40 @@ def test_gate_quantize_rows_divide_by_the_scale():
             bits, scale = eight_bits(64.0 * b[:, k:k + 128])
             assert torch.equal(got.scales[k // 128].cpu(), scale)
             assert same(got.values.view(torch.uint8)[:, k:k + 128].cpu(), bits)
+
+
+@contextlib.contextmanager
+def forced(kernel):
+    before = rs.prof_product_kernel(kernel)
+    try:
+        yield
+    finally:
+        rs.prof_product_kernel(before)
+
+
+KERNELS = {"square": _lib.RS_PRODUCT_SQUARE, "few": _lib.RS_PRODUCT_FEW, "split": _lib.RS_PRODUCT_SPLIT}
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float16"])
+@pytest.mark.parametrize("kernel", list(KERNELS))
+@pytest.mark.parametrize("n,N,K", [(40, 33, 128), (70, 130, 400), (3, 5, 9)])
+def test_fp8_sums_in_float32(n, N, K, kernel, dtype):
+    """In each block two large products cancel, and what is left is 2^-10 of them and
+    less: sums in float32 lose 2^-24 of a partial sum a step."""
+    note(f"fp8 sums {kernel} {dtype} n={n} N={N} K={K}")
+    gen = torch.Generator().manual_seed(n + K)
+    x = torch.randint(-15, 16, (n, K), generator=gen).float() * 2.0 ** -6
+    w = torch.randint(-15, 16, (1, N, K), generator=gen).float() * 2.0 ** -6
+    for b in range(0, K, 128):
+        last = min(b + 128, K) - 1
+        x[:, b], x[:, last], w[:, :, b], w[:, :, last] = 8.0, -8.0, 8.0, 8.0
+    x, w = x.cuda().to(FP8), w.cuda().to(FP8)
+    qs = torch.exp2(torch.rand((K + 127) // 128, n, generator=gen)).cuda()
+    ws = torch.exp2(torch.rand(1, (N + 127) // 128, (K + 127) // 128, generator=gen)).cuda()
+    spans = [(0, n)]
+    exact, size = po.product(po.expand(x, qs), spans, po.expand_weights(w, ws), torch.zeros(n, N, device="cuda"))
+    with forced(KERNELS[kernel]):
+        got = rs.expert_products_fp8(x, qs, None, w, ws, DTYPES[dtype]).double()
+    # K products, a product of scales and one with them for each block.
+    bound = po.product_bound(exact, size, K + 2, dtype)
+    assert ((got - exact).abs() <= bound).all(), f"{float(((got - exact).abs() / bound).max())} bounds off"
