@@ -127,3 +127,29 @@ def test_fp8_sums_in_float32(n, N, K, kernel, dtype):
     # K products, a product of scales and one with them for each block.
     bound = po.product_bound(exact, size, K + 2, dtype)
     assert ((got - exact).abs() <= bound).all(), f"{float(((got - exact).abs() / bound).max())} bounds off"
+
+
+# A kernel each, and the wide one, which serves bfloat16 alone; magnitudes of the scales of rows
+# and of matrices, whose products are normal numbers.
+@pytest.mark.parametrize("rows,matrix", [(-100, 80), (-90, 110), (100, -100), (50, 48), (-105, -18), (0, 0)])
+@pytest.mark.parametrize("kernel,dtype", [(k, d) for k in KERNELS for d in ("float32", "bfloat16")] + [("wide", "bfloat16")])
+def test_fp8_scales_of_any_size(kernel, dtype, rows, matrix):
+    """Results in float32's range are right, whatever the scales are; rows and blocks of
+    zeros, whose scales' product may be too small for float32, give zeros."""
+    note(f"fp8 scales {kernel} {dtype} 2^{rows} 2^{matrix}")
+    gen = torch.Generator().manual_seed(rows + 200)
+    n, N, K = 70, 136, 384
+    x, w = torch.randint(-15, 16, (n, K), generator=gen).float(), torch.randint(-15, 16, (1, N, K), generator=gen).float()
+    qs, ws = torch.exp2(rows + torch.rand(3, n, generator=gen)), torch.exp2(matrix + torch.rand(1, 2, 3, generator=gen))
+    least = 2.0 ** -100 / 448
+    x[:, 128:256], qs[1], w[:, 128:], ws[:, 1] = 0, least, 0, least       # as they become in 8 bits
+    x, w, qs, ws = x.cuda().to(FP8), w.cuda().to(FP8), qs.cuda(), ws.cuda()
+    values, matrices, none = po.expand(x, qs), po.expand_weights(w, ws), torch.zeros(n, N, device="cuda")
+    exact, size = po.product(values, [(0, n)], matrices, none)
+    with forced({**KERNELS, "wide": _lib.RS_PRODUCT_WIDE}[kernel]):
+        got = rs.expert_products_fp8(x, qs, None, w, ws, DTYPES[dtype]).double()
+    bound = po.product_bound(exact, size, K + 2, dtype)
+    if dtype == "bfloat16":
+        bound += po.fp8_lost(values, [(0, n)], matrices, none)
+    assert ((got - exact).abs() <= bound).all(), (float(got.abs().max()), float(exact.abs().max()))
+    assert (got[:, 128:] == 0).all()
