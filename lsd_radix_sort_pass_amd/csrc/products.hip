@@ -95,7 +95,7 @@ bool aligned_rows(const rs::ProductWork<T, OUT> &w) {
 // every CU, in 8 bits 1.4 and 2.6; of 64 x 64 in float32 1, and 0.52 of a CU's time.  Tiles whose
 // contraction is split take 1.4 us for eight times 128 bytes on half of the CUs and 1.75 on all, in 8 bits
 // 2.2, 2.6 and, if they are many, 3.3, where rows do not begin at 16 bytes 1.9 and 3.  Whole sums of
-// 8-bit operands take 1.1 to 1.4 times as long, in few rows 1.5 us a round more.
+// 8-bit operands take 1.1 to 1.3 times as long, in few rows 1.5 us a round more.
 // Measured, in us, wide / few rows / square / split (bfloat16, rows x experts x out x in):
 // 8 of 64 x 2048 x 2048 24 / 12 / 32 / -, 512 of 64 x 4096 x 4096 346 / 424 / - / -, 16 of one x
 // 8192 x 8192 75 / 28 / 107 / -, 128 of one 95 / 88 / 101 / 33, 256 of one 154 / 172 / 102 / 62,
@@ -103,8 +103,8 @@ bool aligned_rows(const rs::ProductWork<T, OUT> &w) {
 // 1000 of 7 x 1001 x 1537 - / 79 / 34 / 27, 40 of 7 - / 18 / 34 / 15, 5003 of 7 - / - / 41 / 78,
 // 64 of one x 1024 x 8192 - / 38 / - / 28, 256 of one x 4096 x 4096 - / - / 46 / 20;
 // e4m3 256 of 128 x 2048 x 4096 166 / 143 / 310 / -, 128 of one x 4096 x 8192 - / 28 / - / 24, with
-// whole sums 256 of 128 - / 177 / 350 / 215, 128 of one - / 34 / 138 / 24, 4000 of 8 x 1024 x 2048 - / 84 / 48 / 44,
-// 25412 of 89 x 321 x 640 - / 97 / 35 / 71, 512 of one x 7168 x 4096 - / 117 / 73 / 52, e4m3
+// whole sums 256 of 128 - / 177 / 298 / 217, 128 of one - / 34 / 102 / 24, 4000 of 8 x 1024 x 2048 - / 84 / 41 / 43,
+// 25412 of 89 x 321 x 640 - / 97 / 28 / 71, 512 of one x 7168 x 4096 - / 117 / 55 / 53, e4m3
 // 2042 of 4 x 896 x 2176 - / - / 27 / 18, 4000 of 8 x 1024 x 2048 36 / - / 28 / -, 25412 of 89 x 321 x 640 34 / - / 30 / -; rows' gradient,
 // 128 of one x 4096 x 4096 52 / - / - / 19; weights' gradient, 8192 of one x 1024 x 1024 172 / - / - / 34, 9076 of
 // 2 x 128 x 512 - / - / 58 / 18, 4096 of 8 x 1024 x 1024 20 / - / 18 / 41, 16384 of 64 x 1024 x 2048 128 / - / 167 / -.
@@ -156,7 +156,7 @@ struct Estimate {
     }
     double square() const {
         const double t = words ? tiles(64, 64) : tiles(128, 128);
-        const double alone = whole ? 1.9 : bytes ? 1.4 : apart ? 1.25 : 0.85, two = whole ? 3.6 : bytes ? 2.6 : 1.5;
+        const double alone = whole ? 1.5 : bytes ? 1.4 : apart ? 1.25 : 0.85, two = whole ? 3.0 : bytes ? 2.6 : 1.5;
         const double step = words ? std::max(1.0, 0.52 * t / 256) : t <= 256 ? alone : two * std::ceil(t / 512);
         const double ends = ragged_c && t > 256 ? 3.5 * std::ceil(t / 512) : 0;
         return 4 + std::max(stages * step + ends, weight_bytes / 3.5e6);
@@ -261,7 +261,7 @@ bool launch_product(const rs::ProductWork<T, OUT> &w, hipStream_t stream) {
     const auto go = [&](auto kernel) { return launch(kernel, RS_PRODUCT_SQUARE, std::min(jobs, kMostTiles), 256, work); };
     if (!chunks) return go(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS, 1, true>);
     // (Rows that take less than two steps are not worth the registers of a second, and beside
-    // whole sums of 8-bit operands there are none: 4730 us where one step ahead takes 2530.)
+    // whole sums of 8-bit operands there are none: registers spill: twice the time.)
     constexpr bool kOne = sizeof(T) == 1 && rs::kWhole8<OUT>;
     if (sizeof(T) < 4 && (kOne || !aligned_rows(w) || (RAGGED_C && w.num_rows < 128 * static_cast<size_t>(w.experts)))) {
         return go(rs::product_kernel<T, OUT, RAGGED_C, Q_ACROSS, P_ACROSS, 1, false>);

@@ -495,7 +495,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
 // matrix, and are added to the sums in float32: 16 x 16 of them at a time, while the next
 // are multiplied.  The scales of the rows come with the stage.
 // Results in bfloat16: the others' sums, taken whole, would need 320 conversions a slot here, as
-// there are no registers for p in float16 (32768 rows of 32 x 4096 x 7168 3570 us, 2530 with square tiles).
+// there are no registers for p in float16 (32768 rows of 32 x 4096 x 7168 3570 us, 2130 with square tiles).
 // ---------------------------------------------------------------------------
 // Scales of a stage: of the first 64 rows of both groups, then of their others, each
 // with room for what the six waves bring whose loads nobody reads (all waves load as
