@@ -462,6 +462,16 @@ __device__ __forceinline__ void lds_barrier() {
 #endif
 }
 
+// Orders what lanes of a wave have written to LDS before what others of it read, and what
+// they have read before what is written over it.  The LDS serves a wave's accesses in
+// order: this costs no instruction, and keeps the compiler from moving one lane's access
+// over another's, whose address it can show to differ.
+__device__ __forceinline__ void wave_exchange() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // ---------------------------------------------------------------------------
 // Zeros in `height` rows of no expert (fewer at their end), `columns` of them from col on,
 // by all of the workgroup's threads, 16 bytes a thread.
@@ -683,6 +693,7 @@ __global__ __launch_bounds__(256, kSquare<T> == 64 ? 4 : sizeof(T) == 1 ? 2 : 4 
                     }
                 }
             }
+            wave_exchange();
             rows_from_lds(mine, out, w.out_stride, 64, q0 + q_wave, q_rows, p0 + p_wave, w.pn, lane);
             continue;
         }

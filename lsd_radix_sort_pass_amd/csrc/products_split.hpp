@@ -74,6 +74,7 @@ __global__ __launch_bounds__(64 * kSplitWaves) void split_kernel(const ProductWo
         for (int c = wave * kStep<T>; c < c_n; c += kSpan) {
             sq.store(raw_q, q_tile, c, lane);
             sp.store(raw_p, p_tile, c, lane);
+            wave_exchange();
             [[maybe_unused]] float scale[kCount];
             if constexpr (kFp8) {  // (before the loads that nothing waits for yet)
                 const int block = c / kScaleBlock, blocks = (w.cn + kScaleBlock - 1) / kScaleBlock;
@@ -125,6 +126,7 @@ __global__ __launch_bounds__(64 * kSplitWaves) void split_kernel(const ProductWo
                     }
                 }
             }
+            wave_exchange();
         }
     }
 

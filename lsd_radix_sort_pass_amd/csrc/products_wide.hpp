@@ -486,6 +486,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_product_kernel(const Produc
             }
         }
     }
+    wave_exchange();
     rows_from_lds(mine, out, w.out_stride, height, q0 + q_wave, q_rows, p0 + p_wave, w.pn, lane);
 }
 
@@ -793,6 +794,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_fp8_kernel(const ProductWor
             *reinterpret_cast<t4 *>(mine + result_at(row, chunk) + (lane >> 4 & 1) * 8) = v;
         }
     }
+    wave_exchange();
     rows_from_lds(mine, out, w.out_stride, height, q0 + q_wave, q_rows, p0 + p_wave, w.pn, lane);
 }
 
