@@ -243,11 +243,19 @@ __global__ __launch_bounds__(kGateBlock) void quantize_rows_kernel(const GateWor
         if (!has && !w.clear) continue;
         const T *in = static_cast<const T *>(w.rows) + r * w.rows_stride;
         float f[kBlocks][8], b[kBlocks][8];
+        if (has) {
 #pragma unroll
-        for (int j = 0; j < kBlocks; ++j) {
-            const int c = (first + j) * kScaleBlock + 8 * g;
-            load8<T, ROW>(in, c, w.width, !has, f[j]);
-            if constexpr (GATE) load8<T, ROW>(in + w.width, c, w.width, !has, b[j]);
+            for (int j = 0; j < kBlocks; ++j) {
+                const int c = (first + j) * kScaleBlock + 8 * g;
+                load8<T, ROW>(in, c, w.width, false, f[j]);
+                if constexpr (GATE) load8<T, ROW>(in + w.width, c, w.width, false, b[j]);
+            }
+        } else {  // (is not read)
+#pragma unroll
+            for (int j = 0; j < kBlocks; ++j) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[j][i] = b[j][i] = 0.0f;
+            }
         }
 #pragma unroll
         for (int j = 0; j < kBlocks; ++j) {
