@@ -233,7 +233,7 @@ def expert_products_fp8(rows: torch.Tensor, row_scales: torch.Tensor, offsets: O
     elif dtype not in _ROW_DTYPES:
         raise TypeError(f"dtype must be one of float32, float16, bfloat16 (got {dtype})")
     if _forward._current_level >= 0:
-        _refuse_tangents(row_scales=row_scales, weight_scales=weight_scales, out=out)
+        _refuse_tangents(rows=rows, row_scales=row_scales, weights=weights, weight_scales=weight_scales, out=out)
     if stream is not None or device.index != _current():
         with _on(device, stream, rows, row_scales, offsets, weights, weight_scales, out):
             return expert_products_fp8(rows, row_scales, offsets, weights, weight_scales, dtype, out)
@@ -264,7 +264,7 @@ def _to_8_bits(name, rows, offsets, act, out, scales_out, stream):
     if (out is None) != (scales_out is None):
         raise ValueError("out and scales_out are given together")
     if _forward._current_level >= 0:
-        _refuse_tangents(rows=rows, scales_out=scales_out)
+        _refuse_tangents(rows=rows, out=out, scales_out=scales_out)
     if stream is not None or device.index != _current():
         with _on(device, stream, rows, offsets, out, scales_out):
             return _to_8_bits(name, rows, offsets, act, out, scales_out, None)

@@ -153,3 +153,23 @@ def test_fp8_scales_of_any_size(kernel, dtype, rows, matrix):
         bound += po.fp8_lost(values, [(0, n)], matrices, none)
     assert ((got - exact).abs() <= bound).all(), (float(got.abs().max()), float(exact.abs().max()))
     assert (got[:, 128:] == 0).all()
+
+
+def test_tangents_are_refused():
+    """Of every tensor, the 8-bit ones too, which may carry them."""
+    note("tangents in 8 bits")
+    import torch.autograd.forward_ad as fwd
+    x, w = torch.randn(6, 32, device="cuda"), torch.randn(1, 16, 32, device="cuda")
+    (q, s), (w8, ws) = rs.quantize_rows(x), rs.quantize_weights(w)
+    out = torch.empty(6, 16, device="cuda")
+    operands = {"rows": q, "row_scales": s, "weights": w8, "weight_scales": ws, "out": out}
+    results = {"rows": x, "out": torch.empty_like(q), "scales_out": torch.empty_like(s)}
+    gated = {"rows": torch.randn(6, 64, device="cuda"), "out": torch.empty_like(q), "scales_out": torch.empty_like(s)}
+    for call, given in ((lambda **t: rs.expert_products_fp8(offsets=None, **t), operands), (rs.quantize_rows, results),
+                        (rs.gate_quantize_rows, gated), (rs.quantize_weights, {"weights": w})):
+        with fwd.dual_level():
+            call(**given)
+            for name, t in given.items():
+                dual = fwd.make_dual(t, torch.zeros(t.shape, device="cuda").to(t.dtype))
+                with pytest.raises(ValueError, match=f"^{name} carries a tangent"):
+                    call(**{**given, name: dual})
