@@ -477,7 +477,8 @@ rs_status rs_quantize_weights(const void *weights, int dtype, int experts, int o
  * give, or NaN.  The gradient is that of the whole row, from grad [num_rows][width]:
  * da = grad * b * act'(a), then db = grad * act(a).  rs_gate_quantize_rows gives
  * the gated rows as rs_quantize_rows does, from their values before they are
- * rounded to dtype. */
+ * rounded to dtype; of 16-bit rows act is off by up to 2^-17 of itself (2^-19 where |a| is
+ * below 4), and so may the scales be. */
 typedef enum rs_act { RS_ACT_SILU = 0, RS_ACT_GELU = 1 } rs_act;
 rs_status rs_gate_rows(const void *rows, int dtype, size_t num_rows, int width, size_t rows_stride,
                        const int32_t *offsets, int experts, int act, void *out, size_t out_stride, int all,
