@@ -173,3 +173,29 @@ def test_tangents_are_refused():
                 dual = fwd.make_dual(t, torch.zeros(t.shape, device="cuda").to(t.dtype))
                 with pytest.raises(ValueError, match=f"^{name} carries a tangent"):
                     call(**{**given, name: dual})
+
+
+@pytest.mark.parametrize("kernel,dtype", [(k, d) for k in KERNELS for d in DTYPES] + [("wide", "bfloat16")])
+def test_fp8_every_value(kernel, dtype):
+    """Every e4m3 as a row's and as a matrix's element, times 1; a NaN of either sign makes
+    NaN of its row or column alone.  (The wide kernel serves bfloat16 alone.)"""
+    note(f"fp8 every value {kernel} {dtype}")
+    bits = torch.arange(256, dtype=torch.uint8)
+    finite = bits[(bits & 0x7F) != 0x7F].cuda().view(FP8)                # 254
+    one = torch.eye(254, device="cuda").to(FP8)
+    values = torch.zeros(254, 254, device="cuda").to(FP8)
+    values[:] = finite
+    qs, ws = torch.ones(2, 254, device="cuda"), torch.ones(1, 2, 2, device="cuda")
+    pad = torch.zeros(254, 2, device="cuda").to(FP8)                     # (rows of whole 16 bytes)
+    one, values = torch.cat([one, pad], 1), torch.cat([values, pad], 1)
+    with forced({**KERNELS, "wide": _lib.RS_PRODUCT_WIDE}[kernel]):
+        rows = rs.expert_products_fp8(values, qs, None, one[None], ws, DTYPES[dtype])
+        matrix = rs.expert_products_fp8(one, qs, None, values[None], ws, DTYPES[dtype])
+        assert torch.equal(rows.float(), finite.float().expand(254, 254))
+        assert torch.equal(matrix.float(), finite.float()[:, None].expand(254, 254))
+        x, w = values.clone(), one.clone()
+        x.view(torch.uint8)[7, 200], w.view(torch.uint8)[250, 3] = 0x7F, 0xFF
+        got = rs.expert_products_fp8(x, qs, None, w[None], ws, DTYPES[dtype])
+    nan = torch.zeros(254, 254, dtype=torch.bool, device="cuda")
+    nan[7], nan[:, 250] = True, True
+    assert torch.equal(got.isnan(), nan) and torch.equal(got[~nan], rows[~nan])
