@@ -96,18 +96,20 @@ bool aligned_rows(const rs::ProductWork<T, OUT> &w) {
 // contraction is split take 1.4 us for eight times 128 bytes on half of the CUs and 1.75 on all, in 8 bits
 // 2.2, 2.6 and, if they are many, 3.3, where rows do not begin at 16 bytes 1.9 and 3.  Whole sums of
 // 8-bit operands take 1.1 to 1.3 times as long, in few rows 1.5 us a round more.
+// Rows of no expert, which only the offsets on the device tell, count as if they had one.
 // Measured, in us, wide / few rows / square / split (bfloat16, rows x experts x out x in):
-// 8 of 64 x 2048 x 2048 24 / 12 / 32 / -, 512 of 64 x 4096 x 4096 346 / 424 / - / -, 16 of one x
-// 8192 x 8192 75 / 28 / 107 / -, 128 of one 95 / 88 / 101 / 33, 256 of one 154 / 172 / 102 / 62,
-// 300 of 16 x 2048 x 2048 27 / 33 / 33 / 24, 512 of 8 x 1024 x 1024 16 / 10 / 18 / 8, 2048 of 8 26 / 26 / 15 / -,
-// 1000 of 7 x 1001 x 1537 - / 79 / 34 / 27, 40 of 7 - / 18 / 34 / 15, 5003 of 7 - / - / 41 / 78,
-// 64 of one x 1024 x 8192 - / 38 / - / 28, 256 of one x 4096 x 4096 - / - / 46 / 20;
-// e4m3 256 of 128 x 2048 x 4096 166 / 143 / 310 / -, 128 of one x 4096 x 8192 - / 28 / - / 24, with
-// whole sums 256 of 128 - / 177 / 298 / 217, 128 of one - / 34 / 102 / 24, 4000 of 8 x 1024 x 2048 - / 84 / 41 / 43,
-// 25412 of 89 x 321 x 640 - / 97 / 28 / 71, 512 of one x 7168 x 4096 - / 117 / 55 / 53, e4m3
-// 2042 of 4 x 896 x 2176 - / - / 27 / 18, 4000 of 8 x 1024 x 2048 36 / - / 28 / -, 25412 of 89 x 321 x 640 34 / - / 30 / -; rows' gradient,
-// 128 of one x 4096 x 4096 52 / - / - / 19; weights' gradient, 8192 of one x 1024 x 1024 172 / - / - / 34, 9076 of
-// 2 x 128 x 512 - / - / 58 / 18, 4096 of 8 x 1024 x 1024 20 / - / 18 / 41, 16384 of 64 x 1024 x 2048 128 / - / 167 / -.
+// 8 of 64 x 2048 x 2048 23 / 12 / 27 / 14, 512 of 64 x 4096 x 4096 369 / 400 / 384 / 374, 16 of one x
+// 8192 x 8192 77 / 28 / 92 / 30, 128 of one 94 / 88 / 93 / 34, 256 of one 155 / 174 / 94 / 63,
+// 300 of 16 x 2048 x 2048 23 / 27 / 29 / 27, 512 of 8 x 1024 x 1024 15 / 9 / 14 / 8, 2048 of 8 25 / 25 / 15 / 16,
+// 1000 of 7 x 1001 x 1537 - / 77 / 33 / 26, 40 of 7 - / 17 / 32 / 14, 5003 of 7 - / 302 / 45 / 80,
+// 64 of one x 1024 x 8192 84 / 37 / 81 / 28, 256 of one x 4096 x 4096 82 / 47 / 50 / 20, 1024 of one 83 / 169 / 56 / 70;
+// rows' gradient, 128 of one x 4096 x 4096 49 / - / 51 / 18; weights' gradient, 8192 of one x 1024 x 1024
+// 169 / - / 96 / 32, 9076 of 2 x 128 x 512 55 / - / 56 / 17, 4096 of 8 x 1024 x 1024 19 / - / 17 / 39, 16384 of
+// 64 x 1024 x 2048 125 / - / 163 / 476; e4m3, and with whole sums, 256 of 128 x 2048 x 4096 181 / 171 / 283 / 272, - / 212 / 341 / 285,
+// 128 of one x 4096 x 8192 66 / 27 / 98 / 19, - / 33 / 100 / 24, 4000 of 8 x 1024 x 2048 35 / 68 / 27 / 32, - / 78 / 28 / 38,
+// 25412 of 89 x 321 x 640 34 / - / 30 / 65, - / - / 32 / 70, 512 of one x 7168 x 4096 63 / 101 / 54 / 46, - / 115 / 54 / 54.
+// The choice is off where two are close, and by more for some decoding batches: 16 of 64 x 2048 x 2088 go to
+// the wide kernel, 29 / 21 / 32 / 25.
 // ---------------------------------------------------------------------------
 constexpr double kTwoStrips = 512;  // workgroups of few_rows_kernel, of one strip, from which on they take two
 
