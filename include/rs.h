@@ -446,9 +446,9 @@ rs_status rs_expert_products_backward(const void *grad, int dtype, size_t num_ro
  *               * sum over k of block b of rows[r][k] * weights[e][n][k],
  * out in dtype.  row_scales [B][num_rows] and weight_scales
  * [experts][ceil(out_width / RS_SCALE_BLOCK)][B] are contiguous; the product of two
- * that meet, taken in float32, has to be a normal number, but for blocks whose
- * elements are zeros, where it may also be 0.  For results in
- * float32 and float16 the products are added in float32.  For bfloat16 those of a
+ * that meet, taken in float32, has to be a normal number, or below that where a block's
+ * elements are zeros.  For results in float32 and float16 the products are added in
+ * float32.  For bfloat16 those of a
  * block are added by the 8-bit matrix instruction, which keeps of each what stands at
  * most 18 binary digits below the largest of them: a block's sum is off by up to
  * 2^-11 of its largest product, a quarter of what rounding to bfloat16 may take. */

@@ -122,7 +122,8 @@ struct Estimate {
 
     template <class T, class OUT>
     Estimate(const rs::ProductWork<T, OUT> &w, bool of_weights)
-        : pn(w.pn), bytes(sizeof(T) == 1), words(sizeof(T) == 4), whole(bytes && rs::kWhole8<OUT>), apart(!aligned_rows(w)), ragged_c(of_weights) {
+        : pn(w.pn), bytes(sizeof(T) == 1), words(sizeof(T) == 4), whole(bytes && rs::kWhole8<OUT>),
+          apart(!aligned_rows(w)), ragged_c(of_weights) {
         const double n = static_cast<double>(w.num_rows), e = static_cast<double>(w.experts);
         if (ragged_c) {
             experts_used = e, rows_each = w.qn;
@@ -165,7 +166,8 @@ struct Estimate {
     }
     double split() const {
         const double t = tiles(rs::kSplitSide, rs::kSplitSide);
-        const double some = whole ? 2.6 : apart ? 1.9 : bytes ? 2.2 : 1.4, all = apart ? 3.0 : whole ? 2.9 : bytes ? 2.6 : 1.75;
+        const double some = whole ? 2.6 : apart ? 1.9 : bytes ? 2.2 : 1.4;
+        const double all = apart ? 3.0 : whole ? 2.9 : bytes ? 2.6 : 1.75;
         const double step = t <= 128 ? some : bytes && t > 512 ? (whole ? 3.6 : 3.3) : all;
         return 4 + std::max(std::ceil(t / 256) * (std::ceil(stages / rs::kSplitWaves) * step + 2), weight_bytes / 3.5e6);
     }

@@ -214,7 +214,7 @@ def expert_products_fp8(rows: torch.Tensor, row_scales: torch.Tensor, offsets: O
 
     rows (n, K) and weights (E, N, K) float8_e4m3fn; row_scales (ceil(K / 128), n)
     and weight_scales (E, ceil(N / 128), ceil(K / 128)) float32, the product of two
-    that meet a normal number (or 0, where the elements are zeros); out (n, N) in
+    that meet a normal number (or less, where elements are zeros); out (n, N) in
     dtype (or that of a given `out`), summed in float32, for bfloat16 with the
     products of each 128 cut 2^-18 below the largest of them."""
     _rows(rows, "rows", None, _FP8_DTYPES)
